@@ -21,6 +21,7 @@
 
 #include "qmv_device.h"
 #include "qmv_internal.h"
+#include "step_internal.h"
 
 namespace qmv {
 namespace {
@@ -187,6 +188,47 @@ void quantize_q8_tiles_kernel(const float* __restrict__ x, int8_t* __restrict__ 
         }
         reinterpret_cast<uint4*>(q)[it * kWave + lane] = make_uint4(packed[0], packed[1], packed[2], packed[3]);
         if (h == 0) ds[it * 32 + i] = bf16_split3(db);
+    }
+}
+
+// Row-major codes [M][K] and scales [M][K/32] brought into the layout of an
+// MFMA tiling: what the two kernels above write, from codes that exist
+// already (qmm_q4_0_q8).  kLayoutFrag: one thread per 4 codes, as in
+// quantize_q8_kernel.  Rows M .. Mrows - 1 become zeros.
+__global__ __launch_bounds__(kBlockThreads)
+void layout_q8_frag_kernel(const int8_t* __restrict__ qin, const float* __restrict__ din, int8_t* __restrict__ q,
+                           float* __restrict__ d, int64_t K, int64_t M, int64_t Mrows) {
+    const int64_t nb = K / 32;
+    const int64_t items = Mrows * nb * 8;  // dwords of codes
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kBlockThreads;
+    const FragLayout L{nb};
+    for (int64_t it = static_cast<int64_t>(blockIdx.x) * kBlockThreads + threadIdx.x; it < items; it += stride) {
+        const int64_t blk = it >> 3;
+        const int t = static_cast<int>(it & 7);
+        const int64_t m = blk / nb, b = blk - m * nb;
+        const bool ok = m < M;
+        reinterpret_cast<uint32_t*>(q)[L.code_dword(m, b, t)] = ok ? reinterpret_cast<const uint32_t*>(qin)[it] : 0u;
+        if (t == 0) d[L.scale_index(m, b)] = ok ? din[blk] : 0.0f;
+    }
+}
+
+// kLayoutSplit: one wave per (32-row tile, block), 16 codes a lane.
+__global__ __launch_bounds__(kBlockThreads)
+void layout_q8_tiles_kernel(const int8_t* __restrict__ qin, const float* __restrict__ din, int8_t* __restrict__ q,
+                            uint4* __restrict__ ds, int64_t K, int64_t M, int64_t Mrows) {
+    const int64_t nb = K / 32;
+    const int64_t items = (Mrows / 32) * nb;
+    const int lane = threadIdx.x & (kWave - 1);
+    const int i = lane & 31, h = lane >> 5;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWavesPerBlock;
+    for (int64_t it = static_cast<int64_t>(blockIdx.x) * kWavesPerBlock + threadIdx.x / kWave; it < items;
+         it += stride) {
+        const int64_t mt = it / nb, b = it - mt * nb;
+        const int64_t m = mt * 32 + i;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (m < M) v = *reinterpret_cast<const uint4*>(qin + m * K + 32 * b + 16 * h);
+        reinterpret_cast<uint4*>(q)[it * kWave + lane] = v;
+        if (h == 0) ds[it * 32 + i] = bf16_split3(m < M ? din[m * nb + b] : 0.0f);
     }
 }
 
@@ -1476,17 +1518,11 @@ hipError_t launch_quantize_q8(const float* x, int8_t* q, float* d, int64_t K, in
     return launch_quantize<kLayoutRows>(x, q, d, K, M, M, stream);
 }
 
-hipError_t launch_qmm_q8act(const void* W, const float* x, float* y, int32_t* isum, int64_t isn0, int64_t isn1,
-                            int64_t N, int64_t K, int64_t M, void* ws, hipStream_t stream) {
-    const QmmPlan p = plan_qmm(N, K, M);
-    int8_t* q = static_cast<int8_t*>(ws);
-    float* d = reinterpret_cast<float*>(static_cast<char*>(ws) + p.q_bytes);
-    float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.q_bytes + p.d_bytes);
+// Step 2 on activations in the layout of the plan's path.
+static hipError_t launch_step2(const QmmPlan& p, const void* W, const int8_t* q, const float* d, float* part, float* y,
+                               int32_t* isum, int64_t isn0, int64_t isn1, int64_t N, int64_t K, int64_t M,
+                               hipStream_t stream) {
     const bool mfma = p.path == kPathWide || p.path == kPathNarrow;
-    hipError_t e = p.path == kPathWide     ? launch_quantize<kLayoutSplit>(x, q, d, K, M, p.xrows, stream)
-                   : p.path == kPathNarrow ? launch_quantize<kLayoutFrag>(x, q, d, K, M, p.xrows, stream)
-                                           : launch_quantize<kLayoutRows>(x, q, d, K, M, M, stream);
-    if (e != hipSuccess) return e;
     if (!mfma) return launch_dot(p, W, q, d, isum ? nullptr : y, isum, isn0, isn1, N, K, M, stream);
     if (p.path == kPathWide) {
         return isum ? launch_wide<kModeISum>(p, W, q, d, nullptr, part, isum, isn0, isn1, N, K, M, stream)
@@ -1495,7 +1531,7 @@ hipError_t launch_qmm_q8act(const void* W, const float* x, float* y, int32_t* is
     // the narrow tiling: the block-sum mode runs the same grid, K splits included
     if (isum) return launch_mfma<QMM_NARROW, kModeISum>(p, W, q, d, nullptr, isum, isn0, isn1, N, K, M, stream);
     if (p.ks == 1) return launch_mfma<QMM_NARROW, kModeY>(p, W, q, d, y, nullptr, 0, 0, N, K, M, stream);
-    e = launch_mfma<QMM_NARROW, kModePartial>(p, W, q, d, part, nullptr, 0, 0, N, K, M, stream);
+    const hipError_t e = launch_mfma<QMM_NARROW, kModePartial>(p, W, q, d, part, nullptr, 0, 0, N, K, M, stream);
     if (e != hipSuccess) return e;
     const int64_t MN = M * N;
     int64_t blocks = ceil_div(MN, kBlockThreads);
@@ -1504,6 +1540,44 @@ hipError_t launch_qmm_q8act(const void* W, const float* x, float* y, int32_t* is
     hipLaunchKernelGGL(qmm_reduce_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kBlockThreads), 0, stream,
                        part, y, p.ks, MN);
     return hipGetLastError();
+}
+
+hipError_t launch_qmm_q8act(const void* W, const float* x, float* y, int32_t* isum, int64_t isn0, int64_t isn1,
+                            int64_t N, int64_t K, int64_t M, void* ws, hipStream_t stream) {
+    const QmmPlan p = plan_qmm(N, K, M);
+    int8_t* q = static_cast<int8_t*>(ws);
+    float* d = reinterpret_cast<float*>(static_cast<char*>(ws) + p.q_bytes);
+    float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.q_bytes + p.d_bytes);
+    const hipError_t e = p.path == kPathWide     ? launch_quantize<kLayoutSplit>(x, q, d, K, M, p.xrows, stream)
+                         : p.path == kPathNarrow ? launch_quantize<kLayoutFrag>(x, q, d, K, M, p.xrows, stream)
+                                                 : launch_quantize<kLayoutRows>(x, q, d, K, M, M, stream);
+    if (e != hipSuccess) return e;
+    return launch_step2(p, W, q, d, part, y, isum, isn0, isn1, N, K, M, stream);
+}
+
+hipError_t launch_qmm_q8(const void* W, const int8_t* qin, const float* din, float* y, int64_t N, int64_t K, int64_t M,
+                         void* ws, hipStream_t stream) {
+    const QmmPlan p = plan_qmm(N, K, M);
+    int8_t* q = static_cast<int8_t*>(ws);
+    float* d = reinterpret_cast<float*>(static_cast<char*>(ws) + p.q_bytes);
+    float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.q_bytes + p.d_bytes);
+    if (p.path != kPathWide && p.path != kPathNarrow)
+        return launch_step2(p, W, qin, din, part, y, nullptr, 0, 0, N, K, M, stream);
+    const int64_t cap = static_cast<int64_t>(device_cus()) * 16;
+    if (p.path == kPathWide) {
+        int64_t blocks = ceil_div((p.xrows / 32) * (K / 32), kWavesPerBlock);
+        if (blocks > cap) blocks = cap;
+        hipLaunchKernelGGL(layout_q8_tiles_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kBlockThreads), 0, stream,
+                           qin, din, q, reinterpret_cast<uint4*>(d), K, M, p.xrows);
+    } else {
+        int64_t blocks = ceil_div(p.xrows * (K / 4), kBlockThreads);
+        if (blocks > cap) blocks = cap;
+        hipLaunchKernelGGL(layout_q8_frag_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kBlockThreads), 0, stream,
+                           qin, din, q, d, K, M, p.xrows);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    return launch_step2(p, W, q, d, part, y, nullptr, 0, 0, N, K, M, stream);
 }
 
 size_t qmm_f32act_ws_bytes(int64_t N, int64_t K, int64_t M) {

@@ -1,7 +1,7 @@
 """Python binding of libqmv.so (argument marshalling only).
 
 Every function has the name and argument order of the C entry point declared
-in include/qmv.h.  Buffer arguments are torch tensors on the GPU (or raw
+in include/qmv.h or include/qmv_step.h.  Buffer arguments are torch tensors on the GPU (or raw
 device addresses as ints); sizes are ints; ``stream`` is a torch stream (None:
 torch's current stream).  A non-zero status raises QmvError.  All compute
 happens in the HIP kernels of libqmv.so; there is no fallback of any kind.
@@ -51,12 +51,38 @@ _SIGS = {
     "qmvdbg_sample_f32": ([_P, _P, _P, _P, _P, _I64, _I32, _F, _F, _P], ctypes.c_int),
     "qmvdbg_stream_read": ([_P, _I64, _P, _I32, _P], ctypes.c_int),
 }
-for _name, (_args, _res) in _SIGS.items():
+
+
+class _KVCache(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("num_pages", _I64), ("kv_heads", _I32),
+                ("head_dim", _I32), ("page_size", _I32), ("format", _I32)]
+
+
+class _KVBatch(ctypes.Structure):
+    _fields_ = [("page_table", _P), ("row_start", _P), ("kv_len", _P), ("T", _I64), ("B", _I32), ("max_pages", _I32)]
+
+
+# include/qmv_step.h
+_STEP_SIGS = {
+    "kv_write": ([_P, _P, _P, _I64, _P, _I64, _P], ctypes.c_int),
+    "kv_read": ([_P, _P, _P, _I64, _P, _I64, _P], ctypes.c_int),
+    "attn_paged_ws_bytes": ([_P, _P, _I32], _SZ),
+    "attn_paged": ([_P, _P, _P, _I64, _P, _I64, _I32, _F, _I32, _P, _SZ, _P], ctypes.c_int),
+    "rmsnorm_add": ([_P, _P, _P, _P, _P, _I64, _I64, _F, _P], ctypes.c_int),
+    "rmsnorm_add_q8": ([_P, _P, _P, _P, _P, _P, _I64, _I64, _F, _P], ctypes.c_int),
+    "qmm_q4_0_q8_ws_bytes": ([_I64, _I64, _I64], _SZ),
+    "qmm_q4_0_q8": ([_P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P], ctypes.c_int),
+    "draft_verify_ws_bytes": ([_I64, _I32, _I64], _SZ),
+    "draft_verify": ([_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _I32, _I64, _F, _F, _P, _SZ, _P], ctypes.c_int),
+}
+for _name, (_args, _res) in (_SIGS | _STEP_SIGS).items():
     _fn = getattr(lib, _name)
     _fn.argtypes = _args
     _fn.restype = _res
 
 EXPORTS = tuple(_SIGS)
+STEP_EXPORTS = tuple(_STEP_SIGS)
+KV_Q8, KV_F16 = 0, 1
 
 QMV_OK, QMV_ERR_NULL, QMV_ERR_SHAPE, QMV_ERR_ALIGN, QMV_ERR_WORKSPACE, QMV_ERR_LAUNCH, QMV_ERR_ARG = range(7)
 
@@ -191,3 +217,102 @@ def qmvdbg_sample_f32(top_val, top_idx, u, token, nucleus, M, k, temperature, to
 
 def qmvdbg_stream_read(p, nbytes, out, workgroups, stream=None):
     _call("qmvdbg_stream_read", _ptr(p), nbytes, _ptr(out), workgroups, _stream(stream))
+
+
+# ---- include/qmv_step.h ----
+
+class KVCache:
+    """qmv_kv_cache over torch tensors: k, v [num_pages][kv_heads][page_size][head_dim], int8 with k_scale, v_scale
+    float32 [num_pages][kv_heads][page_size] (KV_Q8), or float16 without (KV_F16).  Keeps the tensors alive."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        q8 = k.dtype == torch.int8
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.dtype not in (torch.int8, torch.float16):
+            raise ValueError("k and v: one shape [num_pages][kv_heads][page_size][head_dim], both int8 or both float16")
+        scales = (k_scale, v_scale)
+        if q8 and any(s is None or s.shape != k.shape[:3] or s.dtype != torch.float32 for s in scales):
+            raise ValueError("int8 codes need k_scale and v_scale, float32 [num_pages][kv_heads][page_size]")
+        if not q8 and any(s is not None for s in scales):
+            raise ValueError("a float16 cache has no scales")
+        self.tensors = tuple(t for t in (k, v, *scales) if t is not None)
+        _on_gpu(*self.tensors)
+        self.struct = _KVCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.shape[0], k.shape[1], k.shape[3],
+                               k.shape[2], KV_Q8 if q8 else KV_F16)
+        self.ref = ctypes.addressof(self.struct)
+
+
+class KVBatch:
+    """qmv_kv_batch over torch tensors: page_table int32 [B][max_pages], row_start int32 [B + 1], kv_len int32 [B];
+    T rows in the row buffers.  Keeps the tensors alive."""
+
+    def __init__(self, page_table, row_start, kv_len, T):
+        tensors = (page_table, row_start, kv_len)
+        if any(t.dtype != torch.int32 for t in tensors) or page_table.dim() != 2:
+            raise ValueError("page_table [B][max_pages], row_start [B + 1] and kv_len [B] are int32")
+        B = page_table.shape[0]
+        if row_start.shape != (B + 1,) or kv_len.shape != (B,):
+            raise ValueError("row_start has B + 1 entries and kv_len B")
+        _on_gpu(*tensors)
+        self.tensors = tensors
+        self.struct = _KVBatch(_ptr(page_table), _ptr(row_start), _ptr(kv_len), T, B, page_table.shape[1])
+        self.ref = ctypes.addressof(self.struct)
+
+
+def _on_gpu(*tensors):
+    """The descriptors' tensors are contiguous and on the current GPU."""
+    for t in tensors:
+        _gpu(t)
+        if not t.is_contiguous():
+            raise ValueError("the tensors of a descriptor are contiguous")
+
+
+def _gpu(t):
+    """Address of a tensor that the current GPU's kernels can use (a raw address is the caller's word)."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"a tensor on {t.device} was given to a kernel of the current GPU")
+    return t.data_ptr()
+
+
+def kv_write(cache, batch, k, ldk, v, ldv, stream=None):
+    _call("kv_write", cache.ref, batch.ref, _gpu(k), ldk, _gpu(v), ldv, _stream(stream))
+
+
+def kv_read(cache, batch, k, ldk, v, ldv, stream=None):
+    _call("kv_read", cache.ref, batch.ref, _gpu(k), ldk, _gpu(v), ldv, _stream(stream))
+
+
+def attn_paged_ws_bytes(cache, batch, q_heads) -> int:
+    return int(lib.attn_paged_ws_bytes(cache.ref, batch.ref, q_heads))
+
+
+def attn_paged(cache, batch, q, ldq, out, ldo, q_heads, scale, window, ws, ws_bytes, stream=None):
+    _call("attn_paged", cache.ref, batch.ref, _gpu(q), ldq, _gpu(out), ldo, q_heads, scale, window, _gpu(ws), ws_bytes,
+          _stream(stream))
+
+
+def rmsnorm_add(x, r, w, z, y, K, M, eps, stream=None):
+    _call("rmsnorm_add", _gpu(x), _gpu(r), _gpu(w), _gpu(z), _gpu(y), K, M, eps, _stream(stream))
+
+
+def rmsnorm_add_q8(x, r, w, z, q, d, K, M, eps, stream=None):
+    _call("rmsnorm_add_q8", _gpu(x), _gpu(r), _gpu(w), _gpu(z), _gpu(q), _gpu(d), K, M, eps, _stream(stream))
+
+
+def qmm_q4_0_q8_ws_bytes(N, K, M) -> int:
+    return int(lib.qmm_q4_0_q8_ws_bytes(N, K, M))
+
+
+def qmm_q4_0_q8(W, q, d, y, N, K, M, ws, ws_bytes, stream=None):
+    _call("qmm_q4_0_q8", _gpu(W), _gpu(q), _gpu(d), _gpu(y), N, K, M, _gpu(ws), ws_bytes, _stream(stream))
+
+
+def draft_verify_ws_bytes(B, G, V) -> int:
+    return int(lib.draft_verify_ws_bytes(B, G, V))
+
+
+def draft_verify(target, ldt, draft, ldd, draft_tokens, n_draft, u, accepted, tokens, B, G, V, temperature, softcap, ws,
+                 ws_bytes, stream=None):
+    _call("draft_verify", _gpu(target), ldt, _gpu(draft), ldd, _gpu(draft_tokens), _gpu(n_draft), _gpu(u), _gpu(accepted),
+          _gpu(tokens), B, G, V, temperature, softcap, _gpu(ws), ws_bytes, _stream(stream))
