@@ -95,7 +95,15 @@ def attention(q, k, v, positions, scale, window):
     sum|q k|.  A relative error e^ds - 1 of every weight moves the result by at
     most 2 max|ds| sum p|v|.  exp2, the scale and the split of p into two
     float16 terms cost a few roundings each (16 eps), and a running sum of L
-    terms a random walk of half steps (4 sqrt(L) eps)."""
+    terms a random walk of half steps (4 sqrt(L) eps).
+
+    A weight is held as p c with c such that p = 1 at the largest value scale
+    is 2^10 (float16 caches: c = 2^10), and its second float16 term ends at
+    float16's smallest step 2^-24: a weight is off by at most 2^-34 of the
+    largest one however small it is.  The sum of the weights is at least 1, so
+    the result is off by at most L 2^-34 max|v| more, with max|v| at most
+    twice the largest element (127 codes of the largest scale; every row here
+    has a code of 64 or more)."""
     n, Hq, D = q.shape
     L, H, _ = k.shape
     out = np.zeros((n, Hq, D))
@@ -115,6 +123,7 @@ def attention(q, k, v, positions, scale, window):
             e /= e.sum()
             out[i, h] = e @ vv
             tol[i, h] += (e @ np.abs(vv)) * (2 * ds.max() + (16 + 4 * math.sqrt(hi - lo)) * EPS32)
+            tol[i, h] += (hi - lo) * 2.0 ** -34 * 2 * np.abs(vv).max()
     return out, tol
 
 
