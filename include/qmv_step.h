@@ -74,7 +74,7 @@ typedef struct qmv_kv_cache {
  * from max_pages * page_size on have no place.  The contents of the three
  * arrays are checked where they are used, on the device: a page number
  * outside [0, num_pages) is never followed, its positions hold nothing.
- * 1 <= T < 2^24, 1 <= B <= 65535, max_pages * page_size < 2^31. */
+ * 1 <= T < 2^24, 1 <= B <= 65535, max_pages * page_size <= 2^30. */
 typedef struct qmv_kv_batch {
     const int32_t* page_table;
     const int32_t* row_start;

@@ -66,7 +66,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_inff();
 constexpr int kTile = 32;                        // keys of one wave's step
 constexpr int kStep = kTile * kWavesPerBlock;    // keys of the workgroup's step
-constexpr int kUnit = kStep;                     // keys of one unit of work
+constexpr int kUnitShift = 7;                    // a unit of work is one step (more for huge tables)
 constexpr float kQParts = 127.0f * 16384.0f;     // largest |q| in parts: 127 2^14
 constexpr float kSlack = 3.0f;                   // p may reach 2^3 before the maximum moves
 
@@ -78,14 +78,15 @@ struct AttnArgs {
     const float* vs;
     const float* q;
     float* out;
-    float* part;       // partial results, slot(w, s) = part + (2 w + s) * slot size
+    float* part;       // partial results: slot i of workgroup w at part + (2 w + i) * slot size
+    int4* owners;      // of item (tile slot, head): first and last workgroup, slot of the first
     int64_t ldq, ldo;
     int group;         // query heads of a key/value head
     float scale_log2;  // |scale| log2(e)
     float sign;        // of scale
     int window;
-    int unit;          // keys of one unit
-    int workgroups;    // of one round (a run each)
+    int unit_shift;    // log2 of a unit's keys (split only)
+    int workgroups;    // of one round, a run of units each (split only)
     bool vec_q, vec_o;
 };
 
@@ -98,7 +99,7 @@ struct Seq {
     int units;      // of one row tile and head
 };
 
-template <int ROWS>
+template <int ROWS, bool SPLIT>
 __device__ __forceinline__ Seq sequence(const AttnArgs& A, int b) {
     Seq s;
     s.first = A.view.row_start[b];
@@ -112,100 +113,114 @@ __device__ __forceinline__ Seq sequence(const AttnArgs& A, int b) {
     s.lo = lo > 0 ? static_cast<int>(lo) & ~(kTile - 1) : 0;
     s.tiles = (s.n * A.group + ROWS - 1) / ROWS;
     // an item whose rows see nothing is one empty unit: its zeros are written
-    s.units = s.hi > s.lo ? (s.hi - s.lo - 1) / A.unit + 1 : 1;
+    s.units = SPLIT && s.hi > s.lo ? ((s.hi - s.lo - 1) >> A.unit_shift) + 1 : 1;
     return s;
 }
 
-struct Place {
-    int b;
-    int64_t units_before;  // units of all sequences before b
-    int tiles_before;
-    int64_t total;         // units of the batch
+// Row tiles are numbered without a sum over the sequences before: sequence b
+// has the numbers from floor(row_start[b] group / ROWS) + b on, as many as
+// it can need (its last ones may be unused).
+template <int ROWS>
+__device__ __forceinline__ int first_tile(const AttnArgs& A, int b) {
+    return min(max(A.view.row_start[b], 0), A.view.T) * A.group / ROWS + b;
+}
+
+// The sequence whose numbers hold tile x: the wave tests 64 entries a step.
+template <int ROWS>
+__device__ __forceinline__ int sequence_of_tile(const AttnArgs& A, int x) {
+    const int lane = threadIdx.x & (kWave - 1);
+    int lo = 0, span = A.view.B - 1;
+    while (span > 0) {
+        const int step = (span + kWave - 1) / kWave;
+        const int off = (lane + 1) * step;
+        const bool below = off <= span && first_tile<ROWS>(A, lo + off) <= x;
+        const int c = __popcll(__ballot(below));
+        const int left = span - c * step;
+        lo += c * step;
+        span = left < step - 1 ? left : step - 1;
+    }
+    return lo;
+}
+
+// Inclusive sum over the lanes of a wave: within rows of 16 (row_shr 1, 2, 4,
+// 8), then across them (row_bcast 15 and 31).
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+    return v;
+}
+
+// Runs: `total` units in min(workgroups, total) runs whose lengths differ by
+// at most one, the longer ones first.
+struct Runs {
+    int total, per, longer;
+    __device__ __forceinline__ Runs(int total_, int workgroups)
+        : total(total_), per(static_cast<int>(static_cast<uint32_t>(total_) / static_cast<uint32_t>(workgroups))),
+          longer(total_ - per * workgroups) {}
+    __device__ __forceinline__ int start(int w) const { return w * per + min(w, longer); }
+    // the run that holds unit u
+    __device__ __forceinline__ int owner(int u) const {
+        const int head = longer * (per + 1);
+        if (u < head) return static_cast<int>(static_cast<uint32_t>(u) / static_cast<uint32_t>(per + 1));
+        return longer + static_cast<int>(static_cast<uint32_t>(u - head) / static_cast<uint32_t>(per));
+    }
 };
 
-// Finds the sequence that holds unit `key` (of the batch's units in order of
-// sequence, row tile, head, position), or, with BY_TILE, row tile `key`.
-// All 256 threads; B sequences, 256 at a time.  b = B if there is none.
-template <int ROWS, bool BY_TILE>
-__device__ Place locate(const AttnArgs& A, int64_t key, bool by_share, int64_t* lds /* 12 */) {
+struct Place {
+    int b;       // the sequence that holds the first unit of the run; B: no run
+    int before;  // units of the sequences before it
+    int total;   // units of the batch
+};
+
+// Units are numbered by sequence, row tile, head, position.  All 256 threads
+// sum the sequences' units, 256 sequences at a time.
+template <int ROWS>
+__device__ Place locate(const AttnArgs& A, int w, int* lds /* 6 */) {
     const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave;
-    const int heads = A.view.heads;
-    int64_t* sums = lds;       // [4]: units of the waves' sequences
-    int64_t* tsum = lds + 4;   // [4]: row tiles
-    int64_t* found = lds + 8;  // b, units before, tiles before
     const bool one = A.view.B <= kBlockThreads;
-    int64_t u = 0, c = 0;
+    auto units = [&](int b) {
+        if (b >= A.view.B) return 0;
+        const Seq s = sequence<ROWS, true>(A, b);
+        return s.tiles * A.view.heads * s.units;
+    };
     Place P;
     P.total = 0;
-    if (t == 0) found[0] = A.view.B;
-    for (int b0 = 0; b0 < A.view.B; b0 += kBlockThreads) {
-        u = c = 0;
-        if (b0 + t < A.view.B) {
-            const Seq s = sequence<ROWS>(A, b0 + t);
-            c = s.tiles;
-            u = static_cast<int64_t>(s.tiles) * heads * s.units;
-        }
-        if (one) break;
-        int64_t w = u;
-        for (int o = kWave / 2; o > 0; o >>= 1) w += __shfl_xor(w, o, kWave);
-        __syncthreads();
-        if (lane == 0) sums[wave] = w;
-        __syncthreads();
-        P.total += sums[0] + sums[1] + sums[2] + sums[3];
-    }
-    int64_t base_u = 0, base_c = 0;
-    for (int b0 = 0; b0 < A.view.B; b0 += kBlockThreads) {
-        if (!one) {
-            u = c = 0;
-            if (b0 + t < A.view.B) {
-                const Seq s = sequence<ROWS>(A, b0 + t);
-                c = s.tiles;
-                u = static_cast<int64_t>(s.tiles) * heads * s.units;
+    P.b = A.view.B;
+    P.before = 0;
+    if (t == 0) lds[4] = A.view.B;
+    int scan = 0, mine = 0, key = 0;
+    for (int pass = one ? 1 : 0; pass < 2; ++pass) {  // the sum, then the place
+        int base = 0;
+        for (int b0 = 0; b0 < A.view.B; b0 += kBlockThreads) {
+            mine = units(b0 + t);
+            scan = wave_scan(mine);
+            __syncthreads();
+            if (lane == kWave - 1) lds[wave] = scan;
+            __syncthreads();
+            int before = base;
+            for (int i = 0; i < kWavesPerBlock; ++i) {
+                if (i < wave) before += lds[i];
+                base += lds[i];
+            }
+            if (pass == 0) continue;
+            if (one) P.total = base;
+            const Runs R(P.total, A.workgroups);
+            key = R.start(w) < R.start(w + 1) ? R.start(w) : -1;
+            const int begin = before + scan - mine;
+            if (key >= begin && key < begin + mine) {
+                lds[4] = b0 + t;
+                lds[5] = begin;
             }
         }
-        int64_t iu = u, ic = c;
-        for (int o = 1; o < kWave; o <<= 1) {
-            const int64_t xu = __shfl_up(iu, o, kWave), xc = __shfl_up(ic, o, kWave);
-            if (lane >= o) {
-                iu += xu;
-                ic += xc;
-            }
-        }
-        __syncthreads();
-        if (lane == kWave - 1) {
-            sums[wave] = iu;
-            tsum[wave] = ic;
-        }
-        __syncthreads();
-        int64_t strip = 0, strip_c = 0, before = base_u, before_c = base_c;
-        for (int w = 0; w < kWavesPerBlock; ++w) {
-            if (w < wave) {
-                before += sums[w];
-                before_c += tsum[w];
-            }
-            strip += sums[w];
-            strip_c += tsum[w];
-        }
-        if (one) P.total = strip;
-        if (by_share && b0 == 0) {
-            // the first unit of workgroup `key`'s run, of min(workgroups, total) runs
-            const int64_t W = P.total < A.workgroups ? P.total : A.workgroups;
-            key = key < W ? key * P.total / W : P.total;
-        }
-        const int64_t end = BY_TILE ? before_c + ic : before + iu;
-        const int64_t begin = end - (BY_TILE ? c : u);
-        if (key >= begin && key < end) {
-            found[0] = b0 + t;
-            found[1] = before + iu - u;
-            found[2] = before_c + ic - c;
-        }
-        base_u += strip;
-        base_c += strip_c;
+        if (pass == 0) P.total = base;
     }
     __syncthreads();
-    P.b = static_cast<int>(found[0]);
-    P.units_before = P.b < A.view.B ? found[1] : 0;
-    P.tiles_before = P.b < A.view.B ? static_cast<int>(found[2]) : 0;
+    P.b = lds[4];
+    if (P.b < A.view.B) P.before = lds[5];
     return P;
 }
 
@@ -272,8 +287,12 @@ __device__ __forceinline__ Pages pages_of(const AttnArgs& A, int b, int h, int k
     return p;
 }
 
+// Keys and their scales, values and theirs: loaded apart, each into the
+// registers that the step before has just used, so that a tile's keys arrive
+// while the tile before is in its softmax and products, and its values while
+// its own scores are computed.
 template <int D, bool F16>
-__device__ __forceinline__ void load_tile(const AttnArgs& A, const Pages& p, KvRegs<D, F16>& r) {
+__device__ __forceinline__ void load_keys(const AttnArgs& A, const Pages& p, KvRegs<D, F16>& r) {
     using T = KvRegs<D, F16>;
     constexpr int kRow = D * T::kE;  // bytes of a key
     const int lane = threadIdx.x & (kWave - 1), n = lane & 15, g = lane >> 4;
@@ -282,10 +301,18 @@ __device__ __forceinline__ void load_tile(const AttnArgs& A, const Pages& p, KvR
         const uint8_t* kp = A.k + p.cell[u] * kRow + (n * kRow + g * 16);
 #pragma unroll
         for (int s = 0; s < T::kKLoads; ++s) r.k[u][s] = *reinterpret_cast<const u32x4*>(kp + 64 * s);
-        if constexpr (!F16) {
-            r.ks[u] = *reinterpret_cast<const f32x4*>(A.ks + p.cell[u] + 4 * g);
-            r.vs[u] = *reinterpret_cast<const f32x4*>(A.vs + p.cell[u] + 4 * g);
-        }
+        if constexpr (!F16) r.ks[u] = *reinterpret_cast<const f32x4*>(A.ks + p.cell[u] + 4 * g);
+    }
+}
+
+template <int D, bool F16>
+__device__ __forceinline__ void load_values(const AttnArgs& A, const Pages& p, KvRegs<D, F16>& r) {
+    using T = KvRegs<D, F16>;
+    constexpr int kRow = D * T::kE;
+    const int lane = threadIdx.x & (kWave - 1), n = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        if constexpr (!F16) r.vs[u] = *reinterpret_cast<const f32x4*>(A.vs + p.cell[u] + 4 * g);
         const uint8_t* vp = A.v + p.cell[u] * kRow + (4 * g * kRow + n * (kRow / 16));
 #pragma unroll
         for (int e = 0; e < 4; ++e) load_words(r.v[4 * u + e], vp + e * kRow);
@@ -298,7 +325,8 @@ struct Rows {
     static constexpr int kQ = F16 ? D / 32 : D / 64;  // instructions of one term over D
     static constexpr int kTerms = F16 ? 2 : 3;
     u32x4 q[R][kTerms][kQ];
-    float qs[R];   // score in log2 units = qs * (integer or float16 score) [* key scale]
+    float qs[R];   // score in log2 units = qs * (integer or float16 score) [* key scale], > 0
+    bool broken[R];  // the query is not finite
     int pos[R];    // position of the lane's row, -1 for a row past the item's
     f32x4 o[R][D / 16];
     float m[R];    // running maximum, before qs
@@ -359,8 +387,14 @@ __device__ __forceinline__ void load_rows(const AttnArgs& A, const Seq& S, int t
             back = an * (1.0f / kQParts);
         }
         W.qs[r] = __builtin_amdgcn_ldexpf(back * A.scale_log2, k);
-        broken = row_max(broken ? 1.0f : 0.0f) != 0.0f;
-        if (broken) W.qs[r] = __uint_as_float(0x7fc00000u);
+        // all scores equal (a zero query or scale), or a row that will be NaN:
+        // zero parts with a factor that keeps masked scores at -infinity
+        W.broken[r] = row_max(broken ? 1.0f : 0.0f) != 0.0f;
+        const bool flat = W.broken[r] || !(W.qs[r] > 0.0f);
+        if (flat) {
+            W.qs[r] = 1.0f;
+            inv = 0.0f;
+        }
         inv *= A.sign;
 #pragma unroll
         for (int s = 0; s < T::kQ; ++s) {
@@ -368,8 +402,8 @@ __device__ __forceinline__ void load_rows(const AttnArgs& A, const Seq& S, int t
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
-                    const float a = __builtin_amdgcn_ldexpf(x[s][e], -k) * inv;
-                    const float b = __builtin_amdgcn_ldexpf(x[s][e + 1], -k) * inv;
+                    const float a = flat ? 0.0f : __builtin_amdgcn_ldexpf(x[s][e], -k) * inv;
+                    const float b = flat ? 0.0f : __builtin_amdgcn_ldexpf(x[s][e + 1], -k) * inv;
                     const f16x2 f = {static_cast<_Float16>(a), static_cast<_Float16>(b)};
                     hi[e / 2] = __builtin_bit_cast(uint32_t, f);
                     const f16x2 d = {static_cast<_Float16>(a - static_cast<float>(f[0])),
@@ -383,7 +417,7 @@ __device__ __forceinline__ void load_rows(const AttnArgs& A, const Seq& S, int t
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     // x = a 2^14 + b 2^7 + c, b and c in [-64, 63]
-                    const int v = static_cast<int>(rintf(__builtin_amdgcn_ldexpf(x[s][e], -k) * inv));
+                    const int v = flat ? 0 : static_cast<int>(rintf(__builtin_amdgcn_ldexpf(x[s][e], -k) * inv));
                     const int vc = ((v + 64) & 127) - 64;
                     const int v1 = (v - vc) >> 7;
                     const int vb = ((v1 + 64) & 127) - 64;
@@ -406,42 +440,20 @@ __device__ __forceinline__ void load_rows(const AttnArgs& A, const Seq& S, int t
     }
 }
 
-// One tile of 32 keys, at positions key ..; MASK: some row does not see some
-// key of it (or a half has no page).
-template <bool MASK, int D, bool F16, int R>
-__device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv, Rows<D, F16, R>& W, int key,
-                                          bool ok0, bool ok1, int hi_any, int lo_any) {
+// One tile of 32 keys at positions key ..  edge: some row does not see some
+// key of it, or a half has no page (wave-uniform).  `reload_keys` and
+// `reload_values` fetch the next tile as soon as the registers are free.
+template <int D, bool F16, int R, class LoadK, class LoadV>
+__device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv, Rows<D, F16, R>& W, int key, bool edge,
+                                          bool ok0, bool ok1, int hi_any, int lo_any, LoadK reload_keys,
+                                          LoadV reload_values) {
     using T = Rows<D, F16, R>;
     using V = KvRegs<D, F16>;
     const int lane = threadIdx.x & (kWave - 1), g = lane >> 4;
 
-    // float16 values at positions no row sees may be anything: zero times
-    // them has to be zero.  At positions that only some rows see, a value
-    // that is not finite is taken out and makes those rows NaN by their sum.
-    uint32_t broken = 0;
-    if constexpr (MASK && F16) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int j = key + 16 * (e >> 2) + 4 * g + (e & 3);
-            const bool any = (e < 4 ? ok0 : ok1) && j < hi_any && j >= lo_any;
-            bool bad = false;
-#pragma unroll
-            for (int w = 0; w < V::kVWords; ++w) {
-                const uint32_t x = kv.v[e][w];
-                bad |= (x & 0x7c00u) == 0x7c00u || (x & 0x7c000000u) == 0x7c000000u;
-            }
-            const uint64_t where = __ballot(bad && any);
-            const bool out = ((where >> (16 * g)) & 0xffffu) != 0;
-            if (out) broken |= 1u << e;
-#pragma unroll
-            for (int w = 0; w < V::kVWords; ++w) kv.v[e][w] = (any && !out) ? kv.v[e][w] : 0u;
-        }
-    }
-
-    uint32_t ph[R][4], pl[R][4];
+    float s[R][8];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        float s[8];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             if constexpr (F16) {
@@ -453,7 +465,7 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
                         a = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, kv.k[u][i]),
                                                                    __builtin_bit_cast(f16x8, W.q[r][term][i]), a, 0, 0, 0);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[4 * u + e] = a[e];
+                for (int e = 0; e < 4; ++e) s[r][4 * u + e] = a[e];
             } else {
                 i32x4 a[3] = {};
 #pragma unroll
@@ -465,29 +477,67 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
                                                                         0, 0, 0);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    s[4 * u + e] = fmaf(static_cast<float>(a[0][e]), 16384.0f,
-                                        static_cast<float>((a[1][e] << 7) + a[2][e])) * kv.ks[u][e];
+                    s[r][4 * u + e] = fmaf(static_cast<float>(a[0][e]), 16384.0f,
+                                           static_cast<float>((a[1][e] << 7) + a[2][e])) * kv.ks[u][e];
             }
         }
-        bool seen[8];
-        float top = -kInf, big = 0.0f;
+    }
+    reload_keys();
+
+    // float16 values at positions no row sees may be anything: zero times
+    // them has to be zero.  At positions that only some rows see, a value
+    // that is not finite is taken out and makes those rows NaN by their sum.
+    uint32_t taken = 0;
+    if constexpr (F16) {
+        if (edge) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if constexpr (MASK) {
+            for (int e = 0; e < 8; ++e) {
                 const int j = key + 16 * (e >> 2) + 4 * g + (e & 3);
-                seen[e] = (e < 4 ? ok0 : ok1) && j <= W.pos[r] && j < hi_any &&
-                          (A.window == 0 || j - W.pos[r] > -A.window);
-                s[e] = seen[e] ? s[e] : -kInf;
-                if constexpr (!F16) big = fmaxf(big, seen[e] ? kv.vs[e >> 2][e & 3] : 0.0f);
-            } else {
-                seen[e] = true;
-                if constexpr (!F16) big = fmaxf(big, kv.vs[e >> 2][e & 3]);
+                const bool any = (e < 4 ? ok0 : ok1) && j < hi_any && j >= lo_any;
+                bool bad = false;
+#pragma unroll
+                for (int w = 0; w < V::kVWords; ++w) {
+                    const uint32_t x = kv.v[e][w];
+                    bad |= (x & 0x7c00u) == 0x7c00u || (x & 0x7c000000u) == 0x7c000000u;
+                }
+                const uint64_t where = __ballot(bad && any);
+                const bool out = ((where >> (16 * g)) & 0xffffu) != 0;
+                if (out) taken |= 1u << e;
+#pragma unroll
+                for (int w = 0; w < V::kVWords; ++w) kv.v[e][w] = (any && !out) ? kv.v[e][w] : 0u;
             }
-            top = fmaxf(top, s[e]);
+        }
+    }
+
+    uint32_t ph[R][4], pl[R][4];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        float dv[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dv[e] = F16 ? 1.0f : kv.vs[e >> 2][e & 3];
+        if (edge) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int j = key + 16 * (e >> 2) + 4 * g + (e & 3);
+                const bool seen = (e < 4 ? ok0 : ok1) && j <= W.pos[r] && j < hi_any &&
+                                  (A.window == 0 || j - W.pos[r] > -A.window);
+                s[r][e] = seen ? s[r][e] : -kInf;
+                if constexpr (F16) {
+                    if (seen && (taken >> e & 1)) W.l[r] = __uint_as_float(0x7fc00000u);
+                } else {
+                    dv[e] = seen ? dv[e] : 0.0f;
+                }
+            }
+        }
+        float top = fmaxf(fmaxf(fmaxf(s[r][0], s[r][1]), fmaxf(s[r][2], s[r][3])),
+                          fmaxf(fmaxf(s[r][4], s[r][5]), fmaxf(s[r][6], s[r][7])));
+        float big = 0.0f;
+        if constexpr (!F16) {
+            big = fmaxf(fmaxf(fmaxf(dv[0], dv[1]), fmaxf(dv[2], dv[3])), fmaxf(fmaxf(dv[4], dv[5]), fmaxf(dv[6], dv[7])));
         }
         // The maximum and the factor of the value scales move only when a
         // row has outgrown them: p and its products stay within float16.
-        const bool grow = (top - W.m[r]) * W.qs[r] > kSlack || (W.m[r] == -kInf && top > -kInf) || big > W.lim[r];
+        const bool grow = (top - W.m[r]) * W.qs[r] > kSlack || big > W.lim[r];
         if (__ballot(grow) != 0) {
             top = row_max(top);
             const float mn = fmaxf(W.m[r], top);
@@ -514,17 +564,9 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
         float p[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            p[e] = __builtin_amdgcn_exp2f(fmaf(s[e], W.qs[r], -mq));
-            if constexpr (MASK) p[e] = seen[e] ? p[e] : 0.0f;
+            p[e] = __builtin_amdgcn_exp2f(fmaf(s[r][e], W.qs[r], -mq));
             W.l[r] += p[e];
-            if constexpr (MASK && F16)
-                if (seen[e] && (broken >> e & 1)) W.l[r] = __uint_as_float(0x7fc00000u);
-            if constexpr (F16) {
-                p[e] *= 1024.0f;
-            } else {
-                p[e] *= kv.vs[e >> 2][e & 3] * W.c[r];
-                if constexpr (MASK) p[e] = seen[e] ? p[e] : 0.0f;
-            }
+            p[e] *= F16 ? 1024.0f : dv[e] * W.c[r];
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -561,48 +603,84 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
                 va, __builtin_bit_cast(f16x8, u32x4{pl[r][0], pl[r][1], pl[r][2], pl[r][3]}), W.o[r][t], 0, 0, 0);
         }
     }
+    reload_values();
 }
 
 // Floats of one partial slot: 16 R rows of D sums, then their maxima, then sums.
 template <int D, int R>
 constexpr int kSlotFloats = 16 * R * (D + 2);
 
-template <int D, bool F16, int R>
+// Four dimensions of a row's result.  A row that saw nothing has sum 0.
+template <int D>
+__device__ __forceinline__ void store_row(const AttnArgs& A, const Seq& S, int h, int rho, int d, f32x4 v, float sum) {
+    v = sum == 0.0f ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : v / sum;
+    const int i = rho / A.group;
+    float* o = A.out + static_cast<int64_t>(S.first + i) * A.ldo + static_cast<int64_t>(h * A.group + rho - i * A.group) * D + d;
+    if (A.vec_o) {
+        *reinterpret_cast<f32x4*>(o) = v;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = v[e];
+    }
+}
+
+template <int D, bool F16, int R, bool SPLIT>
 __global__ __launch_bounds__(kBlockThreads)
 void attn_kernel(AttnArgs A) {
     constexpr int kRows = 16 * R;
     constexpr int kPad = D + 4;
     __shared__ __align__(16) float so[kWavesPerBlock * 16 * kPad];
     __shared__ float sm[kWavesPerBlock][kRows], sl[kWavesPerBlock][kRows];
-    __shared__ int64_t place[12];
+    __shared__ int place[6];
     const int lane = threadIdx.x & (kWave - 1), n = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int w = blockIdx.x;
-    const Place P = locate<kRows, false>(A, w, true, place);
-    if (P.b >= A.view.B) return;  // no run
-    const int64_t W64 = P.total < A.workgroups ? P.total : A.workgroups;
-    int64_t u = static_cast<int64_t>(w) * P.total / W64;
-    const int64_t u_end = (static_cast<int64_t>(w) + 1) * P.total / W64;
-    int b = __builtin_amdgcn_readfirstlane(P.b);
-    int64_t before = P.units_before;
-    Seq S = sequence<kRows>(A, b);
+    int b, before = 0, total = 0, u = 0, u_end = 1;  // the run of units, and the units before sequence b
+    int tile = 0, h = 0, c0 = 0, c1 = 1;  // the piece: units c0 .. c1 - 1 of an item
+    Seq S;
+    if constexpr (SPLIT) {
+        const Place P = locate<kRows>(A, w, place);
+        b = __builtin_amdgcn_readfirstlane(P.b);
+        if (b >= A.view.B) return;  // no run
+        before = __builtin_amdgcn_readfirstlane(P.before);
+        total = __builtin_amdgcn_readfirstlane(P.total);
+        const Runs runs(total, A.workgroups);
+        u = runs.start(w);
+        u_end = runs.start(w + 1);
+        S = sequence<kRows, true>(A, b);
+    } else {
+        // items in order of tile, heads fastest: workgroups w and w + 8 (one
+        // XCD) work on the same few heads' keys
+        const int x = w / A.view.heads;
+        h = w - x * A.view.heads;
+        b = __builtin_amdgcn_readfirstlane(sequence_of_tile<kRows>(A, x));
+        S = sequence<kRows, false>(A, b);
+        tile = x - first_tile<kRows>(A, b);
+        if (tile < 0 || tile >= S.tiles) return;
+        tile = S.tiles - 1 - tile;  // the longest first
+    }
     bool first_piece = true;
     while (u < u_end) {
-        // the piece: an item's units from u on, as far as the run goes
-        while (u - before >= static_cast<int64_t>(S.tiles) * A.view.heads * S.units) {
-            before += static_cast<int64_t>(S.tiles) * A.view.heads * S.units;
-            S = sequence<kRows>(A, ++b);
+        if constexpr (SPLIT) {
+            while (u - before >= S.tiles * A.view.heads * S.units) {
+                before += S.tiles * A.view.heads * S.units;
+                S = sequence<kRows, true>(A, ++b);
+            }
+            const int item = static_cast<int>(static_cast<uint32_t>(u - before) / static_cast<uint32_t>(S.units));
+            c0 = u - before - item * S.units;
+            c1 = min(c0 + (u_end - u), S.units);
+            tile = static_cast<int>(static_cast<uint32_t>(item) / static_cast<uint32_t>(A.view.heads));
+            h = item - tile * A.view.heads;
+            if (c0 == 0 && threadIdx.x == 0) {
+                const Runs runs(total, A.workgroups);
+                const int last = c1 == S.units ? w : runs.owner(u + S.units - 1);
+                A.owners[static_cast<int64_t>(first_tile<kRows>(A, b) + tile) * A.view.heads + h] =
+                    make_int4(w, last, first_piece ? 0 : 1, 0);
+            }
+            u += c1 - c0;
+        } else {
+            u = u_end;
         }
-        const int64_t local = u - before;
-        const int item = static_cast<int>(local / S.units);
-        const int c0 = static_cast<int>(local - static_cast<int64_t>(item) * S.units);
-        const int64_t left = u_end - u;
-        const int c1 = static_cast<int>(left < S.units - c0 ? c0 + left : S.units);
-        const int h = item % A.view.heads, tile = item / A.view.heads;
-        u += c1 - c0;
-
-        Rows<D, F16, R> rows;
-        load_rows<D, F16, R>(A, S, tile, h, rows);
 
         // positions of the item's rows: tokens i0 .. i1
         const int i0 = tile * kRows / A.group;
@@ -615,43 +693,51 @@ void attn_kernel(AttnArgs A) {
             lo_any = static_cast<int>(max(static_cast<int64_t>(p0) - A.window + 1, int64_t{0}));
             lo_all = static_cast<int>(max(static_cast<int64_t>(p1) - A.window + 1, int64_t{0}));
         }
-        int64_t k1 = S.lo + static_cast<int64_t>(c1) * A.unit;
-        k1 = k1 < hi_any ? k1 : hi_any;
-        int64_t k0 = S.lo + static_cast<int64_t>(c0) * A.unit;
-        const int64_t low = lo_any & ~(kTile - 1);
-        k0 = k0 > low ? k0 : low;
-        const int end = static_cast<int>(k1 > 0 ? k1 : 0);
-        int key = static_cast<int>(k0 < end ? k0 : end) + wave * kTile;
-        if (key < end) {
-            KvRegs<D, F16> cur, nxt;
-            Pages pg = pages_of(A, b, h, key), pn;
-            load_tile<D, F16>(A, pg, cur);
-            pn = pages_of(A, b, h, min(key + kStep, end - 1) & ~(kTile - 1));
+        int end = hi_any, key = max(S.lo, lo_any & ~(kTile - 1));
+        if constexpr (SPLIT) {
+            const int64_t k1 = S.lo + (static_cast<int64_t>(c1) << A.unit_shift);
+            if (k1 < end) end = static_cast<int>(k1);
+            const int64_t k0 = S.lo + (static_cast<int64_t>(c0) << A.unit_shift);
+            if (k0 > key) key = static_cast<int>(k0 < end ? k0 : end);
+        }
+        key += wave * kTile;
+
+        KvRegs<D, F16> kv;
+        Pages pg = {};
+        const bool any = key < end;
+        if (any) {
+            pg = pages_of(A, b, h, key);
+            load_keys<D, F16>(A, pg, kv);
+            load_values<D, F16>(A, pg, kv);
+        }
+        Rows<D, F16, R> rows;
+        load_rows<D, F16, R>(A, S, tile, h, rows);
+        if (any) {
+            Pages pn = pages_of(A, b, h, end - key > kStep ? key + kStep : key);
             for (;;) {
                 const bool more = end - key > kStep;
-                if (more) load_tile<D, F16>(A, pn, nxt);
                 const Pages pt = pages_of(A, b, h, end - key > 2 * kStep ? key + 2 * kStep : key);
-                if (pg.ok[0] && pg.ok[1] && key + kTile <= hi_all && key >= lo_all)
-                    tile_step<false, D, F16, R>(A, cur, rows, key, true, true, hi_any, lo_any);
-                else
-                    tile_step<true, D, F16, R>(A, cur, rows, key, pg.ok[0], pg.ok[1], hi_any, lo_any);
+                const bool edge = !(pg.ok[0] && pg.ok[1] && key + kTile <= hi_all && key >= lo_all);
+                tile_step<D, F16, R>(
+                    A, kv, rows, key, edge, pg.ok[0], pg.ok[1], hi_any, lo_any,
+                    [&] { if (more) load_keys<D, F16>(A, pn, kv); }, [&] { if (more) load_values<D, F16>(A, pn, kv); });
                 if (!more) break;
                 key += kStep;
-                cur = nxt;
                 pg = pn;
                 pn = pt;
             }
         }
 
         // join the four waves, 16 rows at a time
-        float mq[R], ls[R];
+        float mq[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             mq[r] = rows.m[r] == -kInf ? -kInf : rows.m[r] * rows.qs[r];
-            ls[r] = row_sum(rows.l[r]);
+            float l = row_sum(rows.l[r]);
+            if (rows.broken[r] && rows.m[r] != -kInf) l = __uint_as_float(0x7fc00000u);
             if (g == 0) {
                 sm[wave][16 * r + n] = mq[r];
-                sl[wave][16 * r + n] = ls[r];
+                sl[wave][16 * r + n] = l;
             }
         }
         const bool whole = c0 == 0 && c1 == S.units;
@@ -686,17 +772,8 @@ void attn_kernel(AttnArgs A) {
 #pragma unroll
                 for (int i = 0; i < kWavesPerBlock; ++i)
                     L += sl[i][16 * r + row] * __builtin_amdgcn_exp2f(sm[i][16 * r + row] - (Mr == -kInf ? 0.0f : Mr));
-                if (whole) {
-                    v = L == 0.0f ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : v / L;
-                    const int i = rho / A.group;
-                    float* o = A.out + static_cast<int64_t>(S.first + i) * A.ldo +
-                               static_cast<int64_t>(h * A.group + rho - i * A.group) * D + d;
-                    if (A.vec_o) {
-                        *reinterpret_cast<f32x4*>(o) = v;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[e] = v[e];
-                    }
+                if (!SPLIT || whole) {
+                    store_row<D>(A, S, h, rho, d, v, L);
                 } else {
                     *reinterpret_cast<f32x4*>(slot + (16 * r + row) * D + d) = v;
                     if (d == 0) {
@@ -711,60 +788,73 @@ void attn_kernel(AttnArgs A) {
     }
 }
 
-// Joins the parts of every item that more than one workgroup worked on: one
-// workgroup a (row tile, head), slots in order of position.
+// Joins the parts of every item that more than one workgroup worked on, in
+// order of position: one workgroup a (row tile, head).  The threads that a
+// few rows leave idle share the parts among them.
 template <int D, int R>
 __global__ __launch_bounds__(kBlockThreads)
 void attn_join_kernel(AttnArgs A) {
     constexpr int kRows = 16 * R;
-    __shared__ int64_t place[12];
-    const int h = blockIdx.x % A.view.heads, tile_all = blockIdx.x / A.view.heads;
-    const Place P = locate<kRows, true>(A, tile_all, false, place);
-    if (P.b >= A.view.B) return;
-    const Seq S = sequence<kRows>(A, P.b);
-    const int tile = tile_all - P.tiles_before;
-    const int64_t W = P.total < A.workgroups ? P.total : A.workgroups;
-    const int64_t ua = P.units_before + (static_cast<int64_t>(tile) * A.view.heads + h) * S.units;
-    const int64_t ub = ua + S.units;
-    // owner of unit u: the largest w with floor(w total / W) <= u
-    const int64_t w0 = ((ua + 1) * W - 1) / P.total, w1 = (ub * W - 1) / P.total;
-    if (w0 == w1) return;
-    const int rows = min(kRows, S.n * A.group - tile * kRows);
-    for (int x = threadIdx.x; x < rows * (D / 4); x += kBlockThreads) {
-        const int row = x / (D / 4), d = x % (D / 4) * 4;
-        float M = -kInf;
-        for (int64_t w = w0; w <= w1; ++w) {
-            const float* slot = A.part + (2 * w + (w * P.total / W >= ua ? 0 : 1)) * kSlotFloats<D, R>;
-            M = fmaxf(M, slot[kRows * D + row]);
-        }
-        if (M == -kInf) M = 0.0f;
+    constexpr int kQuads = D / 4;
+    __shared__ __align__(16) f32x4 sv[kBlockThreads];
+    __shared__ float sl[kBlockThreads], sm[kBlockThreads];
+    const int x = blockIdx.x / A.view.heads, h = blockIdx.x - x * A.view.heads;
+    const int4 own = A.owners[blockIdx.x];  // checked below before it is used
+    const int b = __builtin_amdgcn_readfirstlane(sequence_of_tile<kRows>(A, x));
+    const Seq S = sequence<kRows, false>(A, b);
+    const int tile = x - first_tile<kRows>(A, b);
+    if (tile < 0 || tile >= S.tiles) return;  // not an item: nobody wrote its owners
+    const int w0 = own.x, parts = own.y - own.x + 1;
+    if (parts == 1) return;
+    const int quads = min(kRows, S.n * A.group - tile * kRows) * kQuads;  // (row, 4 dimensions) pairs
+    const int shares = max(kBlockThreads / quads, 1);
+    for (int q0 = 0; q0 < quads; q0 += kBlockThreads) {
+        const int share = shares > 1 ? threadIdx.x / quads : 0;
+        const int q = shares > 1 ? threadIdx.x - share * quads : q0 + threadIdx.x;
+        const bool mine = share < shares && q < quads;
+        const int row = q / kQuads, d = q % kQuads * 4;
+        float M = -kInf, L = 0.0f;
         f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-        float L = 0.0f;
-        for (int64_t w = w0; w <= w1; ++w) {
-            const float* slot = A.part + (2 * w + (w * P.total / W >= ua ? 0 : 1)) * kSlotFloats<D, R>;
-            const float f = __builtin_amdgcn_exp2f(slot[kRows * D + row] - M);
-            L += slot[kRows * D + kRows + row] * f;
-            v += *reinterpret_cast<const f32x4*>(slot + row * D + d) * f;
+        if (mine) {
+            const int i0 = parts * share / shares, i1 = parts * (share + 1) / shares;
+            for (int i = i0; i < i1; ++i) {
+                const float* slot = A.part + (2 * static_cast<int64_t>(w0 + i) + (i == 0 ? own.z : 0)) * kSlotFloats<D, R>;
+                const float m = slot[kRows * D + row], l = slot[kRows * D + kRows + row];
+                const f32x4 o = *reinterpret_cast<const f32x4*>(slot + row * D + d);
+                const float mn = fmaxf(M, m), use = mn == -kInf ? 0.0f : mn;
+                const float fa = __builtin_amdgcn_exp2f(M - use), fb = __builtin_amdgcn_exp2f(m - use);
+                L = L * fa + l * fb;
+                v = v * fa + o * fb;
+                M = mn;
+            }
         }
-        v = L == 0.0f ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : v / L;
-        const int rho = tile * kRows + row, i = rho / A.group;
-        float* o = A.out + static_cast<int64_t>(S.first + i) * A.ldo +
-                   static_cast<int64_t>(h * A.group + rho - i * A.group) * D + d;
-        if (A.vec_o) {
-            *reinterpret_cast<f32x4*>(o) = v;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = v[e];
+        if (shares > 1) {
+            sv[threadIdx.x] = v;
+            sl[threadIdx.x] = L;
+            sm[threadIdx.x] = M;
+            __syncthreads();
+            if (!mine || share > 0) return;
+            for (int i = 1; i < shares; ++i) {
+                const int t = i * quads + q;
+                const float mn = fmaxf(M, sm[t]), use = mn == -kInf ? 0.0f : mn;
+                const float fa = __builtin_amdgcn_exp2f(M - use), fb = __builtin_amdgcn_exp2f(sm[t] - use);
+                L = L * fa + sl[t] * fb;
+                v = v * fa + sv[t] * fb;
+                M = mn;
+            }
         }
+        if (mine) store_row<D>(A, S, h, tile * kRows + row, d, v, L);
     }
 }
 
 // Everything about a call that depends on the descriptors' numbers.
 struct AttnPlan {
     int r = 1;             // 16-row tiles of a workgroup
-    int64_t tiles = 0;     // at most this many row tiles in the batch
-    int workgroups = 0;
-    bool split = true;     // units of 128 keys and a second kernel; else whole items
+    bool split = true;     // units of keys and a second kernel; else whole items
+    int unit_shift = kUnitShift;
+    int workgroups = 0;    // of the split
+    int64_t tiles = 0;     // numbers of row tiles (first_tile)
+    size_t part_bytes = 0, owner_bytes = 0;
 };
 
 constexpr int kRound = 512;  // workgroups of one round: two on each of 256 CUs
@@ -774,13 +864,20 @@ AttnPlan plan_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, int q_heads) {
     const int64_t group = q_heads / c.kv_heads;
     p.r = 1;
     const int64_t rows = 16 * p.r;
-    // sum over sequences of ceil(n group / rows), for any split of T rows
+    p.tiles = b.T * group / rows + b.B;
+    // the row tiles that there can be: sum of ceil(n group / rows) over the
+    // sequences, for any split of T rows
     const int64_t seqs = b.B < b.T ? b.B : b.T;
     const int64_t x = b.T * ((group + rows - 1) / rows), y = (b.T * group + seqs * (rows - 1)) / rows;
-    p.tiles = x < y ? x : y;
-    const int64_t items = p.tiles * c.kv_heads;
+    const int64_t items = (x < y ? x : y) * c.kv_heads;
     p.split = items < 2 * kRound;
-    p.workgroups = p.split ? kRound : static_cast<int>(items < (1 << 24) - 1 ? items : (1 << 24) - 1);
+    if (!p.split) return p;
+    p.workgroups = kRound;
+    // unit numbers fit 31 bits whatever the lengths
+    const int64_t keys = static_cast<int64_t>(b.max_pages) * c.page_size;
+    while (items * ((keys >> p.unit_shift) + 1) >= (int64_t{1} << 31)) ++p.unit_shift;
+    p.part_bytes = static_cast<size_t>(2 * p.workgroups) * static_cast<size_t>(16 * p.r * (c.head_dim + 2)) * sizeof(float);
+    p.owner_bytes = static_cast<size_t>(p.tiles * c.kv_heads) * sizeof(int4);
     return p;
 }
 
@@ -788,8 +885,7 @@ AttnPlan plan_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, int q_heads) {
 
 size_t attn_ws_bytes(const qmv_kv_cache& c, const qmv_kv_batch& b, int q_heads) {
     const AttnPlan p = plan_attn(c, b, q_heads);
-    if (!p.split) return 256;
-    return static_cast<size_t>(2 * p.workgroups) * static_cast<size_t>(16 * p.r * (c.head_dim + 2)) * sizeof(float);
+    return p.split ? p.part_bytes + p.owner_bytes : 256;
 }
 
 hipError_t launch_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, const float* q, int64_t ldq, float* out,
@@ -804,21 +900,27 @@ hipError_t launch_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, const float
     A.q = q;
     A.out = out;
     A.part = static_cast<float*>(ws);
+    A.owners = reinterpret_cast<int4*>(static_cast<char*>(ws) + p.part_bytes);
     A.ldq = ldq;
     A.ldo = ldo;
     A.group = q_heads / c.kv_heads;
     A.scale_log2 = (scale < 0.0f ? -scale : scale) * kLog2e;
     A.sign = scale < 0.0f ? -1.0f : 1.0f;
     A.window = window;
-    A.unit = p.split ? kUnit : INT32_MAX;
+    A.unit_shift = p.unit_shift;
     A.workgroups = p.workgroups;
     A.vec_q = (reinterpret_cast<uintptr_t>(q) & 15) == 0 && ldq % 4 == 0;
     A.vec_o = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && ldo % 4 == 0;
-    const dim3 grid(static_cast<unsigned>(p.workgroups)), join(static_cast<unsigned>(p.tiles * c.kv_heads));
-#define ATTN(D, F16, R)                                                                                     \
-    do {                                                                                                    \
-        hipLaunchKernelGGL((attn_kernel<D, F16, R>), grid, dim3(kBlockThreads), 0, stream, A);              \
-        if (p.split) hipLaunchKernelGGL((attn_join_kernel<D, R>), join, dim3(kBlockThreads), 0, stream, A); \
+    const dim3 items(static_cast<unsigned>(p.tiles * c.kv_heads));
+    const dim3 runs(static_cast<unsigned>(p.workgroups));
+#define ATTN(D, F16, R)                                                                                      \
+    do {                                                                                                     \
+        if (p.split) {                                                                                       \
+            hipLaunchKernelGGL((attn_kernel<D, F16, R, true>), runs, dim3(kBlockThreads), 0, stream, A);     \
+            hipLaunchKernelGGL((attn_join_kernel<D, R>), items, dim3(kBlockThreads), 0, stream, A);          \
+        } else {                                                                                             \
+            hipLaunchKernelGGL((attn_kernel<D, F16, R, false>), items, dim3(kBlockThreads), 0, stream, A);   \
+        }                                                                                                    \
     } while (0)
     if (c.format == QMV_KV_F16) {
         if (c.head_dim == 64) ATTN(64, true, 1);

@@ -34,7 +34,7 @@ int check_cache_shape(const qmv_kv_cache& c) {
 
 int check_batch_shape(const qmv_kv_cache& c, const qmv_kv_batch& b) {
     if (b.T < 1 || b.T > kMaxT || b.B < 1 || b.B > 65535 || b.max_pages < 1) return QMV_ERR_SHAPE;
-    if (static_cast<int64_t>(b.max_pages) * c.page_size > kMaxInt) return QMV_ERR_SHAPE;
+    if (static_cast<int64_t>(b.max_pages) * c.page_size > (int64_t{1} << 30)) return QMV_ERR_SHAPE;
     return QMV_OK;
 }
 

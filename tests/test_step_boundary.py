@@ -57,7 +57,7 @@ BAD_CACHE = [(dict(k=None), NUL), (dict(v=None), NUL), (dict(k_scale=None), NUL)
              (dict(k_scale=FAKE + 4), ALIGN), (dict(v_scale=FAKE + 8), ALIGN)]
 BAD_BATCH = [(dict(page_table=None), NUL), (dict(row_start=None), NUL), (dict(kv_len=None), NUL), (dict(T=0), SHAPE),
              (dict(T=-1), SHAPE), (dict(T=2 ** 24), SHAPE), (dict(B=0), SHAPE), (dict(B=65536), SHAPE),
-             (dict(max_pages=0), SHAPE), (dict(max_pages=2 ** 27), SHAPE), (dict(page_table=FAKE + 2), ALIGN),
+             (dict(max_pages=0), SHAPE), (dict(max_pages=2 ** 26 + 1), SHAPE), (dict(page_table=FAKE + 2), ALIGN),
              (dict(row_start=FAKE + 1), ALIGN), (dict(kv_len=FAKE + 2), ALIGN)]
 
 
