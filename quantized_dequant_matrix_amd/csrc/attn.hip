@@ -154,19 +154,20 @@ __device__ __forceinline__ int wave_scan(int v) {
     return v;
 }
 
-// Runs: `total` units in min(workgroups, total) runs whose lengths differ by
-// at most one, the longer ones first.
+// Runs: `total` units in as many runs as there are workgroups, or units if
+// these are fewer, run w from floor(w total / runs) on.  Where the runs are a
+// multiple of equally long items no run crosses from one item to the next.
 struct Runs {
-    int total, per, longer;
+    int total, runs, per, rest;
     __device__ __forceinline__ Runs(int total_, int workgroups)
-        : total(total_), per(static_cast<int>(static_cast<uint32_t>(total_) / static_cast<uint32_t>(workgroups))),
-          longer(total_ - per * workgroups) {}
-    __device__ __forceinline__ int start(int w) const { return w * per + min(w, longer); }
-    // the run that holds unit u
+        : total(total_), runs(max(min(workgroups, total_), 1)),
+          per(static_cast<int>(static_cast<uint32_t>(total_) / static_cast<uint32_t>(runs))), rest(total_ - per * runs) {}
+    __device__ __forceinline__ int start(int w) const {
+        return w * per + static_cast<int>(static_cast<uint32_t>(w * rest) / static_cast<uint32_t>(runs));
+    }
+    // the run that holds unit u: the largest w with floor(w total / runs) <= u
     __device__ __forceinline__ int owner(int u) const {
-        const int head = longer * (per + 1);
-        if (u < head) return static_cast<int>(static_cast<uint32_t>(u) / static_cast<uint32_t>(per + 1));
-        return longer + static_cast<int>(static_cast<uint32_t>(u - head) / static_cast<uint32_t>(per));
+        return static_cast<int>(((static_cast<int64_t>(u) + 1) * runs - 1) / total);
     }
 };
 
@@ -174,30 +175,27 @@ struct Place {
     int b;       // the sequence that holds the first unit of the run; B: no run
     int before;  // units of the sequences before it
     int total;   // units of the batch
+    Seq s;       // the sequence
 };
 
 // Units are numbered by sequence, row tile, head, position.  All 256 threads
 // sum the sequences' units, 256 sequences at a time.
 template <int ROWS>
-__device__ Place locate(const AttnArgs& A, int w, int* lds /* 6 */) {
+__device__ Place locate(const AttnArgs& A, int w, int* lds /* 5 */, Place* found) {
     const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave;
     const bool one = A.view.B <= kBlockThreads;
-    auto units = [&](int b) {
-        if (b >= A.view.B) return 0;
-        const Seq s = sequence<ROWS, true>(A, b);
-        return s.tiles * A.view.heads * s.units;
-    };
-    Place P;
-    P.total = 0;
-    P.b = A.view.B;
-    P.before = 0;
-    if (t == 0) lds[4] = A.view.B;
-    int scan = 0, mine = 0, key = 0;
+    int total = 0;
+    if (t == 0) found->b = A.view.B;
     for (int pass = one ? 1 : 0; pass < 2; ++pass) {  // the sum, then the place
         int base = 0;
         for (int b0 = 0; b0 < A.view.B; b0 += kBlockThreads) {
-            mine = units(b0 + t);
-            scan = wave_scan(mine);
+            Seq s = {};
+            int mine = 0;
+            if (b0 + t < A.view.B) {
+                s = sequence<ROWS, true>(A, b0 + t);
+                mine = s.tiles * A.view.heads * s.units;
+            }
+            const int scan = wave_scan(mine);
             __syncthreads();
             if (lane == kWave - 1) lds[wave] = scan;
             __syncthreads();
@@ -207,20 +205,21 @@ __device__ Place locate(const AttnArgs& A, int w, int* lds /* 6 */) {
                 base += lds[i];
             }
             if (pass == 0) continue;
-            if (one) P.total = base;
-            const Runs R(P.total, A.workgroups);
-            key = R.start(w) < R.start(w + 1) ? R.start(w) : -1;
+            if (one) total = base;
+            const Runs R(total, A.workgroups);
+            const int key = w < R.runs ? R.start(w) : -1;
             const int begin = before + scan - mine;
-            if (key >= begin && key < begin + mine) {
-                lds[4] = b0 + t;
-                lds[5] = begin;
-            }
+            if (key >= begin && key < begin + mine) *found = Place{b0 + t, begin, total, s};
         }
-        if (pass == 0) P.total = base;
+        if (pass == 0) total = base;
     }
     __syncthreads();
-    P.b = lds[4];
-    if (P.b < A.view.B) P.before = lds[5];
+    Place P;
+    int* to = reinterpret_cast<int*>(&P);
+    const int* from = reinterpret_cast<const int*>(found);
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(Place) / sizeof(int)); ++i)
+        to[i] = __builtin_amdgcn_readfirstlane(from[i]);
     return P;
 }
 
@@ -335,12 +334,19 @@ struct Rows {
     float lim[R];  // ... and the largest scale it is good for
 };
 
-// q of row rho: 16 (8 for float16) dimensions at a time as the lane's B
-// operand takes them: dimension 64 s + 16 g + byte (32 s + 8 g + e).
+// q of the lane's rows, 16 (8 for float16) dimensions at a time as the
+// lane's B operand takes them: dimension 64 s + 16 g + byte (32 s + 8 g + e).
 template <int D, bool F16, int R>
-__device__ __forceinline__ void load_rows(const AttnArgs& A, const Seq& S, int tile, int h, Rows<D, F16, R>& W) {
-    using T = Rows<D, F16, R>;
-    constexpr int kPer = F16 ? 8 : 16;
+struct Queries {
+    static constexpr int kPer = F16 ? 8 : 16;
+    static constexpr int kQ = Rows<D, F16, R>::kQ;
+    float x[R][kQ][kPer];
+    int pos[R];
+};
+
+template <int D, bool F16, int R>
+__device__ __forceinline__ void fetch_queries(const AttnArgs& A, const Seq& S, int tile, int h, Queries<D, F16, R>& Q) {
+    constexpr int kPer = Queries<D, F16, R>::kPer;
     const int lane = threadIdx.x & (kWave - 1), n = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -348,31 +354,44 @@ __device__ __forceinline__ void load_rows(const AttnArgs& A, const Seq& S, int t
         const bool real = rho < S.n * A.group;
         const int i = real ? rho / A.group : 0;
         const int head = h * A.group + (real ? rho - i * A.group : 0);
-        W.pos[r] = real ? S.base + i : -1;
+        Q.pos[r] = real ? S.base + i : INT32_MIN;
         const float* src = A.q + static_cast<int64_t>(S.first + i) * A.ldq + static_cast<int64_t>(head) * D;
-        float x[T::kQ][kPer];
-        float amax = 0.0f;
-        bool broken = false;
 #pragma unroll
-        for (int s = 0; s < T::kQ; ++s) {
+        for (int s = 0; s < Queries<D, F16, R>::kQ; ++s) {
             const float* p = src + s * (4 * kPer) + g * kPer;
             if (A.vec_q) {
 #pragma unroll
                 for (int e = 0; e < kPer; e += 4) {
                     const float4 f = *reinterpret_cast<const float4*>(p + e);
-                    x[s][e] = f.x; x[s][e + 1] = f.y; x[s][e + 2] = f.z; x[s][e + 3] = f.w;
+                    Q.x[r][s][e] = f.x; Q.x[r][s][e + 1] = f.y; Q.x[r][s][e + 2] = f.z; Q.x[r][s][e + 3] = f.w;
                 }
             } else {
 #pragma unroll
-                for (int e = 0; e < kPer; ++e) x[s][e] = p[e];
+                for (int e = 0; e < kPer; ++e) Q.x[r][s][e] = p[e];
             }
+        }
+    }
+}
+
+template <int D, bool F16, int R>
+__device__ __forceinline__ void prepare_rows(const AttnArgs& A, Queries<D, F16, R>& Q, Rows<D, F16, R>& W) {
+    using T = Rows<D, F16, R>;
+    constexpr int kPer = Queries<D, F16, R>::kPer;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const bool real = Q.pos[r] != INT32_MIN;
+        W.pos[r] = real ? Q.pos[r] : -1;
+        float(&x)[T::kQ][kPer] = Q.x[r];
+        float amax = 0.0f;
+        bool broken = false;
+#pragma unroll
+        for (int s = 0; s < T::kQ; ++s)
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
                 if (!real) x[s][e] = 0.0f;
                 amax = fmaxf(amax, fabsf(x[s][e]));
                 broken |= !(fabsf(x[s][e]) < kInf);
             }
-        }
         amax = row_max(amax);
         // whole row scaled by a power of two first: amax in [1/2, 1)
         int k = 0;
@@ -631,7 +650,8 @@ void attn_kernel(AttnArgs A) {
     constexpr int kPad = D + 4;
     __shared__ __align__(16) float so[kWavesPerBlock * 16 * kPad];
     __shared__ float sm[kWavesPerBlock][kRows], sl[kWavesPerBlock][kRows];
-    __shared__ int place[6];
+    __shared__ int sums[kWavesPerBlock];
+    __shared__ Place place;
     const int lane = threadIdx.x & (kWave - 1), n = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int w = blockIdx.x;
@@ -639,15 +659,15 @@ void attn_kernel(AttnArgs A) {
     int tile = 0, h = 0, c0 = 0, c1 = 1;  // the piece: units c0 .. c1 - 1 of an item
     Seq S;
     if constexpr (SPLIT) {
-        const Place P = locate<kRows>(A, w, place);
-        b = __builtin_amdgcn_readfirstlane(P.b);
+        const Place P = locate<kRows>(A, w, sums, &place);
+        b = P.b;
         if (b >= A.view.B) return;  // no run
-        before = __builtin_amdgcn_readfirstlane(P.before);
-        total = __builtin_amdgcn_readfirstlane(P.total);
+        before = P.before;
+        total = P.total;
+        S = P.s;
         const Runs runs(total, A.workgroups);
         u = runs.start(w);
         u_end = runs.start(w + 1);
-        S = sequence<kRows, true>(A, b);
     } else {
         // items in order of tile, heads fastest: workgroups w and w + 8 (one
         // XCD) work on the same few heads' keys
@@ -682,6 +702,9 @@ void attn_kernel(AttnArgs A) {
             u = u_end;
         }
 
+        // the queries first: their parts are formed while the first keys come
+        Queries<D, F16, R> queries;
+        fetch_queries<D, F16, R>(A, S, tile, h, queries);
         // positions of the item's rows: tokens i0 .. i1
         const int i0 = tile * kRows / A.group;
         const int i1 = (min((tile + 1) * kRows, S.n * A.group) - 1) / A.group;
@@ -711,7 +734,7 @@ void attn_kernel(AttnArgs A) {
             load_values<D, F16>(A, pg, kv);
         }
         Rows<D, F16, R> rows;
-        load_rows<D, F16, R>(A, S, tile, h, rows);
+        prepare_rows<D, F16, R>(A, queries, rows);
         if (any) {
             Pages pn = pages_of(A, b, h, end - key > kStep ? key + kStep : key);
             for (;;) {
@@ -788,62 +811,59 @@ void attn_kernel(AttnArgs A) {
     }
 }
 
-// Joins the parts of every item that more than one workgroup worked on, in
-// order of position: one workgroup a (row tile, head).  The threads that a
-// few rows leave idle share the parts among them.
-template <int D, int R>
+// Joins the parts of every item that more than one workgroup worked on:
+// blockIdx.x is an item (row tile, head), every kJoinRows-th of its rows from
+// blockIdx.y on is this workgroup's.  D / 4 threads hold a row's dimensions,
+// 1024 / D groups of them share the parts.
+constexpr int kJoinRows = 4;
+
+template <int D>
 __global__ __launch_bounds__(kBlockThreads)
 void attn_join_kernel(AttnArgs A) {
-    constexpr int kRows = 16 * R;
+    constexpr int kRows = 16, R = 1;
     constexpr int kQuads = D / 4;
-    __shared__ __align__(16) f32x4 sv[kBlockThreads];
-    __shared__ float sl[kBlockThreads], sm[kBlockThreads];
+    constexpr int kShares = kBlockThreads / kQuads;
+    __shared__ __align__(16) f32x4 sv[kShares][kQuads];
+    __shared__ float sl[kShares], sm[kShares];
     const int x = blockIdx.x / A.view.heads, h = blockIdx.x - x * A.view.heads;
-    const int4 own = A.owners[blockIdx.x];  // checked below before it is used
+    const int4 own = A.owners[blockIdx.x];  // used only if x is an item's number
     const int b = __builtin_amdgcn_readfirstlane(sequence_of_tile<kRows>(A, x));
     const Seq S = sequence<kRows, false>(A, b);
     const int tile = x - first_tile<kRows>(A, b);
-    if (tile < 0 || tile >= S.tiles) return;  // not an item: nobody wrote its owners
+    if (tile < 0 || tile >= S.tiles) return;
     const int w0 = own.x, parts = own.y - own.x + 1;
     if (parts == 1) return;
-    const int quads = min(kRows, S.n * A.group - tile * kRows) * kQuads;  // (row, 4 dimensions) pairs
-    const int shares = max(kBlockThreads / quads, 1);
-    for (int q0 = 0; q0 < quads; q0 += kBlockThreads) {
-        const int share = shares > 1 ? threadIdx.x / quads : 0;
-        const int q = shares > 1 ? threadIdx.x - share * quads : q0 + threadIdx.x;
-        const bool mine = share < shares && q < quads;
-        const int row = q / kQuads, d = q % kQuads * 4;
+    const int rows = min(kRows, S.n * A.group - tile * kRows);
+    const int share = threadIdx.x / kQuads, quad = threadIdx.x % kQuads;
+    const int i0 = parts * share / kShares, i1 = parts * (share + 1) / kShares;
+    for (int row = blockIdx.y; row < rows; row += kJoinRows) {
         float M = -kInf, L = 0.0f;
         f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (mine) {
-            const int i0 = parts * share / shares, i1 = parts * (share + 1) / shares;
-            for (int i = i0; i < i1; ++i) {
-                const float* slot = A.part + (2 * static_cast<int64_t>(w0 + i) + (i == 0 ? own.z : 0)) * kSlotFloats<D, R>;
-                const float m = slot[kRows * D + row], l = slot[kRows * D + kRows + row];
-                const f32x4 o = *reinterpret_cast<const f32x4*>(slot + row * D + d);
-                const float mn = fmaxf(M, m), use = mn == -kInf ? 0.0f : mn;
-                const float fa = __builtin_amdgcn_exp2f(M - use), fb = __builtin_amdgcn_exp2f(m - use);
-                L = L * fa + l * fb;
-                v = v * fa + o * fb;
-                M = mn;
-            }
+        auto add = [&](float m, float l, f32x4 o) {
+            const float mn = fmaxf(M, m), use = mn == -kInf ? 0.0f : mn;
+            const float fa = __builtin_amdgcn_exp2f(M - use), fb = __builtin_amdgcn_exp2f(m - use);
+            L = L * fa + l * fb;
+            v = v * fa + o * fb;
+            M = mn;
+        };
+#pragma unroll 2
+        for (int i = i0; i < i1; ++i) {
+            const float* slot = A.part + (2 * static_cast<int64_t>(w0 + i) + (i == 0 ? own.z : 0)) * kSlotFloats<D, R>;
+            add(slot[kRows * D + row], slot[kRows * D + kRows + row],
+                *reinterpret_cast<const f32x4*>(slot + row * D + 4 * quad));
         }
-        if (shares > 1) {
-            sv[threadIdx.x] = v;
-            sl[threadIdx.x] = L;
-            sm[threadIdx.x] = M;
-            __syncthreads();
-            if (!mine || share > 0) return;
-            for (int i = 1; i < shares; ++i) {
-                const int t = i * quads + q;
-                const float mn = fmaxf(M, sm[t]), use = mn == -kInf ? 0.0f : mn;
-                const float fa = __builtin_amdgcn_exp2f(M - use), fb = __builtin_amdgcn_exp2f(sm[t] - use);
-                L = L * fa + sl[t] * fb;
-                v = v * fa + sv[t] * fb;
-                M = mn;
-            }
+        sv[share][quad] = v;
+        if (quad == 0) {
+            sl[share] = L;
+            sm[share] = M;
         }
-        if (mine) store_row<D>(A, S, h, tile * kRows + row, d, v, L);
+        __syncthreads();
+        if (share == 0) {
+#pragma unroll
+            for (int i = 1; i < kShares; ++i) add(sm[i], sl[i], sv[i][quad]);
+            store_row<D>(A, S, h, tile * kRows + row, 4 * quad, v, L);
+        }
+        __syncthreads();
     }
 }
 
@@ -857,26 +877,39 @@ struct AttnPlan {
     size_t part_bytes = 0, owner_bytes = 0;
 };
 
-constexpr int kRound = 512;  // workgroups of one round: two on each of 256 CUs
+// Workgroups of one round: two on each of 256 CUs, one where the registers
+// allow no more.
+constexpr int kRound = 512, kRoundWide = 256;
 
 AttnPlan plan_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, int q_heads) {
     AttnPlan p;
     const int64_t group = q_heads / c.kv_heads;
-    p.r = 1;
-    const int64_t rows = 16 * p.r;
-    p.tiles = b.T * group / rows + b.B;
-    // the row tiles that there can be: sum of ceil(n group / rows) over the
-    // sequences, for any split of T rows
     const int64_t seqs = b.B < b.T ? b.B : b.T;
-    const int64_t x = b.T * ((group + rows - 1) / rows), y = (b.T * group + seqs * (rows - 1)) / rows;
-    const int64_t items = (x < y ? x : y) * c.kv_heads;
-    p.split = items < 2 * kRound;
-    if (!p.split) return p;
-    p.workgroups = kRound;
+    // the items that there can be with `rows` rows a tile: sum of
+    // ceil(n group / rows) over the sequences, for any split of T rows
+    auto items_of = [&](int64_t rows) {
+        const int64_t x = b.T * ((group + rows - 1) / rows), y = (b.T * group + seqs * (rows - 1)) / rows;
+        return (x < y ? x : y) * c.kv_heads;
+    };
+    const int round = c.head_dim == 256 ? kRoundWide : kRound;
+    int64_t items = items_of(16);
+    p.split = items < 2 * round;
+    if (!p.split) {
+        // Two row tiles share the keys' and values' loads and conversions.
+        // Two prompts of 1024 new tokens over 6000, 8 heads of 128: 275 us
+        // against 376 us (float16: 309 against 517); 64 wide 129 against
+        // 126 us, 256 wide 176 against 130 us (registers), and with fewer
+        // items than a round (256 new tokens of one prompt) no difference.
+        p.r = c.head_dim == 128 && items_of(32) >= kRound && b.T * group >= 64 * seqs ? 2 : 1;
+        p.tiles = b.T * group / (16 * p.r) + b.B;
+        return p;
+    }
+    p.tiles = b.T * group / 16 + b.B;
+    p.workgroups = round;
     // unit numbers fit 31 bits whatever the lengths
     const int64_t keys = static_cast<int64_t>(b.max_pages) * c.page_size;
     while (items * ((keys >> p.unit_shift) + 1) >= (int64_t{1} << 31)) ++p.unit_shift;
-    p.part_bytes = static_cast<size_t>(2 * p.workgroups) * static_cast<size_t>(16 * p.r * (c.head_dim + 2)) * sizeof(float);
+    p.part_bytes = static_cast<size_t>(2 * p.workgroups) * static_cast<size_t>(16 * (c.head_dim + 2)) * sizeof(float);
     p.owner_bytes = static_cast<size_t>(p.tiles * c.kv_heads) * sizeof(int4);
     return p;
 }
@@ -913,23 +946,25 @@ hipError_t launch_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, const float
     A.vec_o = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && ldo % 4 == 0;
     const dim3 items(static_cast<unsigned>(p.tiles * c.kv_heads));
     const dim3 runs(static_cast<unsigned>(p.workgroups));
-#define ATTN(D, F16, R)                                                                                      \
-    do {                                                                                                     \
-        if (p.split) {                                                                                       \
-            hipLaunchKernelGGL((attn_kernel<D, F16, R, true>), runs, dim3(kBlockThreads), 0, stream, A);     \
-            hipLaunchKernelGGL((attn_join_kernel<D, R>), items, dim3(kBlockThreads), 0, stream, A);          \
-        } else {                                                                                             \
-            hipLaunchKernelGGL((attn_kernel<D, F16, R, false>), items, dim3(kBlockThreads), 0, stream, A);   \
-        }                                                                                                    \
+#define ATTN(D, F16)                                                                                                 \
+    do {                                                                                                             \
+        if (p.split) {                                                                                               \
+            hipLaunchKernelGGL((attn_kernel<D, F16, 1, true>), runs, dim3(kBlockThreads), 0, stream, A);             \
+            hipLaunchKernelGGL((attn_join_kernel<D>), dim3(items.x, kJoinRows), dim3(kBlockThreads), 0, stream, A);  \
+        } else if (D == 128 && p.r == 2) {                                                                           \
+            hipLaunchKernelGGL((attn_kernel<128, F16, 2, false>), items, dim3(kBlockThreads), 0, stream, A);         \
+        } else {                                                                                                     \
+            hipLaunchKernelGGL((attn_kernel<D, F16, 1, false>), items, dim3(kBlockThreads), 0, stream, A);           \
+        }                                                                                                            \
     } while (0)
     if (c.format == QMV_KV_F16) {
-        if (c.head_dim == 64) ATTN(64, true, 1);
-        else if (c.head_dim == 128) ATTN(128, true, 1);
-        else ATTN(256, true, 1);
+        if (c.head_dim == 64) ATTN(64, true);
+        else if (c.head_dim == 128) ATTN(128, true);
+        else ATTN(256, true);
     } else {
-        if (c.head_dim == 64) ATTN(64, false, 1);
-        else if (c.head_dim == 128) ATTN(128, false, 1);
-        else ATTN(256, false, 1);
+        if (c.head_dim == 64) ATTN(64, false);
+        else if (c.head_dim == 128) ATTN(128, false);
+        else ATTN(256, false);
     }
     return hipGetLastError();
 }
