@@ -232,6 +232,14 @@ __device__ __forceinline__ float row_sum(float v) {
     return v + __shfl_xor(v, 32, kWave);
 }
 
+// v_max3_f32 as it is: fmaxf of values the compiler cannot trace to an
+// arithmetic result adds an instruction an operand to quiet NaNs.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t pk(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
 }
@@ -330,8 +338,8 @@ struct Rows {
     f32x4 o[R][D / 16];
     float m[R];    // running maximum, before qs
     float l[R];    // this lane's share of the sum
-    float c[R];    // 8-bit values: factor of the value scales
-    float lim[R];  // ... and the largest scale it is good for
+    float lc[R];   // 8-bit values: log2 of the power of two in every p
+    uint32_t lim[R];  // ... and the largest value scale it is good for, as bits
 };
 
 // q of the lane's rows, 16 (8 for float16) dimensions at a time as the
@@ -452,8 +460,8 @@ __device__ __forceinline__ void prepare_rows(const AttnArgs& A, Queries<D, F16, 
         }
         W.m[r] = -kInf;
         W.l[r] = 0.0f;
-        W.c[r] = 1.0f;
-        W.lim[r] = 0.0f;
+        W.lc[r] = 0.0f;
+        W.lim[r] = 0;
 #pragma unroll
         for (int t = 0; t < D / 16; ++t) W.o[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
@@ -548,11 +556,12 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
                 }
             }
         }
-        float top = fmaxf(fmaxf(fmaxf(s[r][0], s[r][1]), fmaxf(s[r][2], s[r][3])),
-                          fmaxf(fmaxf(s[r][4], s[r][5]), fmaxf(s[r][6], s[r][7])));
-        float big = 0.0f;
+        float top = fmaxf(max3(s[r][0], s[r][1], max3(s[r][2], s[r][3], s[r][4])), max3(s[r][5], s[r][6], s[r][7]));
+        // scales are never negative: they compare as their bits (NaN above all)
+        uint32_t big = 0;
         if constexpr (!F16) {
-            big = fmaxf(fmaxf(fmaxf(dv[0], dv[1]), fmaxf(dv[2], dv[3])), fmaxf(fmaxf(dv[4], dv[5]), fmaxf(dv[6], dv[7])));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) big = max(big, __float_as_uint(dv[e]));
         }
         // The maximum and the factor of the value scales move only when a
         // row has outgrown them: p and its products stay within float16.
@@ -560,32 +569,32 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
         if (__ballot(grow) != 0) {
             top = row_max(top);
             const float mn = fmaxf(W.m[r], top);
-            const float alpha = W.m[r] == -kInf ? 0.0f : __builtin_amdgcn_exp2f((W.m[r] - mn) * W.qs[r]);
-            float f = alpha;
+            float alpha = W.m[r] == -kInf ? 0.0f : __builtin_amdgcn_exp2f((W.m[r] - mn) * W.qs[r]);
             if constexpr (!F16) {
-                big = row_max(big);
+                big = max(big, static_cast<uint32_t>(__shfl_xor(static_cast<int>(big), 16, kWave)));
+                big = max(big, static_cast<uint32_t>(__shfl_xor(static_cast<int>(big), 32, kWave)));
                 if (big > W.lim[r]) {
-                    // c = 2^10 / 2^floor(log2 big); good up to four times that power
-                    const int e = static_cast<int>(__float_as_uint(big) >> 23);
-                    const int ce = min(max(264 - e, 1), 254);
-                    const float c = __uint_as_float(static_cast<uint32_t>(ce) << 23);
-                    f *= W.lim[r] == 0.0f ? 1.0f : c / W.c[r];
-                    W.c[r] = c;
-                    W.lim[r] = __uint_as_float(static_cast<uint32_t>(min(max(e, 1) + 2, 254)) << 23);
+                    // factor 2^10 / 2^floor(log2 big), good up to four times that power
+                    const int e = static_cast<int>(big >> 23);
+                    const float lc = static_cast<float>(min(max(137 - e, -117), 127));
+                    alpha *= W.lim[r] == 0 ? 1.0f : __builtin_amdgcn_exp2f(lc - W.lc[r]);
+                    W.lc[r] = lc;
+                    W.lim[r] = static_cast<uint32_t>(min(max(e, 1) + 2, 254)) << 23;
                 }
             }
             W.m[r] = mn;
             W.l[r] *= alpha;
 #pragma unroll
-            for (int t = 0; t < D / 16; ++t) W.o[r][t] *= f;
+            for (int t = 0; t < D / 16; ++t) W.o[r][t] *= alpha;
         }
-        const float mq = W.m[r] == -kInf ? 0.0f : W.m[r] * W.qs[r];
+        // p, with the factor in it
+        const float shift = (W.m[r] == -kInf ? 0.0f : W.m[r] * W.qs[r]) - (F16 ? 10.0f : W.lc[r]);
         float p[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            p[e] = __builtin_amdgcn_exp2f(fmaf(s[r][e], W.qs[r], -mq));
+            p[e] = __builtin_amdgcn_exp2f(fmaf(s[r][e], W.qs[r], -shift));
             W.l[r] += p[e];
-            p[e] *= F16 ? 1024.0f : dv[e] * W.c[r];
+            if constexpr (!F16) p[e] *= dv[e];
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -756,7 +765,7 @@ void attn_kernel(AttnArgs A) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             mq[r] = rows.m[r] == -kInf ? -kInf : rows.m[r] * rows.qs[r];
-            float l = row_sum(rows.l[r]);
+            float l = row_sum(rows.l[r]) * __builtin_amdgcn_exp2f(F16 ? -10.0f : -rows.lc[r]);
             if (rows.broken[r] && rows.m[r] != -kInf) l = __uint_as_float(0x7fc00000u);
             if (g == 0) {
                 sm[wave][16 * r + n] = mq[r];
@@ -771,8 +780,8 @@ void attn_kernel(AttnArgs A) {
             float M = -kInf;
 #pragma unroll
             for (int i = 0; i < kWavesPerBlock; ++i) M = fmaxf(M, sm[i][16 * r + n]);
-            const float f = __builtin_amdgcn_exp2f(mq[r] - (M == -kInf ? 0.0f : M)) *
-                            (F16 ? 1.0f / 1024.0f : 512.0f / rows.c[r]);
+            const float f = __builtin_amdgcn_exp2f(mq[r] - (M == -kInf ? 0.0f : M) - (F16 ? 10.0f : rows.lc[r])) *
+                            (F16 ? 1.0f : 512.0f);
             float* dst = so + (wave * 16 + n) * kPad + 4 * g * (D / 16);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
