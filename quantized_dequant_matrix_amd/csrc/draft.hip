@@ -10,13 +10,14 @@
 // (gfx950's float64 FMA rate equals its float32 rate without packing), and
 // neither the order of a sum nor the split over workgroups changes a token.
 //
-// Three launches:
+// Three launches, chunks of 8192 logits, groups of 1024:
 //   stats  one workgroup per (chunk of a row, row, sequence): maximum and sum
 //          of weights of the chunk.  Reads every logit once: this is the
 //          traffic.
 //   pick   one workgroup per (chunk, sequence): joins the rows' chunks, makes
-//          the accept tests, and sums its chunk of the row to draw from.
-//   draw   one workgroup a sequence: the chunk that holds the drawn point,
+//          the accept tests, and sums the groups of its chunk of the row to
+//          draw from, a wave each.
+//   draw   one workgroup a sequence: the group that holds the drawn point,
 //          then the element.
 #include <stdint.h>
 
@@ -27,31 +28,50 @@
 namespace qmv {
 namespace {
 
-constexpr int kChunk = 4096;                          // logits of one workgroup
-constexpr int kPer = kChunk / kBlockThreads;          // 16 a thread
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kChunk = 8192;                // logits of one workgroup
+constexpr int kPer = kChunk / kThreads;     // 16 a thread
+constexpr int kGroup = kChunk / kWaves;     // 1024: a wave's part of a chunk
+constexpr int kGroupPer = kGroup / kThreads; // 2 a thread
+constexpr int kMaxRows = 2 * 64 + 1;        // rows of a sequence: G + 1 target rows, G draft rows
 constexpr double kLog2e = 1.4426950408889634074;
 constexpr float kNegInf = -__builtin_inff();
 
-// 2^t for t <= 0 (also for t somewhat above): t = n + f with n whole and
-// |f| <= 1/2, 2^f by its Taylor series (ln 2)^k / k! up to k = 11, whose next
-// term is below 7e-15 of the result.  -infinity gives 0.
+// 2^(j / 64), j < 64, in LDS: filled by the first wave of a workgroup before
+// its first barrier.
+__shared__ double exp_table[kWave];
+
+__device__ __forceinline__ void fill_exp_table() {
+    if (threadIdx.x < kWave) {
+        // (ln 2 / 64) j by the series up to the 17th power: below 2^-54 left
+        const double x = static_cast<double>(threadIdx.x) * (0.69314718055994530942 / 64.0);
+        double p = 1.0;
+#pragma unroll
+        for (int k = 17; k >= 1; --k) p = fma(p * x, 1.0 / k, 1.0);
+        exp_table[threadIdx.x] = p;
+    }
+}
+
+// 2^t for t <= 64: t = n + j / 64 + f, |f| <= 1/128, with n + j / 64 rounded
+// off by an addition of 1.5 2^46 (whose last place is 1/64), 2^(j / 64) from
+// the table and 2^f by its series up to the 5th power, whose next term is
+// below 4e-17.  Below 2^-1020 the result is 0 (the row's maximum is 2^0).
 __device__ __forceinline__ double exp2_f64(double t) {
-    t = fmax(t, -1100.0);
-    const double n = rint(t);
-    const double f = (t - n) * 0.69314718055994530942;
-    double p = 1.0 / 39916800.0;
-    p = fma(p, f, 1.0 / 3628800.0);
-    p = fma(p, f, 1.0 / 362880.0);
-    p = fma(p, f, 1.0 / 40320.0);
-    p = fma(p, f, 1.0 / 5040.0);
-    p = fma(p, f, 1.0 / 720.0);
-    p = fma(p, f, 1.0 / 120.0);
-    p = fma(p, f, 1.0 / 24.0);
+    const bool none = t < -1020.0;
+    t = fmax(t, -1020.0);
+    constexpr double kShift = 105553116266496.0;
+    const double r = t + kShift;
+    const int k = static_cast<int>(__builtin_bit_cast(uint64_t, r));  // 64 n + j
+    const double f = (t - (r - kShift)) * 0.69314718055994530942;
+    double p = fma(f, 1.0 / 120.0, 1.0 / 24.0);
     p = fma(p, f, 1.0 / 6.0);
     p = fma(p, f, 0.5);
     p = fma(p, f, 1.0);
-    p = fma(p, f, 1.0);
-    return ldexp(p, static_cast<int>(n));
+    const double e = exp_table[k & 63];
+    const uint64_t v = __builtin_bit_cast(uint64_t, fma(p * f, e, e));
+    const double x = __builtin_bit_cast(double, v + (static_cast<uint64_t>(static_cast<uint32_t>(k >> 6) << 20) << 32));
+    return none ? 0.0 : x;
 }
 
 // 1 / x for x in [1, 2^200]: the hardware's estimate and two Newton steps.
@@ -62,16 +82,17 @@ __device__ __forceinline__ double rcp_f64(double x) {
 }
 
 struct Weights {
-    double cap;    // softcap, 0: none
+    double cap;    // softcap / temperature in units of log2, 0: none
     double k;      // log2(e) / temperature
     double twice;  // 2 log2(e) / softcap
-    // cap(y) in units of log2: the exponent of a weight up to the row's maximum
+    // cap(y) / temperature in units of log2: the exponent of a weight up to
+    // the row's maximum.  Logits are bounded: y k stays finite.
     __device__ __forceinline__ double level(float y) const {
         const double v = static_cast<double>(y);
         if (cap == 0.0) return v * k;
         // tanh z = 1 - 2 / (1 + e^(2 z)); beyond |z| = 20 it is +-1 in 64 bits
         const double e = exp2_f64(fmin(fmax(v * twice, -64.0), 64.0));
-        return (1.0 - 2.0 * rcp_f64(1.0 + e)) * (cap * k);
+        return fma(-2.0, rcp_f64(1.0 + e), 1.0) * cap;
     }
     // weight relative to the level `top` of the row's (or chunk's) maximum
     __device__ __forceinline__ double weight(float y, double top) const {
@@ -88,13 +109,22 @@ struct Stat {
     float pad;
 };
 
+// What the draw of a sequence looks at.
+struct Pick {
+    double p_level, p_inv, q_level, q_inv;  // levels of the rows' maxima, 1 / sums (0: no weight)
+    int accepted;
+    int residual;  // the row is one of the drafts' (else the bonus row)
+};
+
 struct DraftView {
     DraftArgs a;
     Weights w;
-    int chunks;
-    Stat* stats;       // [B][2 G + 1][chunks]: target rows 0 .. G, then draft rows
-    double* rest;      // [B][chunks]: sums of max(p - q, 0) (or of p for the bonus row)
-    double* whole;     // [B][chunks]: sums of p
+    int chunks, groups;  // groups = chunks * kWaves
+    bool vec;      // rows of logits are 16-byte aligned
+    Stat* stats;   // [B][2 G + 1][chunks]: target rows 0 .. G, then draft rows
+    double* rest;  // [B][groups]: sums of max(p - q, 0) (of p for the bonus row)
+    double* whole; // [B][groups]: sums of p
+    Pick* picks;   // [B]
     __device__ __forceinline__ int drafts(int64_t b) const {
         const int n = a.n_draft ? a.n_draft[b] : a.G;
         return n < 0 ? 0 : (n > a.G ? a.G : n);
@@ -104,55 +134,99 @@ struct DraftView {
     }
 };
 
+// A double of another lane (0 where the pattern has none).
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ double dpp_f64(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, ROW_MASK, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, ROW_MASK, 0xF, false);
+    return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+}
+
+__device__ __forceinline__ double lane_f64(double v, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), lane);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), lane);
+    return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+}
+
+// Inclusive sum over the lanes, in lane order: within rows of 16 lanes
+// (row_shr 1, 2, 4, 8), then across them (row_bcast 15 and 31).
+__device__ __forceinline__ double wave_prefix(double v) {
+    v += dpp_f64<0x111, 0xF>(v);
+    v += dpp_f64<0x112, 0xF>(v);
+    v += dpp_f64<0x114, 0xF>(v);
+    v += dpp_f64<0x118, 0xF>(v);
+    v += dpp_f64<0x142, 0xA>(v);
+    v += dpp_f64<0x143, 0xC>(v);
+    return v;
+}
+
+__device__ __forceinline__ double wave_add(double v) { return lane_f64(wave_prefix(v), kWave - 1); }
+
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ float dpp_max(float v) {
+    const int bits = __builtin_bit_cast(int, v);
+    return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(bits, bits, CTRL, ROW_MASK, 0xF, false)));
+}
+
 __device__ __forceinline__ float wave_max(float v) {
-    for (int o = kWave / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, kWave));
-    return v;
+    v = dpp_max<0x111, 0xF>(v);
+    v = dpp_max<0x112, 0xF>(v);
+    v = dpp_max<0x114, 0xF>(v);
+    v = dpp_max<0x118, 0xF>(v);
+    v = dpp_max<0x142, 0xA>(v);
+    v = dpp_max<0x143, 0xC>(v);
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), kWave - 1));
 }
 
-__device__ __forceinline__ double wave_add(double v) {
-    for (int o = kWave / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
-    return v;
-}
-
-__device__ __forceinline__ double block_add(double v, double* lds) {
-    v = wave_add(v);
-    if ((threadIdx.x & (kWave - 1)) == 0) lds[threadIdx.x / kWave] = v;
-    __syncthreads();
-    double s = 0.0;
+// 16 logits of the wave's group of a chunk, 4 by 4 across the wave (a sum's
+// order is free); past the row's end: no weight.
+__device__ __forceinline__ void load_spread(const DraftView& D, const float* y, int c, float (&v)[kPer]) {
+    const int64_t base = static_cast<int64_t>(c) * kChunk + threadIdx.x / kWave * kGroup + 4 * (threadIdx.x & (kWave - 1));
 #pragma unroll
-    for (int i = 0; i < kWavesPerBlock; ++i) s += lds[i];
-    return s;
+    for (int i = 0; i < kPer / 4; ++i) {
+        const int64_t at = base + i * 4 * kWave;
+        if (D.vec && at + 4 <= D.a.V) {
+            const float4 f = *reinterpret_cast<const float4*>(y + at);
+            v[4 * i] = clean(f.x); v[4 * i + 1] = clean(f.y); v[4 * i + 2] = clean(f.z); v[4 * i + 3] = clean(f.w);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * i + e] = at + e < D.a.V ? clean(y[at + e]) : kNegInf;
+        }
+    }
 }
 
-__global__ __launch_bounds__(kBlockThreads)
+__global__ __launch_bounds__(kThreads)
 void draft_stats_kernel(DraftView D) {
-    __shared__ float mx[kWavesPerBlock];
-    __shared__ double sm[kWavesPerBlock];
+    __shared__ float mx[kWaves];
+    __shared__ double sm[kWaves];
     const int c = blockIdx.x, r = blockIdx.y;
     const int64_t b = blockIdx.z;
     const int n = D.drafts(b);
     if (r <= D.a.G ? r > n : r - D.a.G - 1 >= n) return;  // a row that no draft uses
-    const float* y = D.row(b, r);
-    const int64_t base = static_cast<int64_t>(c) * kChunk + threadIdx.x;
     float v[kPer];
+    load_spread(D, D.row(b, r), c, v);
+    fill_exp_table();
     float top = kNegInf;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int64_t at = base + i * kBlockThreads;
-        v[i] = at < D.a.V ? clean(y[at]) : kNegInf;
-        top = fmaxf(top, v[i]);
-    }
+    for (int i = 0; i < kPer; ++i) top = fmaxf(top, v[i]);
     top = wave_max(top);
     if ((threadIdx.x & (kWave - 1)) == 0) mx[threadIdx.x / kWave] = top;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kWavesPerBlock; ++i) top = fmaxf(top, mx[i]);
+    for (int i = 0; i < kWaves; ++i) top = fmaxf(top, mx[i]);
     const double level = D.w.level(top);
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) sum += D.w.weight(v[i], level);
-    sum = block_add(sum, sm);
+    sum = wave_add(sum);
+    if ((threadIdx.x & (kWave - 1)) == 0) sm[threadIdx.x / kWave] = sum;
+    __syncthreads();
     if (threadIdx.x == 0) {
+        sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) sum += sm[i];
         Stat* s = D.stats + (b * (2 * D.a.G + 1) + r) * D.chunks + c;
         s->sum = sum;
         s->top = top;
@@ -163,177 +237,199 @@ void draft_stats_kernel(DraftView D) {
 __device__ __forceinline__ void join_row(const DraftView& D, int64_t b, int r, double* level, double* sum) {
     const Stat* s = D.stats + (b * (2 * D.a.G + 1) + r) * D.chunks;
     const int lane = threadIdx.x & (kWave - 1);
-    float top = kNegInf;
-    for (int c = lane; c < D.chunks; c += kWave) top = fmaxf(top, s[c].top);
+    Stat first = {0.0, kNegInf, 0.0f};  // a wave's worth of chunks stays in registers
+    if (lane < D.chunks) first = s[lane];
+    float top = first.top;
+    for (int c = lane + kWave; c < D.chunks; c += kWave) top = fmaxf(top, s[c].top);
     top = wave_max(top);
     *level = D.w.level(top);
-    double z = 0.0;
-    for (int c = lane; c < D.chunks; c += kWave)
+    double z = first.top != kNegInf ? first.sum * exp2_f64(D.w.level(first.top) - *level) : 0.0;
+    for (int c = lane + kWave; c < D.chunks; c += kWave)
         if (s[c].top != kNegInf) z += s[c].sum * exp2_f64(D.w.level(s[c].top) - *level);
     *sum = wave_add(z);
 }
 
-__device__ __forceinline__ double probability(const DraftView& D, float y, double level, double sum) {
-    return sum > 0.0 ? D.w.weight(clean(y), level) / sum : 0.0;
-}
+__device__ __forceinline__ double inverse(double sum) { return sum > 0.0 ? 1.0 / sum : 0.0; }
 
-// What the draw of a sequence looks at.
-struct Pick {
-    double p_level, p_sum, q_level, q_sum;
-    int accepted;
-    int residual;
-};
-
-__device__ void pick_row(const DraftView& D, int64_t b, Pick* lds, int* yes) {
+__global__ __launch_bounds__(kThreads)
+void draft_pick_kernel(DraftView D) {
+    __shared__ double levels[kMaxRows], inverses[kMaxRows];
+    __shared__ Pick P;
+    const int c = blockIdx.x;
+    const int64_t b = blockIdx.y;
     const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
     const int n = D.drafts(b), G = D.a.G;
-    for (int i = wave; i < n; i += kWavesPerBlock) {
-        double pl, ps, ql, qs;
-        join_row(D, b, i, &pl, &ps);
-        join_row(D, b, G + 1 + i, &ql, &qs);
-        const int t = D.a.draft_tokens[b * G + i];
-        bool ok = false;
-        if (t >= 0 && t < D.a.V) {
-            const double p = probability(D, D.row(b, i)[t], pl, ps);
-            const double q = probability(D, D.row(b, G + 1 + i)[t], ql, qs);
-            ok = static_cast<double>(D.a.u[b * (G + 1) + i]) * q < p;
+    // the drafted tokens' logits, by the wave that tests them
+    float yp = kNegInf, yq = kNegInf, u = 0.0f;
+    bool real = false;
+    if (wave == 0 && lane < n) {
+        const int t = D.a.draft_tokens[b * G + lane];
+        u = D.a.u[b * (G + 1) + lane];
+        real = t >= 0 && t < D.a.V;
+        if (real) {
+            yp = clean(D.row(b, lane)[t]);
+            yq = clean(D.row(b, G + 1 + lane)[t]);
         }
-        if (lane == 0) yes[i] = ok;
+    }
+    fill_exp_table();
+    __syncthreads();
+    for (int i = wave; i < 2 * n + 1; i += kWaves) {
+        const int r = i <= n ? i : G + i - n;  // target rows 0 .. n, draft rows G + 1 ..
+        double level, sum;
+        join_row(D, b, r, &level, &sum);
+        if (lane == 0) {
+            levels[r] = level;
+            inverses[r] = inverse(sum);
+        }
     }
     __syncthreads();
     if (wave == 0) {
-        const bool no = lane < n && !yes[lane < n ? lane : 0];
+        bool no = false;
+        if (lane < n) {
+            const double p = D.w.weight(yp, levels[lane]) * inverses[lane];
+            const double q = D.w.weight(yq, levels[G + 1 + lane]) * inverses[G + 1 + lane];
+            no = !(real && static_cast<double>(u) * q < p);
+        }
         const uint64_t nos = __ballot(no);
         const int a = nos ? __ffsll(static_cast<unsigned long long>(nos)) - 1 : n;
-        Pick P;
-        P.accepted = a;
-        P.residual = a < n;
-        join_row(D, b, a, &P.p_level, &P.p_sum);
-        P.q_level = P.q_sum = 0.0;
-        if (a < n) join_row(D, b, G + 1 + a, &P.q_level, &P.q_sum);
-        if (lane == 0) *lds = P;
+        if (lane == 0) {
+            P.accepted = a;
+            P.residual = a < n;
+            P.p_level = levels[a];
+            P.p_inv = inverses[a];
+            P.q_level = a < n ? levels[G + 1 + a] : 0.0;
+            P.q_inv = a < n ? inverses[G + 1 + a] : 0.0;
+            if (c == 0) D.picks[b] = P;
+        }
     }
     __syncthreads();
-}
-
-// Weights of 16 consecutive logits of the row to draw from: thread t of the
-// workgroup has elements 16 t .. 16 t + 15 of the chunk.  rest: max(p - q, 0)
-// (p for the bonus row), whole: p.
-__device__ __forceinline__ void weights_of(const DraftView& D, int64_t b, int c, const Pick& P, double (&rest)[kPer],
-                                           double (&whole)[kPer]) {
-    const float* yp = D.row(b, P.accepted);
-    const float* yq = P.residual ? D.row(b, D.a.G + 1 + P.accepted) : yp;
-    const int64_t base = static_cast<int64_t>(c) * kChunk + threadIdx.x * kPer;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int64_t at = base + i;
-        double p = 0.0, q = 0.0;
-        if (at < D.a.V) {
-            p = probability(D, yp[at], P.p_level, P.p_sum);
-            if (P.residual) q = probability(D, yq[at], P.q_level, P.q_sum);
-        }
-        whole[i] = p;
-        rest[i] = fmax(p - q, 0.0);
-    }
-}
-
-__global__ __launch_bounds__(kBlockThreads)
-void draft_pick_kernel(DraftView D) {
-    __shared__ Pick P;
-    __shared__ int yes[64];
-    __shared__ double sa[kWavesPerBlock], sb[kWavesPerBlock];
-    const int c = blockIdx.x;
-    const int64_t b = blockIdx.y;
-    pick_row(D, b, &P, yes);
-    double rest[kPer], whole[kPer];
-    weights_of(D, b, c, P, rest, whole);
+    float vp[kPer], vq[kPer];
+    load_spread(D, D.row(b, P.accepted), c, vp);
     double x = 0.0, y = 0.0;
+    if (P.residual) {
+        load_spread(D, D.row(b, G + 1 + P.accepted), c, vq);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        x += rest[i];
-        y += whole[i];
+        for (int i = 0; i < kPer; ++i) {
+            const double p = D.w.weight(vp[i], P.p_level) * P.p_inv;
+            y += p;
+            x += fmax(p - D.w.weight(vq[i], P.q_level) * P.q_inv, 0.0);
+        }
+        x = wave_add(x);
+        y = wave_add(y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) x += D.w.weight(vp[i], P.p_level) * P.p_inv;
+        x = y = wave_add(x);
     }
-    x = block_add(x, sa);
-    y = block_add(y, sb);
-    if (threadIdx.x == 0) {
-        D.rest[b * D.chunks + c] = x;
-        D.whole[b * D.chunks + c] = y;
+    if (lane == 0) {
+        D.rest[b * D.groups + c * kWaves + wave] = x;
+        D.whole[b * D.groups + c * kWaves + wave] = y;
     }
 }
 
-__global__ __launch_bounds__(kBlockThreads)
-void draft_draw_kernel(DraftView D) {
-    __shared__ Pick P;
-    __shared__ int yes[64];
-    __shared__ double scan[kBlockThreads];
-    __shared__ int found, last;
-    const int64_t b = blockIdx.x;
-    const int t = threadIdx.x, G = D.a.G;
-    pick_row(D, b, &P, yes);
-    // the chunk, by one thread: the running sum in index order
-    __shared__ int chunk, from_whole;
-    __shared__ double target, before;
-    if (t == 0) {
-        double total = 0.0;
-        for (int c = 0; c < D.chunks; ++c) total += D.rest[b * D.chunks + c];
-        from_whole = !(total > 0.0);
-        const double* s = from_whole ? D.whole + b * D.chunks : D.rest + b * D.chunks;
-        if (from_whole) {
-            total = 0.0;
-            for (int c = 0; c < D.chunks; ++c) total += s[c];
-        }
-        target = static_cast<double>(D.a.u[b * (G + 1) + G]) * total;
-        double run = 0.0;
-        chunk = -1;
-        before = 0.0;
-        for (int c = 0; c < D.chunks; ++c) {
-            if (s[c] > 0.0) {
-                chunk = c;  // the last chunk with weight, should none pass the point
-                before = run;
-                if (run + s[c] > target) break;
-            }
-            run += s[c];
-        }
-        found = kChunk;
-        last = -1;
+// The group that holds the drawn point, by one wave: the first whose running
+// sum exceeds u times the whole sum, or the last with any weight (-1: none
+// has).  A lane sums `per` consecutive groups, the wave their sums; then the
+// lane with the point goes through its own.
+__device__ __forceinline__ int find_group(const double* s, int groups, double u, double* target, double* before) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int per = (groups + kWave - 1) / kWave;
+    const int g0 = min(lane * per, groups), g1 = min(g0 + per, groups);
+    double mine = 0.0;
+    int tail = -1;
+    for (int g = g0; g < g1; ++g) {
+        mine += s[g];
+        if (s[g] > 0.0) tail = g;
     }
+    const double upto = wave_prefix(mine);
+    *target = u * lane_f64(upto, kWave - 1);
+    int hit = -1;
+    double run = upto - mine, from = run;
+    for (int g = g0; g < g1 && hit < 0; ++g) {
+        from = run;
+        run += s[g];
+        if (s[g] > 0.0 && run > *target) hit = g;
+    }
+    uint64_t lanes = __ballot(hit >= 0);
+    if (lanes == 0) {  // the point lies at the very end: the last group with weight
+        hit = tail;
+        lanes = __ballot(tail >= 0);
+        if (lanes == 0) return -1;
+        lanes = uint64_t{1} << (63 - __clzll(static_cast<long long>(lanes)));
+        from = run;
+        if (tail >= 0)
+            for (int g = g1 - 1; g >= tail; --g) from -= s[g];
+    }
+    const int at = __ffsll(static_cast<unsigned long long>(lanes)) - 1;
+    *before = lane_f64(from, at);
+    return __builtin_amdgcn_readlane(hit, at);
+}
+
+__global__ __launch_bounds__(kThreads)
+void draft_draw_kernel(DraftView D) {
+    __shared__ double sums[kWaves];
+    __shared__ int found, last, group, from_whole;
+    __shared__ double target, before;
+    const int64_t b = blockIdx.x;
+    const int t = threadIdx.x, wave = t / kWave, lane = t & (kWave - 1), G = D.a.G;
+    const Pick P = D.picks[b];
+    if (wave == 0) {
+        const double u = static_cast<double>(D.a.u[b * (G + 1) + G]);
+        double to, from;
+        int g = find_group(D.rest + b * D.groups, D.groups, u, &to, &from);
+        const bool all = g < 0;  // no rest anywhere: from p itself
+        if (all) g = find_group(D.whole + b * D.groups, D.groups, u, &to, &from);
+        if (lane == 0) {
+            group = g;
+            from_whole = all;
+            target = to;
+            before = from;
+            found = kGroup;
+            last = -1;
+        }
+    }
+    fill_exp_table();
     __syncthreads();
     int token = -1;
-    if (chunk >= 0) {
-        double rest[kPer], whole[kPer];
-        weights_of(D, b, chunk, P, rest, whole);
+    if (group >= 0) {
+        // thread t has elements 2 t and 2 t + 1 of the group
+        const float* yp = D.row(b, P.accepted);
+        const bool minus = P.residual && !from_whole;
+        const float* yq = minus ? D.row(b, G + 1 + P.accepted) : yp;
+        const int64_t base = static_cast<int64_t>(group) * kGroup + t * kGroupPer;
+        double w[kGroupPer];
         double mine = 0.0;
         int tail = -1;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            if (from_whole) rest[i] = whole[i];
-            mine += rest[i];
-            if (rest[i] > 0.0) tail = t * kPer + i;
+        for (int i = 0; i < kGroupPer; ++i) {
+            w[i] = 0.0;
+            if (base + i < D.a.V) {
+                w[i] = D.w.weight(clean(yp[base + i]), P.p_level) * P.p_inv;
+                if (minus) w[i] = fmax(w[i] - D.w.weight(clean(yq[base + i]), P.q_level) * P.q_inv, 0.0);
+            }
+            mine += w[i];
+            if (w[i] > 0.0) tail = t * kGroupPer + i;
         }
-        scan[t] = mine;
+        const double upto = wave_prefix(mine);
+        if (lane == kWave - 1) sums[wave] = upto;
         __syncthreads();
-        for (int o = 1; o < kBlockThreads; o <<= 1) {
-            const double v = t >= o ? scan[t - o] : 0.0;
-            __syncthreads();
-            scan[t] += v;
-            __syncthreads();
-        }
-        double run = before + (t ? scan[t - 1] : 0.0);
-        int hit = kChunk;
+        double run = before + (upto - mine);
+        for (int i = 0; i < wave; ++i) run += sums[i];
+        int hit = kGroup;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            run += rest[i];
-            if (hit == kChunk && rest[i] > 0.0 && run > target) hit = t * kPer + i;
+        for (int i = 0; i < kGroupPer; ++i) {
+            run += w[i];
+            if (hit == kGroup && w[i] > 0.0 && run > target) hit = t * kGroupPer + i;
         }
-        if (hit < kChunk) atomicMin(&found, hit);
+        if (hit < kGroup) atomicMin(&found, hit);
         if (tail >= 0) atomicMax(&last, tail);
         __syncthreads();
-        const int at = found < kChunk ? found : last;
-        token = at < 0 ? -1 : static_cast<int>(static_cast<int64_t>(chunk) * kChunk + at);
+        const int at = found < kGroup ? found : last;
+        token = at < 0 ? -1 : static_cast<int>(static_cast<int64_t>(group) * kGroup + at);
     }
     const int a = P.accepted;
     if (t == 0) D.a.accepted[b] = a;
-    for (int i = t; i <= G; i += kBlockThreads)
+    for (int i = t; i <= G; i += kThreads)
         D.a.tokens[b * (G + 1) + i] = i < a ? D.a.draft_tokens[b * G + i] : (i == a ? token : -1);
 }
 
@@ -344,31 +440,37 @@ size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
 size_t draft_ws_bytes(int64_t B, int G, int64_t V) {
     const size_t n = static_cast<size_t>(B) * static_cast<size_t>(chunks_of(V));
-    return align256(n * static_cast<size_t>(2 * G + 1) * sizeof(Stat)) + 2 * align256(n * sizeof(double));
+    return align256(n * static_cast<size_t>(2 * G + 1) * sizeof(Stat)) + 2 * align256(n * kWaves * sizeof(double)) +
+           align256(static_cast<size_t>(B) * sizeof(Pick));
 }
 
 hipError_t launch_draft_verify(const DraftArgs& a, void* ws, hipStream_t stream) {
     DraftView D;
     D.a = a;
-    D.w.cap = a.softcap;
     D.w.k = kLog2e / static_cast<double>(a.temperature);
+    D.w.cap = static_cast<double>(a.softcap) * D.w.k;
     D.w.twice = a.softcap > 0.0f ? 2.0 * kLog2e / static_cast<double>(a.softcap) : 0.0;
     D.chunks = static_cast<int>(chunks_of(a.V));
+    D.groups = D.chunks * kWaves;
     const size_t n = static_cast<size_t>(a.B) * static_cast<size_t>(D.chunks);
     char* p = static_cast<char*>(ws);
     D.stats = reinterpret_cast<Stat*>(p);
     p += align256(n * static_cast<size_t>(2 * a.G + 1) * sizeof(Stat));
     D.rest = reinterpret_cast<double*>(p);
-    D.whole = reinterpret_cast<double*>(p + align256(n * sizeof(double)));
+    p += align256(n * kWaves * sizeof(double));
+    D.whole = reinterpret_cast<double*>(p);
+    D.picks = reinterpret_cast<Pick*>(p + align256(n * kWaves * sizeof(double)));
+    D.vec = ((reinterpret_cast<uintptr_t>(a.target) | reinterpret_cast<uintptr_t>(a.draft)) & 15) == 0 &&
+            a.ldt % 4 == 0 && a.ldd % 4 == 0;
     const unsigned ch = static_cast<unsigned>(D.chunks), B = static_cast<unsigned>(a.B);
-    hipLaunchKernelGGL(draft_stats_kernel, dim3(ch, static_cast<unsigned>(2 * a.G + 1), B), dim3(kBlockThreads), 0,
+    hipLaunchKernelGGL(draft_stats_kernel, dim3(ch, static_cast<unsigned>(2 * a.G + 1), B), dim3(kThreads), 0,
                        stream, D);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(draft_pick_kernel, dim3(ch, B), dim3(kBlockThreads), 0, stream, D);
+    hipLaunchKernelGGL(draft_pick_kernel, dim3(ch, B), dim3(kThreads), 0, stream, D);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(draft_draw_kernel, dim3(B), dim3(kBlockThreads), 0, stream, D);
+    hipLaunchKernelGGL(draft_draw_kernel, dim3(B), dim3(kThreads), 0, stream, D);
     return hipGetLastError();
 }
 
