@@ -87,16 +87,24 @@ struct Weights {
     double twice;  // 2 log2(e) / softcap
     // cap(y) / temperature in units of log2: the exponent of a weight up to
     // the row's maximum.  Logits are bounded: y k stays finite.
+    template <bool CAP>
     __device__ __forceinline__ double level(float y) const {
+#pragma clang fp contract(off)
+        // (the product is rounded as the row's own level was: the difference
+        // of the largest logit to it is 0, however large both are)
         const double v = static_cast<double>(y);
-        if (cap == 0.0) return v * k;
+        if constexpr (!CAP) return v * k;
         // tanh z = 1 - 2 / (1 + e^(2 z)); beyond |z| = 20 it is +-1 in 64 bits
         const double e = exp2_f64(fmin(fmax(v * twice, -64.0), 64.0));
         return fma(-2.0, rcp_f64(1.0 + e), 1.0) * cap;
     }
-    // weight relative to the level `top` of the row's (or chunk's) maximum
+    // weight relative to the level `top` of the row's (or chunk's) maximum;
+    // no branches, so that a thread's weights overlap
+    template <bool CAP>
     __device__ __forceinline__ double weight(float y, double top) const {
-        return y == kNegInf ? 0.0 : exp2_f64(level(y) - top);
+#pragma clang fp contract(off)
+        const double w = exp2_f64(level<CAP>(y) - top);
+        return y == kNegInf ? 0.0 : w;
     }
 };
 
@@ -184,19 +192,29 @@ __device__ __forceinline__ float wave_max(float v) {
 // order is free); past the row's end: no weight.
 __device__ __forceinline__ void load_spread(const DraftView& D, const float* y, int c, float (&v)[kPer]) {
     const int64_t base = static_cast<int64_t>(c) * kChunk + threadIdx.x / kWave * kGroup + 4 * (threadIdx.x & (kWave - 1));
+    if (D.vec && (c + 1) * static_cast<int64_t>(kChunk) <= D.a.V) {  // all loads first
+        float4 f[kPer / 4];
 #pragma unroll
-    for (int i = 0; i < kPer / 4; ++i) {
-        const int64_t at = base + i * 4 * kWave;
-        if (D.vec && at + 4 <= D.a.V) {
-            const float4 f = *reinterpret_cast<const float4*>(y + at);
-            v[4 * i] = clean(f.x); v[4 * i + 1] = clean(f.y); v[4 * i + 2] = clean(f.z); v[4 * i + 3] = clean(f.w);
-        } else {
+        for (int i = 0; i < kPer / 4; ++i) f[i] = *reinterpret_cast<const float4*>(y + base + i * 4 * kWave);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[4 * i + e] = at + e < D.a.V ? clean(y[at + e]) : kNegInf;
+        for (int i = 0; i < kPer / 4; ++i) {
+            v[4 * i] = clean(f[i].x); v[4 * i + 1] = clean(f[i].y); v[4 * i + 2] = clean(f[i].z); v[4 * i + 3] = clean(f[i].w);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {  // past the end: the last one again, then taken out
+            const int64_t at = base + i / 4 * 4 * kWave + i % 4;
+            v[i] = y[at < D.a.V ? at : D.a.V - 1];
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int64_t at = base + i / 4 * 4 * kWave + i % 4;
+            v[i] = at < D.a.V ? clean(v[i]) : kNegInf;
         }
     }
 }
 
+template <bool CAP>
 __global__ __launch_bounds__(kThreads)
 void draft_stats_kernel(DraftView D) {
     __shared__ float mx[kWaves];
@@ -216,10 +234,10 @@ void draft_stats_kernel(DraftView D) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) top = fmaxf(top, mx[i]);
-    const double level = D.w.level(top);
+    const double level = D.w.template level<CAP>(top);
     double sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) sum += D.w.weight(v[i], level);
+    for (int i = 0; i < kPer; ++i) sum += D.w.template weight<CAP>(v[i], level);
     sum = wave_add(sum);
     if ((threadIdx.x & (kWave - 1)) == 0) sm[threadIdx.x / kWave] = sum;
     __syncthreads();
@@ -234,6 +252,7 @@ void draft_stats_kernel(DraftView D) {
 }
 
 // The level of a row's maximum and its sum of weights, joined by one wave.
+template <bool CAP>
 __device__ __forceinline__ void join_row(const DraftView& D, int64_t b, int r, double* level, double* sum) {
     const Stat* s = D.stats + (b * (2 * D.a.G + 1) + r) * D.chunks;
     const int lane = threadIdx.x & (kWave - 1);
@@ -242,15 +261,16 @@ __device__ __forceinline__ void join_row(const DraftView& D, int64_t b, int r, d
     float top = first.top;
     for (int c = lane + kWave; c < D.chunks; c += kWave) top = fmaxf(top, s[c].top);
     top = wave_max(top);
-    *level = D.w.level(top);
-    double z = first.top != kNegInf ? first.sum * exp2_f64(D.w.level(first.top) - *level) : 0.0;
+    *level = D.w.template level<CAP>(top);
+    double z = first.top != kNegInf ? first.sum * exp2_f64(D.w.template level<CAP>(first.top) - *level) : 0.0;
     for (int c = lane + kWave; c < D.chunks; c += kWave)
-        if (s[c].top != kNegInf) z += s[c].sum * exp2_f64(D.w.level(s[c].top) - *level);
+        if (s[c].top != kNegInf) z += s[c].sum * exp2_f64(D.w.template level<CAP>(s[c].top) - *level);
     *sum = wave_add(z);
 }
 
 __device__ __forceinline__ double inverse(double sum) { return sum > 0.0 ? 1.0 / sum : 0.0; }
 
+template <bool CAP>
 __global__ __launch_bounds__(kThreads)
 void draft_pick_kernel(DraftView D) {
     __shared__ double levels[kMaxRows], inverses[kMaxRows];
@@ -276,7 +296,7 @@ void draft_pick_kernel(DraftView D) {
     for (int i = wave; i < 2 * n + 1; i += kWaves) {
         const int r = i <= n ? i : G + i - n;  // target rows 0 .. n, draft rows G + 1 ..
         double level, sum;
-        join_row(D, b, r, &level, &sum);
+        join_row<CAP>(D, b, r, &level, &sum);
         if (lane == 0) {
             levels[r] = level;
             inverses[r] = inverse(sum);
@@ -286,8 +306,8 @@ void draft_pick_kernel(DraftView D) {
     if (wave == 0) {
         bool no = false;
         if (lane < n) {
-            const double p = D.w.weight(yp, levels[lane]) * inverses[lane];
-            const double q = D.w.weight(yq, levels[G + 1 + lane]) * inverses[G + 1 + lane];
+            const double p = D.w.template weight<CAP>(yp, levels[lane]) * inverses[lane];
+            const double q = D.w.template weight<CAP>(yq, levels[G + 1 + lane]) * inverses[G + 1 + lane];
             no = !(real && static_cast<double>(u) * q < p);
         }
         const uint64_t nos = __ballot(no);
@@ -310,15 +330,15 @@ void draft_pick_kernel(DraftView D) {
         load_spread(D, D.row(b, G + 1 + P.accepted), c, vq);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const double p = D.w.weight(vp[i], P.p_level) * P.p_inv;
+            const double p = D.w.template weight<CAP>(vp[i], P.p_level) * P.p_inv;
             y += p;
-            x += fmax(p - D.w.weight(vq[i], P.q_level) * P.q_inv, 0.0);
+            x += fmax(p - D.w.template weight<CAP>(vq[i], P.q_level) * P.q_inv, 0.0);
         }
         x = wave_add(x);
         y = wave_add(y);
     } else {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) x += D.w.weight(vp[i], P.p_level) * P.p_inv;
+        for (int i = 0; i < kPer; ++i) x += D.w.template weight<CAP>(vp[i], P.p_level) * P.p_inv;
         x = y = wave_add(x);
     }
     if (lane == 0) {
@@ -365,6 +385,7 @@ __device__ __forceinline__ int find_group(const double* s, int groups, double u,
     return __builtin_amdgcn_readlane(hit, at);
 }
 
+template <bool CAP>
 __global__ __launch_bounds__(kThreads)
 void draft_draw_kernel(DraftView D) {
     __shared__ double sums[kWaves];
@@ -404,8 +425,8 @@ void draft_draw_kernel(DraftView D) {
         for (int i = 0; i < kGroupPer; ++i) {
             w[i] = 0.0;
             if (base + i < D.a.V) {
-                w[i] = D.w.weight(clean(yp[base + i]), P.p_level) * P.p_inv;
-                if (minus) w[i] = fmax(w[i] - D.w.weight(clean(yq[base + i]), P.q_level) * P.q_inv, 0.0);
+                w[i] = D.w.template weight<CAP>(clean(yp[base + i]), P.p_level) * P.p_inv;
+                if (minus) w[i] = fmax(w[i] - D.w.template weight<CAP>(clean(yq[base + i]), P.q_level) * P.q_inv, 0.0);
             }
             mine += w[i];
             if (w[i] > 0.0) tail = t * kGroupPer + i;
@@ -434,6 +455,21 @@ void draft_draw_kernel(DraftView D) {
 }
 
 int64_t chunks_of(int64_t V) { return (V + kChunk - 1) / kChunk; }
+
+template <bool CAP>
+hipError_t launch_draft(const DraftView& D, hipStream_t stream) {
+    const unsigned ch = static_cast<unsigned>(D.chunks), B = static_cast<unsigned>(D.a.B);
+    hipLaunchKernelGGL(draft_stats_kernel<CAP>, dim3(ch, static_cast<unsigned>(2 * D.a.G + 1), B), dim3(kThreads), 0,
+                       stream, D);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(draft_pick_kernel<CAP>, dim3(ch, B), dim3(kThreads), 0, stream, D);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(draft_draw_kernel<CAP>, dim3(B), dim3(kThreads), 0, stream, D);
+    return hipGetLastError();
+}
+
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
@@ -462,16 +498,7 @@ hipError_t launch_draft_verify(const DraftArgs& a, void* ws, hipStream_t stream)
     D.picks = reinterpret_cast<Pick*>(p + align256(n * kWaves * sizeof(double)));
     D.vec = ((reinterpret_cast<uintptr_t>(a.target) | reinterpret_cast<uintptr_t>(a.draft)) & 15) == 0 &&
             a.ldt % 4 == 0 && a.ldd % 4 == 0;
-    const unsigned ch = static_cast<unsigned>(D.chunks), B = static_cast<unsigned>(a.B);
-    hipLaunchKernelGGL(draft_stats_kernel, dim3(ch, static_cast<unsigned>(2 * a.G + 1), B), dim3(kThreads), 0,
-                       stream, D);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(draft_pick_kernel, dim3(ch, B), dim3(kThreads), 0, stream, D);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(draft_draw_kernel, dim3(B), dim3(kThreads), 0, stream, D);
-    return hipGetLastError();
+    return a.softcap > 0.0f ? launch_draft<true>(D, stream) : launch_draft<false>(D, stream);
 }
 
 }  // namespace qmv
