@@ -10,13 +10,13 @@
 // (gfx950's float64 FMA rate equals its float32 rate without packing), and
 // neither the order of a sum nor the split over workgroups changes a token.
 //
-// Three launches, chunks of 8192 logits, groups of 1024:
-//   stats  one workgroup per (chunk of a row, row, sequence): maximum and sum
-//          of weights of the chunk.  Reads every logit once: this is the
-//          traffic.
-//   pick   one workgroup per (chunk, sequence): joins the rows' chunks, makes
-//          the accept tests, and sums the groups of its chunk of the row to
-//          draw from, a wave each.
+// Three launches:
+//   stats  one workgroup per (chunk of 4096 logits, row, sequence): maximum
+//          and sum of weights of the chunk.  Reads every logit once: this is
+//          the traffic.
+//   pick   one workgroup per (part, sequence): joins the rows' chunks, makes
+//          the accept tests, and sums groups of 256 weights of the row to draw
+//          from, a wave each.  A part is 2048 logits or a few times that.
 //   draw   one workgroup a sequence: the group that holds the drawn point,
 //          then the element.
 #include <stdint.h>
@@ -28,24 +28,24 @@
 namespace qmv {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / kWave;
-constexpr int kChunk = 8192;                // logits of one workgroup
-constexpr int kPer = kChunk / kThreads;     // 16 a thread
-constexpr int kGroup = kChunk / kWaves;     // 1024: a wave's part of a chunk
-constexpr int kGroupPer = kGroup / kThreads; // 2 a thread
+constexpr int kStatThreads = 256, kStatWaves = kStatThreads / kWave;
+constexpr int kChunk = 4096;                     // logits of a workgroup of the stats kernel
+constexpr int kPickThreads = 512, kPickWaves = kPickThreads / kWave;
+constexpr int kStep = 2048;                      // logits of one step of a workgroup of the pick kernel
+constexpr int kGroup = kStep / kPickWaves;       // 256: a wave's share of a step
+constexpr int kDrawThreads = kGroup, kDrawWaves = kDrawThreads / kWave;
 constexpr int kMaxRows = 2 * 64 + 1;        // rows of a sequence: G + 1 target rows, G draft rows
 constexpr double kLog2e = 1.4426950408889634074;
 constexpr float kNegInf = -__builtin_inff();
 
-// 2^(j / 64), j < 64, in LDS: filled by the first wave of a workgroup before
-// its first barrier.
-__shared__ double exp_table[kWave];
+// 2^(j / 256), j < 256, in LDS: filled by the first 256 threads of a
+// workgroup before its first barrier.
+__shared__ double exp_table[256];
 
 __device__ __forceinline__ void fill_exp_table() {
-    if (threadIdx.x < kWave) {
-        // (ln 2 / 64) j by the series up to the 17th power: below 2^-54 left
-        const double x = static_cast<double>(threadIdx.x) * (0.69314718055994530942 / 64.0);
+    if (threadIdx.x < 256) {
+        // (ln 2 / 256) j by the series up to the 17th power: below 2^-54 left
+        const double x = static_cast<double>(threadIdx.x) * (0.69314718055994530942 / 256.0);
         double p = 1.0;
 #pragma unroll
         for (int k = 17; k >= 1; --k) p = fma(p * x, 1.0 / k, 1.0);
@@ -53,24 +53,25 @@ __device__ __forceinline__ void fill_exp_table() {
     }
 }
 
-// 2^t for t <= 64: t = n + j / 64 + f, |f| <= 1/128, with n + j / 64 rounded
-// off by an addition of 1.5 2^46 (whose last place is 1/64), 2^(j / 64) from
-// the table and 2^f by its series up to the 5th power, whose next term is
-// below 4e-17.  Below 2^-1020 the result is 0 (the row's maximum is 2^0).
-__device__ __forceinline__ double exp2_f64(double t) {
-    const bool none = t < -1020.0;
+// 2^t for t <= 64: t = n + j / 256 + f, |f| <= 1/512, with n + j / 256
+// rounded off by an addition of 1.5 2^44 (whose last place is 1/256),
+// 2^(j / 256) from the table and 2^f by its series up to the third power,
+// whose next term is below 2e-13.  Below 2^-1020 the result is 0 (the row's
+// maximum is 2^0).  About 23 instructions a weight with the sum, no branch: with
+// 31 (a longer series, a table of 64) the sums of 371 MB of logits took 104 us,
+// now 81-90.
+__device__ __forceinline__ double exp2_f64(double t, bool none = false) {
+    none |= t < -1020.0;
     t = fmax(t, -1020.0);
-    constexpr double kShift = 105553116266496.0;
+    constexpr double kShift = 26388279066624.0, kLn2 = 0.69314718055994530942;
     const double r = t + kShift;
-    const int k = static_cast<int>(__builtin_bit_cast(uint64_t, r));  // 64 n + j
-    const double f = (t - (r - kShift)) * 0.69314718055994530942;
-    double p = fma(f, 1.0 / 120.0, 1.0 / 24.0);
-    p = fma(p, f, 1.0 / 6.0);
-    p = fma(p, f, 0.5);
-    p = fma(p, f, 1.0);
-    const double e = exp_table[k & 63];
-    const uint64_t v = __builtin_bit_cast(uint64_t, fma(p * f, e, e));
-    const double x = __builtin_bit_cast(double, v + (static_cast<uint64_t>(static_cast<uint32_t>(k >> 6) << 20) << 32));
+    const uint32_t k = static_cast<uint32_t>(__builtin_bit_cast(uint64_t, r));  // 256 n + j
+    const double f = t - (r - kShift);
+    const double q = fma(fma(kLn2 * kLn2 * kLn2 / 6.0, f, kLn2 * kLn2 / 2.0), f, kLn2);
+    const double e = exp_table[k & 255u];
+    const uint64_t v = __builtin_bit_cast(uint64_t, fma(q * f, e, e));
+    const uint32_t hi = static_cast<uint32_t>(v >> 32) + ((k & ~255u) << 12);
+    const double x = __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | static_cast<uint32_t>(v));
     return none ? 0.0 : x;
 }
 
@@ -103,13 +104,18 @@ struct Weights {
     template <bool CAP>
     __device__ __forceinline__ double weight(float y, double top) const {
 #pragma clang fp contract(off)
-        const double w = exp2_f64(level<CAP>(y) - top);
-        return y == kNegInf ? 0.0 : w;
+        return exp2_f64(level<CAP>(y) - top, CAP && y == kNegInf);
     }
 };
 
-// NaN weighs nothing; +infinity is the largest float.
-__device__ __forceinline__ float clean(float y) { return y == y ? fminf(y, 3.4028234663852886e38f) : kNegInf; }
+// +infinity counts as the largest float; NaN weighs nothing: v_med3_f32 with
+// a NaN gives the smallest of the other two (the compiler's own median drops
+// the -infinity as an identity).
+__device__ __forceinline__ float clean(float y) {
+    float r;
+    asm("v_med3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(y), "v"(kNegInf), "v"(3.4028234663852886e38f));
+    return r;
+}
 
 struct Stat {
     double sum;
@@ -127,7 +133,7 @@ struct Pick {
 struct DraftView {
     DraftArgs a;
     Weights w;
-    int chunks, groups;  // groups = chunks * kWaves
+    int chunks, groups;
     bool vec;      // rows of logits are 16-byte aligned
     Stat* stats;   // [B][2 G + 1][chunks]: target rows 0 .. G, then draft rows
     double* rest;  // [B][groups]: sums of max(p - q, 0) (of p for the bonus row)
@@ -188,63 +194,66 @@ __device__ __forceinline__ float wave_max(float v) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), kWave - 1));
 }
 
-// 16 logits of the wave's group of a chunk, 4 by 4 across the wave (a sum's
-// order is free); past the row's end: no weight.
-__device__ __forceinline__ void load_spread(const DraftView& D, const float* y, int c, float (&v)[kPer]) {
-    const int64_t base = static_cast<int64_t>(c) * kChunk + threadIdx.x / kWave * kGroup + 4 * (threadIdx.x & (kWave - 1));
-    if (D.vec && (c + 1) * static_cast<int64_t>(kChunk) <= D.a.V) {  // all loads first
-        float4 f[kPer / 4];
+// PER logits a lane of the 64 PER from `base` on, 4 by 4 across the wave (a
+// sum's order is free), as they are; past the row's end: no weight.
+template <int PER>
+__device__ __forceinline__ void load_spread(const DraftView& D, const float* y, int64_t base, float (&v)[PER]) {
+    const int lane = threadIdx.x & (kWave - 1);
+    if (D.vec && base + PER * kWave <= D.a.V) {  // all loads first
+        float4 f[PER / 4];
 #pragma unroll
-        for (int i = 0; i < kPer / 4; ++i) f[i] = *reinterpret_cast<const float4*>(y + base + i * 4 * kWave);
+        for (int i = 0; i < PER / 4; ++i) f[i] = *reinterpret_cast<const float4*>(y + base + (i * kWave + lane) * 4);
 #pragma unroll
-        for (int i = 0; i < kPer / 4; ++i) {
-            v[4 * i] = clean(f[i].x); v[4 * i + 1] = clean(f[i].y); v[4 * i + 2] = clean(f[i].z); v[4 * i + 3] = clean(f[i].w);
+        for (int i = 0; i < PER / 4; ++i) {
+            v[4 * i] = f[i].x; v[4 * i + 1] = f[i].y; v[4 * i + 2] = f[i].z; v[4 * i + 3] = f[i].w;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {  // past the end: the last one again, then taken out
-            const int64_t at = base + i / 4 * 4 * kWave + i % 4;
+        for (int i = 0; i < PER; ++i) {  // past the end: the last one again, then taken out
+            const int64_t at = base + i * kWave + lane;
             v[i] = y[at < D.a.V ? at : D.a.V - 1];
         }
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int64_t at = base + i / 4 * 4 * kWave + i % 4;
-            v[i] = at < D.a.V ? clean(v[i]) : kNegInf;
-        }
+        for (int i = 0; i < PER; ++i) v[i] = base + i * kWave + lane < D.a.V ? v[i] : kNegInf;
     }
 }
 
 template <bool CAP>
-__global__ __launch_bounds__(kThreads)
+__global__ __launch_bounds__(kStatThreads)
 void draft_stats_kernel(DraftView D) {
-    __shared__ float mx[kWaves];
-    __shared__ double sm[kWaves];
+    __shared__ float mx[kStatWaves];
+    __shared__ double sm[kStatWaves];
+    constexpr int kPer = kChunk / kStatThreads;
     const int c = blockIdx.x, r = blockIdx.y;
     const int64_t b = blockIdx.z;
     const int n = D.drafts(b);
     if (r <= D.a.G ? r > n : r - D.a.G - 1 >= n) return;  // a row that no draft uses
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
     float v[kPer];
-    load_spread(D, D.row(b, r), c, v);
+    load_spread(D, D.row(b, r), static_cast<int64_t>(c) * kChunk + wave * (kPer * kWave), v);
     fill_exp_table();
     float top = kNegInf;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) top = fmaxf(top, v[i]);
+    for (int i = 0; i < kPer; ++i) {
+        v[i] = clean(v[i]);
+        top = fmaxf(top, v[i]);
+    }
     top = wave_max(top);
-    if ((threadIdx.x & (kWave - 1)) == 0) mx[threadIdx.x / kWave] = top;
+    if (lane == 0) mx[wave] = top;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) top = fmaxf(top, mx[i]);
+    for (int i = 0; i < kStatWaves; ++i) top = fmaxf(top, mx[i]);
     const double level = D.w.template level<CAP>(top);
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) sum += D.w.template weight<CAP>(v[i], level);
     sum = wave_add(sum);
-    if ((threadIdx.x & (kWave - 1)) == 0) sm[threadIdx.x / kWave] = sum;
+    if (lane == 0) sm[wave] = sum;
     __syncthreads();
     if (threadIdx.x == 0) {
         sum = 0.0;
 #pragma unroll
-        for (int i = 0; i < kWaves; ++i) sum += sm[i];
+        for (int i = 0; i < kStatWaves; ++i) sum += sm[i];
         Stat* s = D.stats + (b * (2 * D.a.G + 1) + r) * D.chunks + c;
         s->sum = sum;
         s->top = top;
@@ -270,12 +279,12 @@ __device__ __forceinline__ void join_row(const DraftView& D, int64_t b, int r, d
 
 __device__ __forceinline__ double inverse(double sum) { return sum > 0.0 ? 1.0 / sum : 0.0; }
 
-template <bool CAP>
-__global__ __launch_bounds__(kThreads)
+template <bool CAP, int STEPS>
+__global__ __launch_bounds__(kPickThreads)
 void draft_pick_kernel(DraftView D) {
     __shared__ double levels[kMaxRows], inverses[kMaxRows];
     __shared__ Pick P;
-    const int c = blockIdx.x;
+    const int part = blockIdx.x;
     const int64_t b = blockIdx.y;
     const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
     const int n = D.drafts(b), G = D.a.G;
@@ -293,7 +302,7 @@ void draft_pick_kernel(DraftView D) {
     }
     fill_exp_table();
     __syncthreads();
-    for (int i = wave; i < 2 * n + 1; i += kWaves) {
+    for (int i = wave; i < 2 * n + 1; i += kPickWaves) {
         const int r = i <= n ? i : G + i - n;  // target rows 0 .. n, draft rows G + 1 ..
         double level, sum;
         join_row<CAP>(D, b, r, &level, &sum);
@@ -319,154 +328,173 @@ void draft_pick_kernel(DraftView D) {
             P.p_inv = inverses[a];
             P.q_level = a < n ? levels[G + 1 + a] : 0.0;
             P.q_inv = a < n ? inverses[G + 1 + a] : 0.0;
-            if (c == 0) D.picks[b] = P;
+            if (part == 0) D.picks[b] = P;
         }
     }
     __syncthreads();
-    float vp[kPer], vq[kPer];
-    load_spread(D, D.row(b, P.accepted), c, vp);
-    double x = 0.0, y = 0.0;
-    if (P.residual) {
-        load_spread(D, D.row(b, G + 1 + P.accepted), c, vq);
+    constexpr int kPer = kGroup / kWave;
+    const float* row_p = D.row(b, P.accepted);
+    const float* row_q = D.row(b, P.residual ? G + 1 + P.accepted : P.accepted);
+    float vp[STEPS][kPer], vq[STEPS][kPer];
+    const int64_t group0 = static_cast<int64_t>(part) * STEPS * kPickWaves + wave;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const double p = D.w.template weight<CAP>(vp[i], P.p_level) * P.p_inv;
-            y += p;
-            x += fmax(p - D.w.template weight<CAP>(vq[i], P.q_level) * P.q_inv, 0.0);
-        }
-        x = wave_add(x);
-        y = wave_add(y);
-    } else {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) x += D.w.template weight<CAP>(vp[i], P.p_level) * P.p_inv;
-        x = y = wave_add(x);
+    for (int i = 0; i < STEPS; ++i) {  // all loads first
+        const int64_t base = (group0 + i * kPickWaves) * kGroup;
+        load_spread(D, row_p, base, vp[i]);
+        if (P.residual) load_spread(D, row_q, base, vq[i]);
     }
-    if (lane == 0) {
-        D.rest[b * D.groups + c * kWaves + wave] = x;
-        D.whole[b * D.groups + c * kWaves + wave] = y;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const int64_t group = group0 + i * kPickWaves;
+        double x = 0.0, y = 0.0;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const double p = D.w.template weight<CAP>(clean(vp[i][e]), P.p_level) * P.p_inv;
+            y += p;
+            if (P.residual) x += fmax(p - D.w.template weight<CAP>(clean(vq[i][e]), P.q_level) * P.q_inv, 0.0);
+        }
+        y = wave_add(y);
+        x = P.residual ? wave_add(x) : y;
+        if (lane == 0 && group < D.groups) {
+            D.rest[b * D.groups + group] = x;
+            D.whole[b * D.groups + group] = y;
+        }
     }
 }
 
-// The group that holds the drawn point, by one wave: the first whose running
-// sum exceeds u times the whole sum, or the last with any weight (-1: none
-// has).  A lane sums `per` consecutive groups, the wave their sums; then the
-// lane with the point goes through its own.
-__device__ __forceinline__ int find_group(const double* s, int groups, double u, double* target, double* before) {
-    const int lane = threadIdx.x & (kWave - 1);
-    const int per = (groups + kWave - 1) / kWave;
-    const int g0 = min(lane * per, groups), g1 = min(g0 + per, groups);
-    double mine = 0.0;
-    int tail = -1;
-    for (int g = g0; g < g1; ++g) {
-        mine += s[g];
-        if (s[g] > 0.0) tail = g;
-    }
+// A running sum over the workgroup's threads, in order: the sum before this
+// thread, and the whole.
+__device__ __forceinline__ double block_prefix(double mine, double* lds, double* total) {
     const double upto = wave_prefix(mine);
-    *target = u * lane_f64(upto, kWave - 1);
-    int hit = -1;
-    double run = upto - mine, from = run;
-    for (int g = g0; g < g1 && hit < 0; ++g) {
-        from = run;
-        run += s[g];
-        if (s[g] > 0.0 && run > *target) hit = g;
+    const int wave = threadIdx.x / kWave;
+    __syncthreads();
+    if ((threadIdx.x & (kWave - 1)) == kWave - 1) lds[wave] = upto;
+    __syncthreads();
+    double before = upto - mine;
+    *total = 0.0;
+#pragma unroll
+    for (int i = 0; i < kDrawWaves; ++i) {
+        if (i < wave) before += lds[i];
+        *total += lds[i];
     }
-    uint64_t lanes = __ballot(hit >= 0);
-    if (lanes == 0) {  // the point lies at the very end: the last group with weight
-        hit = tail;
-        lanes = __ballot(tail >= 0);
-        if (lanes == 0) return -1;
-        lanes = uint64_t{1} << (63 - __clzll(static_cast<long long>(lanes)));
-        from = run;
-        if (tail >= 0)
-            for (int g = g1 - 1; g >= tail; --g) from -= s[g];
-    }
-    const int at = __ffsll(static_cast<unsigned long long>(lanes)) - 1;
-    *before = lane_f64(from, at);
-    return __builtin_amdgcn_readlane(hit, at);
+    return before;
 }
 
 template <bool CAP>
-__global__ __launch_bounds__(kThreads)
+__global__ __launch_bounds__(kDrawThreads)
 void draft_draw_kernel(DraftView D) {
-    __shared__ double sums[kWaves];
-    __shared__ int found, last, group, from_whole;
-    __shared__ double target, before;
+    __shared__ double sums[kDrawWaves];
+    __shared__ int found, last;
+    __shared__ double before_group;
     const int64_t b = blockIdx.x;
-    const int t = threadIdx.x, wave = t / kWave, lane = t & (kWave - 1), G = D.a.G;
+    const int t = threadIdx.x, G = D.a.G;
     const Pick P = D.picks[b];
-    if (wave == 0) {
-        const double u = static_cast<double>(D.a.u[b * (G + 1) + G]);
-        double to, from;
-        int g = find_group(D.rest + b * D.groups, D.groups, u, &to, &from);
-        const bool all = g < 0;  // no rest anywhere: from p itself
-        if (all) g = find_group(D.whole + b * D.groups, D.groups, u, &to, &from);
-        if (lane == 0) {
-            group = g;
-            from_whole = all;
-            target = to;
-            before = from;
+    const double u = static_cast<double>(D.a.u[b * (G + 1) + G]);
+    fill_exp_table();
+    const int per = (D.groups + kDrawThreads - 1) / kDrawThreads;
+    const int g0 = min(t * per, D.groups), g1 = min(g0 + per, D.groups);
+    int group = -1;
+    double target = 0.0;
+    bool minus = P.residual;
+    // the group: the first whose running sum exceeds u times the whole, or
+    // the last with any weight.  No rest anywhere: from p itself.
+    for (int pass = 0; pass < 2; ++pass) {
+        const double* s = (pass == 0 ? D.rest : D.whole) + b * D.groups;
+        double mine = 0.0, total;
+        int tail = -1;
+#pragma unroll 4
+        for (int g = g0; g < g1; ++g) {
+            const double v = s[g];
+            mine += v;
+            tail = v > 0.0 ? g : tail;
+        }
+        double run = block_prefix(mine, sums, &total);
+        if (!(total > 0.0)) {
+            minus = false;
+            continue;
+        }
+        target = u * total;
+        if (t == 0) {
+            found = INT32_MAX;
+            last = -1;
+        }
+        __syncthreads();
+        int hit = INT32_MAX;
+        double from = run;
+        if (run + mine > target)
+            for (int g = g0; g < g1; ++g) {
+                const double v = s[g];
+                if (v > 0.0 && run + v > target) {
+                    hit = g;
+                    from = run;
+                    break;
+                }
+                run += v;
+            }
+        if (hit != INT32_MAX) atomicMin(&found, hit);
+        if (tail >= 0) atomicMax(&last, tail);
+        __syncthreads();
+        group = found != INT32_MAX ? found : last;
+        if (hit == group) before_group = from;
+        // the point lies at the very end: nothing in the last group passes it
+        // and its last element with weight is drawn
+        if (found == INT32_MAX && t == 0) before_group = 0.0;
+        __syncthreads();
+        break;
+    }
+    int token = -1;
+    if (group >= 0) {
+        // thread t has element t of the group
+        const int64_t at_v = static_cast<int64_t>(group) * kGroup + t;
+        double weight = 0.0, total;
+        if (at_v < D.a.V) {
+            const float yp = clean(D.row(b, P.accepted)[at_v]);
+            const float yq = minus ? clean(D.row(b, G + 1 + P.accepted)[at_v]) : 0.0f;
+            weight = D.w.template weight<CAP>(yp, P.p_level) * P.p_inv;
+            if (minus) weight = fmax(weight - D.w.template weight<CAP>(yq, P.q_level) * P.q_inv, 0.0);
+        }
+        const double run = before_group + block_prefix(weight, sums, &total) + weight;
+        if (t == 0) {
             found = kGroup;
             last = -1;
         }
-    }
-    fill_exp_table();
-    __syncthreads();
-    int token = -1;
-    if (group >= 0) {
-        // thread t has elements 2 t and 2 t + 1 of the group
-        const float* yp = D.row(b, P.accepted);
-        const bool minus = P.residual && !from_whole;
-        const float* yq = minus ? D.row(b, G + 1 + P.accepted) : yp;
-        const int64_t base = static_cast<int64_t>(group) * kGroup + t * kGroupPer;
-        double w[kGroupPer];
-        double mine = 0.0;
-        int tail = -1;
-#pragma unroll
-        for (int i = 0; i < kGroupPer; ++i) {
-            w[i] = 0.0;
-            if (base + i < D.a.V) {
-                w[i] = D.w.template weight<CAP>(clean(yp[base + i]), P.p_level) * P.p_inv;
-                if (minus) w[i] = fmax(w[i] - D.w.template weight<CAP>(clean(yq[base + i]), P.q_level) * P.q_inv, 0.0);
-            }
-            mine += w[i];
-            if (w[i] > 0.0) tail = t * kGroupPer + i;
-        }
-        const double upto = wave_prefix(mine);
-        if (lane == kWave - 1) sums[wave] = upto;
         __syncthreads();
-        double run = before + (upto - mine);
-        for (int i = 0; i < wave; ++i) run += sums[i];
-        int hit = kGroup;
-#pragma unroll
-        for (int i = 0; i < kGroupPer; ++i) {
-            run += w[i];
-            if (hit == kGroup && w[i] > 0.0 && run > target) hit = t * kGroupPer + i;
+        if (weight > 0.0) {
+            if (run > target) atomicMin(&found, t);
+            atomicMax(&last, t);
         }
-        if (hit < kGroup) atomicMin(&found, hit);
-        if (tail >= 0) atomicMax(&last, tail);
         __syncthreads();
         const int at = found < kGroup ? found : last;
         token = at < 0 ? -1 : static_cast<int>(static_cast<int64_t>(group) * kGroup + at);
     }
     const int a = P.accepted;
     if (t == 0) D.a.accepted[b] = a;
-    for (int i = t; i <= G; i += kThreads)
+    for (int i = t; i <= G; i += kDrawThreads)
         D.a.tokens[b * (G + 1) + i] = i < a ? D.a.draft_tokens[b * G + i] : (i == a ? token : -1);
 }
 
 int64_t chunks_of(int64_t V) { return (V + kChunk - 1) / kChunk; }
+int64_t groups_of(int64_t V) { return (V + kGroup - 1) / kGroup; }
 
 template <bool CAP>
 hipError_t launch_draft(const DraftView& D, hipStream_t stream) {
     const unsigned ch = static_cast<unsigned>(D.chunks), B = static_cast<unsigned>(D.a.B);
-    hipLaunchKernelGGL(draft_stats_kernel<CAP>, dim3(ch, static_cast<unsigned>(2 * D.a.G + 1), B), dim3(kThreads), 0,
+    // Every workgroup of the pick kernel joins the rows' chunks again: it
+    // takes four steps where that leaves enough workgroups for all CUs.
+    const int64_t steps = (D.a.V + kStep - 1) / kStep;
+    const bool few = steps * D.a.B < 2048;
+    const unsigned parts = static_cast<unsigned>(few ? steps : (steps + 3) / 4);
+    hipLaunchKernelGGL(draft_stats_kernel<CAP>, dim3(ch, static_cast<unsigned>(2 * D.a.G + 1), B), dim3(kStatThreads), 0,
                        stream, D);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(draft_pick_kernel<CAP>, dim3(ch, B), dim3(kThreads), 0, stream, D);
+    if (few)
+        hipLaunchKernelGGL((draft_pick_kernel<CAP, 1>), dim3(parts, B), dim3(kPickThreads), 0, stream, D);
+    else
+        hipLaunchKernelGGL((draft_pick_kernel<CAP, 4>), dim3(parts, B), dim3(kPickThreads), 0, stream, D);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(draft_draw_kernel<CAP>, dim3(B), dim3(kThreads), 0, stream, D);
+    hipLaunchKernelGGL(draft_draw_kernel<CAP>, dim3(B), dim3(kDrawThreads), 0, stream, D);
     return hipGetLastError();
 }
 
@@ -475,9 +503,9 @@ size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 }  // namespace
 
 size_t draft_ws_bytes(int64_t B, int G, int64_t V) {
-    const size_t n = static_cast<size_t>(B) * static_cast<size_t>(chunks_of(V));
-    return align256(n * static_cast<size_t>(2 * G + 1) * sizeof(Stat)) + 2 * align256(n * kWaves * sizeof(double)) +
-           align256(static_cast<size_t>(B) * sizeof(Pick));
+    const size_t b = static_cast<size_t>(B);
+    return align256(b * static_cast<size_t>(chunks_of(V)) * static_cast<size_t>(2 * G + 1) * sizeof(Stat)) +
+           2 * align256(b * static_cast<size_t>(groups_of(V)) * sizeof(double)) + align256(b * sizeof(Pick));
 }
 
 hipError_t launch_draft_verify(const DraftArgs& a, void* ws, hipStream_t stream) {
@@ -487,15 +515,15 @@ hipError_t launch_draft_verify(const DraftArgs& a, void* ws, hipStream_t stream)
     D.w.cap = static_cast<double>(a.softcap) * D.w.k;
     D.w.twice = a.softcap > 0.0f ? 2.0 * kLog2e / static_cast<double>(a.softcap) : 0.0;
     D.chunks = static_cast<int>(chunks_of(a.V));
-    D.groups = D.chunks * kWaves;
-    const size_t n = static_cast<size_t>(a.B) * static_cast<size_t>(D.chunks);
+    D.groups = static_cast<int>(groups_of(a.V));
+    const size_t b = static_cast<size_t>(a.B);
     char* p = static_cast<char*>(ws);
     D.stats = reinterpret_cast<Stat*>(p);
-    p += align256(n * static_cast<size_t>(2 * a.G + 1) * sizeof(Stat));
+    p += align256(b * static_cast<size_t>(D.chunks) * static_cast<size_t>(2 * a.G + 1) * sizeof(Stat));
     D.rest = reinterpret_cast<double*>(p);
-    p += align256(n * kWaves * sizeof(double));
+    p += align256(b * static_cast<size_t>(D.groups) * sizeof(double));
     D.whole = reinterpret_cast<double*>(p);
-    D.picks = reinterpret_cast<Pick*>(p + align256(n * kWaves * sizeof(double)));
+    D.picks = reinterpret_cast<Pick*>(p + align256(b * static_cast<size_t>(D.groups) * sizeof(double)));
     D.vec = ((reinterpret_cast<uintptr_t>(a.target) | reinterpret_cast<uintptr_t>(a.draft)) & 15) == 0 &&
             a.ldt % 4 == 0 && a.ldd % 4 == 0;
     return a.softcap > 0.0f ? launch_draft<true>(D, stream) : launch_draft<false>(D, stream);
