@@ -23,6 +23,7 @@
 
 #include "qmv_device.h"
 #include "qmv_internal.h"
+#include "step_device.h"
 #include "step_internal.h"
 
 namespace qmv {
@@ -147,36 +148,6 @@ struct DraftView {
         return r <= a.G ? a.target + (b * (a.G + 1) + r) * a.ldt : a.draft + (b * a.G + (r - a.G - 1)) * a.ldd;
     }
 };
-
-// A double of another lane (0 where the pattern has none).
-template <int CTRL, int ROW_MASK>
-__device__ __forceinline__ double dpp_f64(double v) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, ROW_MASK, 0xF, false);
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, ROW_MASK, 0xF, false);
-    return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
-}
-
-__device__ __forceinline__ double lane_f64(double v, int lane) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), lane);
-    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), lane);
-    return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
-}
-
-// Inclusive sum over the lanes, in lane order: within rows of 16 lanes
-// (row_shr 1, 2, 4, 8), then across them (row_bcast 15 and 31).
-__device__ __forceinline__ double wave_prefix(double v) {
-    v += dpp_f64<0x111, 0xF>(v);
-    v += dpp_f64<0x112, 0xF>(v);
-    v += dpp_f64<0x114, 0xF>(v);
-    v += dpp_f64<0x118, 0xF>(v);
-    v += dpp_f64<0x142, 0xA>(v);
-    v += dpp_f64<0x143, 0xC>(v);
-    return v;
-}
-
-__device__ __forceinline__ double wave_add(double v) { return lane_f64(wave_prefix(v), kWave - 1); }
 
 template <int CTRL, int ROW_MASK>
 __device__ __forceinline__ float dpp_max(float v) {

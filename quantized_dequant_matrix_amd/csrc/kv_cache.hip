@@ -7,36 +7,17 @@
 // 4 bytes in and 1 (2) out an element for the write, the reverse for the
 // read.
 //
-// Work split: blockIdx.x is a row of the batch, blockIdx.y keys or values.
-// D / 4 lanes hold a head's row, four elements each, so that the row's
-// maximum is a few lane exchanges and a wave writes whole rows of codes.
+// Work split: blockIdx.x is one row of the batch or eight, blockIdx.y keys or
+// values.  D / 4 lanes hold a head's row, four elements each, so that the
+// row's maximum is a few lane exchanges and a wave writes whole rows of codes.
 #include <stdint.h>
 
 #include "kv_device.h"
+#include "step_device.h"
 #include "step_internal.h"
 
 namespace qmv {
 namespace {
-
-__device__ __forceinline__ float4 load4(const float* p, bool vec) {
-    if (vec) return *reinterpret_cast<const float4*>(p);
-    return make_float4(p[0], p[1], p[2], p[3]);
-}
-
-__device__ __forceinline__ void store4(float* p, float4 v, bool vec) {
-    if (vec) {
-        *reinterpret_cast<float4*>(p) = v;
-    } else {
-        p[0] = v.x; p[1] = v.y; p[2] = v.z; p[3] = v.w;
-    }
-}
-
-__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
-__device__ __forceinline__ uint32_t code_q8(float v, float d) {
-    const float r = fminf(fmaxf(roundf(v / d), -127.0f), 127.0f);
-    return static_cast<uint32_t>(static_cast<int>(r)) & 0xffu;
-}
 
 struct KvPlanes {
     void* k;
@@ -45,80 +26,183 @@ struct KvPlanes {
     float* v_scale;
 };
 
+// Places of the ROWS rows from `first` on, in LDS: -1 without a place, -2 for
+// a row of no sequence.  The wave that runs this finds the first row's
+// sequence, holds the 64 row starts behind it, and counts for each row how
+// many it has passed.
+template <int ROWS>
+__device__ __forceinline__ void find_slots(const KvView& view, int first, int64_t* slots) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int b0 = find_sequence(view.row_start, view.B, first);
+    const int ahead = b0 + 1 + lane;
+    const int start = ahead <= view.B ? view.row_start[ahead] : INT32_MAX;
+    int row = -1, b = -1;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int r = first + i;
+        int c = __popcll(__ballot(start <= r));
+        if (c == kWave) c = find_sequence(view.row_start, view.B, r) - b0;  // 64 empty sequences in between
+        if (lane == i) {
+            row = r;
+            b = b0 + c;
+        }
+    }
+    if (lane < ROWS) {
+        int64_t slot = -2;
+        if (row < view.T && b < view.B) {
+            const int lo = view.row_start[b], end = view.row_start[b + 1];
+            if (row >= lo && row < end) {
+                slot = -1;
+                const int64_t pos = static_cast<int64_t>(view.kv_len[b]) - (end - static_cast<int64_t>(row));
+                if (pos >= 0 && (pos >> view.page_shift) < view.max_pages) {
+                    const int page = view.table[static_cast<int64_t>(b) * view.max_pages + (pos >> view.page_shift)];
+                    if (page >= 0 && page < view.num_pages)
+                        slot = (static_cast<int64_t>(page) << view.page_shift) + (pos & ((1 << view.page_shift) - 1));
+                }
+            }
+        }
+        slots[lane] = slot;
+    }
+}
+
+// The (row, quad of elements) pairs of ROWS rows of `quads` quads, 256 a
+// step: rows side by side where a row has fewer than 256.
+template <int ROWS>
+struct Steps {
+    int quads, wide, sub, quad, per, count;
+    __device__ __forceinline__ explicit Steps(int quads_) : quads(quads_) {
+        wide = quads < kBlockThreads ? kBlockThreads / quads : 1;  // rows of a step
+        sub = wide > 1 ? threadIdx.x / quads : 0;
+        quad = threadIdx.x - sub * quads;
+        if (sub >= wide) quad = quads;  // left over: never in
+        per = (quads + kBlockThreads - 1) / kBlockThreads;  // steps of a row
+        count = wide > 1 ? (ROWS + wide - 1) / wide : ROWS * per;
+    }
+    __device__ __forceinline__ bool at(int step, int* row, int* q) const {
+        if (wide > 1) {
+            *row = step * wide + sub;
+            *q = quad;
+        } else {
+            *row = step / per;
+            *q = quad + (step - *row * per) * kBlockThreads;
+        }
+        return step < count && *row < ROWS && *q < quads;
+    }
+};
+
+constexpr int kUnroll = 4;  // steps whose loads are in flight together
+
 // F16: the row's maximum decides only whether every element is finite.
-template <int D, bool F16>
+template <int D, bool F16, int ROWS>
 __global__ __launch_bounds__(kBlockThreads)
 void kv_write_kernel(KvView view, KvPlanes c, const float* __restrict__ k, int64_t ldk, const float* __restrict__ v,
                      int64_t ldv, bool vec) {
-    constexpr int L = D / 4;                    // lanes of a head's row
-    constexpr int kHeads = kBlockThreads / L;   // heads of one pass
-    const int row = blockIdx.x;
+    constexpr int L = D / 4;  // lanes of a head's row
+    __shared__ int64_t slots[ROWS];
     const bool values = blockIdx.y != 0;
-    const float* src = values ? v + row * ldv : k + row * ldk;
-    bool belongs;
-    const int64_t slot = row_slot(view, row, &belongs);
-    if (slot < 0) return;
-    const int64_t page = slot >> view.page_shift, at = slot & ((1 << view.page_shift) - 1);
-    const int sub = threadIdx.x % L;
-    for (int h = threadIdx.x / L; h < view.heads; h += kHeads) {
-        const float4 x = load4(src + static_cast<int64_t>(h) * D + 4 * sub, vec);
-        const int64_t cell = ((page * view.heads + h) << view.page_shift) + at;
-        if constexpr (F16) {
-            _Float16 f[4] = {static_cast<_Float16>(x.x), static_cast<_Float16>(x.y), static_cast<_Float16>(x.z),
-                             static_cast<_Float16>(x.w)};
-            uint32_t a = 0;
+    const int first = blockIdx.x * ROWS;
+    const float* src = values ? v : k;
+    const int64_t ld = values ? ldv : ldk;
+    void* codes = values ? c.v : c.k;
+    float* scales = values ? c.v_scale : c.k_scale;
+    if (threadIdx.x < kWave) find_slots<ROWS>(view, first, slots);
+    const Steps<ROWS> steps(view.heads * L);
+    const int in_page = (1 << view.page_shift) - 1;
+    for (int s0 = 0; s0 < steps.count; s0 += kUnroll) {
+        float4 x[kUnroll];
+        int row[kUnroll], q[kUnroll];
+        bool in[kUnroll];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) a = max(a, mag_bits(static_cast<float>(f[e])));
+        for (int i = 0; i < kUnroll; ++i) {
+            in[i] = steps.at(s0 + i, &row[i], &q[i]) && first + row[i] < view.T;
+            x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (in[i]) x[i] = load4(src + (first + row[i]) * ld + 4 * q[i], vec);
+        }
+        if (s0 == 0) __syncthreads();  // the slots, found while the first rows come
 #pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1) a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), o, L)));
-            uint2 packed;
-            packed.x = __builtin_bit_cast(uint16_t, f[0]) | (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, f[1])) << 16);
-            packed.y = __builtin_bit_cast(uint16_t, f[2]) | (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, f[3])) << 16);
-            if (a >= 0x7f800000u) packed = make_uint2(0x7e007e00u, 0x7e007e00u);
-            reinterpret_cast<uint2*>(values ? c.v : c.k)[cell * L + sub] = packed;
-        } else {
-            uint32_t a = max(max(mag_bits(x.x), mag_bits(x.y)), max(mag_bits(x.z), mag_bits(x.w)));
+        for (int i = 0; i < kUnroll; ++i) {
+            // the D / 4 lanes of a head's row are in or out together
+            const int64_t slot = in[i] ? slots[row[i]] : -1;
+            const int h = q[i] / L, sub = q[i] % L;
+            const int64_t cell = (((slot >> view.page_shift) * view.heads + h) << view.page_shift) + (slot & in_page);
+            if constexpr (F16) {
+                const _Float16 f[4] = {static_cast<_Float16>(x[i].x), static_cast<_Float16>(x[i].y),
+                                       static_cast<_Float16>(x[i].z), static_cast<_Float16>(x[i].w)};
+                uint32_t a = 0;
 #pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1) a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), o, L)));
-            const float d = a < 0x7f800000u ? __uint_as_float(a) / 127.0f : __uint_as_float(0x7fc00000u);
-            uint32_t packed = 0;
-            if (a != 0u && a < 0x7f800000u)
-                packed = code_q8(x.x, d) | (code_q8(x.y, d) << 8) | (code_q8(x.z, d) << 16) | (code_q8(x.w, d) << 24);
-            reinterpret_cast<uint32_t*>(values ? c.v : c.k)[cell * L + sub] = packed;
-            if (sub == 0) (values ? c.v_scale : c.k_scale)[cell] = d;
+                for (int e = 0; e < 4; ++e) a = max(a, mag_bits(static_cast<float>(f[e])));
+#pragma unroll
+                for (int o = L / 2; o > 0; o >>= 1) a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), o, L)));
+                uint2 packed;
+                packed.x = __builtin_bit_cast(uint16_t, f[0]) | (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, f[1])) << 16);
+                packed.y = __builtin_bit_cast(uint16_t, f[2]) | (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, f[3])) << 16);
+                if (a >= 0x7f800000u) packed = make_uint2(0x7e007e00u, 0x7e007e00u);
+                if (slot >= 0) reinterpret_cast<uint2*>(codes)[cell * L + sub] = packed;
+            } else {
+                uint32_t a = mag_bits4(x[i]);
+#pragma unroll
+                for (int o = L / 2; o > 0; o >>= 1) a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), o, L)));
+                const float d = scale_q8(a);
+                const uint32_t packed = codes_q8(x[i], a, d);
+                if (slot >= 0) {
+                    reinterpret_cast<uint32_t*>(codes)[cell * L + sub] = packed;
+                    if (sub == 0) scales[cell] = d;
+                }
+            }
         }
     }
 }
 
-template <int D, bool F16>
+template <int D, bool F16, int ROWS>
 __global__ __launch_bounds__(kBlockThreads)
 void kv_read_kernel(KvView view, KvPlanes c, float* __restrict__ k, int64_t ldk, float* __restrict__ v, int64_t ldv,
                     bool vec) {
     constexpr int L = D / 4;
-    constexpr int kHeads = kBlockThreads / L;
-    const int row = blockIdx.x;
+    __shared__ int64_t slots[ROWS];
     const bool values = blockIdx.y != 0;
-    float* dst = values ? v + row * ldv : k + row * ldk;
-    bool belongs;
-    const int64_t slot = row_slot(view, row, &belongs);
-    if (!belongs) return;
-    const int64_t page = slot >> view.page_shift, at = slot & ((1 << view.page_shift) - 1);
-    const int sub = threadIdx.x % L;
-    for (int h = threadIdx.x / L; h < view.heads; h += kHeads) {
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (slot >= 0) {
-            const int64_t cell = ((page * view.heads + h) << view.page_shift) + at;
-            if constexpr (F16) {
-                const uint2 p = reinterpret_cast<const uint2*>(values ? c.v : c.k)[cell * L + sub];
-                x = make_float4(half_bits_to_float(p.x & 0xffffu), half_bits_to_float(p.x >> 16),
-                                half_bits_to_float(p.y & 0xffffu), half_bits_to_float(p.y >> 16));
-            } else {
-                const uint32_t p = reinterpret_cast<const uint32_t*>(values ? c.v : c.k)[cell * L + sub];
-                const float d = (values ? c.v_scale : c.k_scale)[cell];
-                x = make_float4(sbyte<0>(p) * d, sbyte<1>(p) * d, sbyte<2>(p) * d, sbyte<3>(p) * d);
+    const int first = blockIdx.x * ROWS;
+    float* dst = values ? v : k;
+    const int64_t ld = values ? ldv : ldk;
+    const void* codes = values ? c.v : c.k;
+    const float* scales = values ? c.v_scale : c.k_scale;
+    if (threadIdx.x < kWave) find_slots<ROWS>(view, first, slots);
+    const Steps<ROWS> steps(view.heads * L);
+    const int in_page = (1 << view.page_shift) - 1;
+    __syncthreads();
+    for (int s0 = 0; s0 < steps.count; s0 += kUnroll) {
+        uint2 p[kUnroll];
+        float d[kUnroll];
+        int row[kUnroll], q[kUnroll];
+        int64_t slot[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            slot[i] = steps.at(s0 + i, &row[i], &q[i]) ? slots[row[i]] : -2;
+            p[i] = make_uint2(0u, 0u);
+            d[i] = 0.0f;
+            if (slot[i] >= 0) {
+                const int64_t cell =
+                    (((slot[i] >> view.page_shift) * view.heads + q[i] / L) << view.page_shift) + (slot[i] & in_page);
+                if constexpr (F16) {
+                    p[i] = reinterpret_cast<const uint2*>(codes)[cell * L + q[i] % L];
+                } else {
+                    p[i].x = reinterpret_cast<const uint32_t*>(codes)[cell * L + q[i] % L];
+                    d[i] = scales[cell];
+                }
             }
         }
-        store4(dst + static_cast<int64_t>(h) * D + 4 * sub, x, vec);
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            if (slot[i] == -2) continue;
+            float4 x;
+            if constexpr (F16) {
+                x = make_float4(half_bits_to_float(p[i].x & 0xffffu), half_bits_to_float(p[i].x >> 16),
+                                half_bits_to_float(p[i].y & 0xffffu), half_bits_to_float(p[i].y >> 16));
+            } else {
+                x = make_float4(sbyte<0>(p[i].x) * d[i], sbyte<1>(p[i].x) * d[i], sbyte<2>(p[i].x) * d[i],
+                                sbyte<3>(p[i].x) * d[i]);
+            }
+            store4(dst + (first + row[i]) * ld + 4 * q[i], x, vec);
+        }
     }
 }
 
@@ -129,12 +213,24 @@ bool vec_rows(const void* k, int64_t ldk, const void* v, int64_t ldv) {
 
 }  // namespace
 
+// A workgroup takes one row of a few, eight rows of many (their places are
+// found together, and more loads are in flight).
+constexpr int kManyRows = 2048, kRowsOfMany = 8;
+
 #define KV_LAUNCH(kernel, D, ...)                                                                                      \
     do {                                                                                                               \
-        if (c.format == QMV_KV_F16)                                                                                    \
-            hipLaunchKernelGGL((kernel<D, true>), grid, dim3(kBlockThreads), 0, stream, __VA_ARGS__);                  \
-        else                                                                                                           \
-            hipLaunchKernelGGL((kernel<D, false>), grid, dim3(kBlockThreads), 0, stream, __VA_ARGS__);                 \
+        const dim3 one(static_cast<unsigned>(b.T), 2), many(static_cast<unsigned>((b.T + kRowsOfMany - 1) / kRowsOfMany), 2); \
+        if (b.T < kManyRows) {                                                                                         \
+            if (c.format == QMV_KV_F16)                                                                                \
+                hipLaunchKernelGGL((kernel<D, true, 1>), one, dim3(kBlockThreads), 0, stream, __VA_ARGS__);            \
+            else                                                                                                       \
+                hipLaunchKernelGGL((kernel<D, false, 1>), one, dim3(kBlockThreads), 0, stream, __VA_ARGS__);           \
+        } else {                                                                                                       \
+            if (c.format == QMV_KV_F16)                                                                                \
+                hipLaunchKernelGGL((kernel<D, true, kRowsOfMany>), many, dim3(kBlockThreads), 0, stream, __VA_ARGS__); \
+            else                                                                                                       \
+                hipLaunchKernelGGL((kernel<D, false, kRowsOfMany>), many, dim3(kBlockThreads), 0, stream, __VA_ARGS__); \
+        }                                                                                                              \
     } while (0)
 
 hipError_t launch_kv_write(const qmv_kv_cache& c, const qmv_kv_batch& b, const float* k, int64_t ldk, const float* v,
@@ -142,7 +238,6 @@ hipError_t launch_kv_write(const qmv_kv_cache& c, const qmv_kv_batch& b, const f
     const KvView view = view_of(c, b);
     const KvPlanes p{c.k, c.v, c.k_scale, c.v_scale};
     const bool vec = vec_rows(k, ldk, v, ldv);
-    const dim3 grid(static_cast<unsigned>(b.T), 2);
     if (c.head_dim == 64) KV_LAUNCH(kv_write_kernel, 64, view, p, k, ldk, v, ldv, vec);
     else if (c.head_dim == 128) KV_LAUNCH(kv_write_kernel, 128, view, p, k, ldk, v, ldv, vec);
     else KV_LAUNCH(kv_write_kernel, 256, view, p, k, ldk, v, ldv, vec);
@@ -154,7 +249,6 @@ hipError_t launch_kv_read(const qmv_kv_cache& c, const qmv_kv_batch& b, float* k
     const KvView view = view_of(c, b);
     const KvPlanes p{c.k, c.v, c.k_scale, c.v_scale};
     const bool vec = vec_rows(k, ldk, v, ldv);
-    const dim3 grid(static_cast<unsigned>(b.T), 2);
     if (c.head_dim == 64) KV_LAUNCH(kv_read_kernel, 64, view, p, k, ldk, v, ldv, vec);
     else if (c.head_dim == 128) KV_LAUNCH(kv_read_kernel, 128, view, p, k, ldk, v, ldv, vec);
     else KV_LAUNCH(kv_read_kernel, 256, view, p, k, ldk, v, ldv, vec);

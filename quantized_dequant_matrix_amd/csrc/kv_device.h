@@ -55,21 +55,4 @@ __device__ __forceinline__ int find_sequence(const int32_t* __restrict__ row_sta
     return lo;
 }
 
-// A row's place in the cache: index of its (page, offset) as a token slot
-// page * page_size + offset, or -1 if it has none; belongs: whether the row
-// belongs to a sequence at all.  Wave-uniform.
-__device__ __forceinline__ int64_t row_slot(const KvView& v, int row, bool* belongs) {
-    const int b = find_sequence(v.row_start, v.B, row);
-    *belongs = false;
-    if (b >= v.B) return -1;
-    const int first = v.row_start[b], end = v.row_start[b + 1];
-    if (row < first || row >= end) return -1;
-    *belongs = true;
-    const int64_t pos = static_cast<int64_t>(v.kv_len[b]) - (end - static_cast<int64_t>(row));
-    if (pos < 0 || (pos >> v.page_shift) >= v.max_pages) return -1;
-    const int page = v.table[static_cast<int64_t>(b) * v.max_pages + (pos >> v.page_shift)];
-    if (page < 0 || page >= v.num_pages) return -1;
-    return (static_cast<int64_t>(page) << v.page_shift) + (pos & ((1 << v.page_shift) - 1));
-}
-
 }  // namespace qmv

@@ -11,29 +11,99 @@
 
 #include "qmv_device.h"
 #include "qmv_internal.h"
+#include "step_device.h"
 #include "step_internal.h"
 
 namespace qmv {
 namespace {
 
-// |v| of a block of 32 as an unsigned maximum of the bit patterns, which
-// orders finite numbers, infinity and NaN: a block that is not finite ends
-// with a maximum at or above infinity's pattern.
-__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
-// Code of one element.  Half away from zero, as the activation quantizer.
-__device__ __forceinline__ uint32_t code_q8(float v, float d) {
-    const float r = fminf(fmaxf(roundf(v / d), -127.0f), 127.0f);
-    return static_cast<uint32_t>(static_cast<int>(r)) & 0xffu;
-}
-
-__device__ __forceinline__ double wave_sum_f64(double v) {
-    for (int o = kWave / 2; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+// Sum over the workgroup, every thread with the same bits.
+template <int WAVES_MAX>
+__device__ __forceinline__ double block_sum(double v, double* part, int waves) {
+    v = wave_add(v);
+    if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = v;
+    __syncthreads();
+    v = 0.0;
+#pragma unroll
+    for (int i = 0; i < WAVES_MAX; ++i)
+        if (i < waves) v += part[i];
     return v;
 }
 
-// One workgroup a row.  An element is read, added and written by the same
-// thread in both passes, so z may be x or r.
+__device__ __forceinline__ float rstd_of(double sum, int64_t K, float eps) {
+    return static_cast<float>(1.0 / sqrt(sum / static_cast<double>(K) + static_cast<double>(eps)));
+}
+
+// One workgroup a row of K = 4 Q elements, the whole row in registers: thread
+// t holds the float4 t, t + threads, ... .  Memory bounds it: 8 bytes in and 8
+// (5.1 with codes) out an element, each once.  2048 rows of 5376: 52 us when
+// the second pass read the row again 4 bytes at a time.
+template <int VPT, bool Q8>
+__global__ __launch_bounds__(1024)
+void rmsnorm_row_kernel(const float* x, const float* r, const float* __restrict__ w, float* z, float* __restrict__ y,
+                        int8_t* __restrict__ q, float* __restrict__ d, int Q, float eps, bool vec) {
+    __shared__ double part[16];
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * Q;  // in float4
+    const int t = threadIdx.x, threads = blockDim.x;
+    float4 v[VPT], f[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int i = t + j * threads;
+        v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i < Q) v[j] = load4(x + 4 * (row + i), vec);
+    }
+    if (r) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int i = t + j * threads;
+            f[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i < Q) f[j] = load4(r + 4 * (row + i), vec);
+        }
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            v[j] = make_float4(v[j].x + f[j].x, v[j].y + f[j].y, v[j].z + f[j].z, v[j].w + f[j].w);
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int i = t + j * threads;
+        if (i < Q) f[j] = load4(w + 4 * static_cast<int64_t>(i), vec);
+    }
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int i = t + j * threads;
+        if (z && i < Q) store4(z + 4 * (row + i), v[j], vec);
+        const double e[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sum = fma(e[c], e[c], sum);
+    }
+    sum = block_sum<16>(sum, part, threads / kWave);
+    const float rstd = rstd_of(sum, 4 * static_cast<int64_t>(Q), eps);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int i = t + j * threads;
+        const bool in = i < Q;
+        const float4 o = make_float4((v[j].x * rstd) * f[j].x, (v[j].y * rstd) * f[j].y, (v[j].z * rstd) * f[j].z,
+                                     (v[j].w * rstd) * f[j].w);
+        if constexpr (Q8) {
+            // 8 lanes hold a block: Q is a multiple of 8 and so is threads
+            uint32_t a = in ? mag_bits4(o) : 0u;
+#pragma unroll
+            for (int s = 4; s > 0; s >>= 1) a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), s, 8)));
+            if (in) {
+                const float db = scale_q8(a);
+                reinterpret_cast<uint32_t*>(q)[row + i] = codes_q8(o, a, db);
+                if ((i & 7) == 0) d[(row + i) >> 3] = db;
+            }
+        } else {
+            if (in) store4(y + 4 * (row + i), o, vec);
+        }
+    }
+}
+
+// Rows that no workgroup's registers hold, or of a length that is not a
+// multiple of four: the row is read again after the sum.  An element is read,
+// added and written by the same thread in both passes, so z may be x or r.
 template <int THREADS, bool Q8>
 __global__ __launch_bounds__(THREADS)
 void rmsnorm_kernel(const float* x, const float* r, const float* __restrict__ w, float* z, float* __restrict__ y,
@@ -48,13 +118,8 @@ void rmsnorm_kernel(const float* x, const float* r, const float* __restrict__ w,
         const float v = r ? x[i] + r[i] : x[i];
         sum = fma(static_cast<double>(v), static_cast<double>(v), sum);
     }
-    sum = wave_sum_f64(sum);
-    if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = sum;
-    __syncthreads();
-    sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < THREADS / kWave; ++i) sum += part[i];
-    const float rstd = static_cast<float>(1.0 / sqrt(sum / static_cast<double>(K) + static_cast<double>(eps)));
+    sum = block_sum<THREADS / kWave>(sum, part, THREADS / kWave);
+    const float rstd = rstd_of(sum, K, eps);
     // whole waves stay in the loop: the 32 lanes of a block exchange
     for (int64_t i0 = threadIdx.x & ~(kWave - 1); i0 < K; i0 += THREADS) {
         const int64_t i = i0 + (threadIdx.x & (kWave - 1));
@@ -69,9 +134,9 @@ void rmsnorm_kernel(const float* x, const float* r, const float* __restrict__ w,
             uint32_t a = mag_bits(v);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), o, 32)));
-            const float db = a < 0x7f800000u ? __uint_as_float(a) / 127.0f : __uint_as_float(0x7fc00000u);
+            const float db = scale_q8(a);
             if (i < K) {
-                q[row * K + i] = a == 0u ? 0 : static_cast<int8_t>(code_q8(v, db));
+                q[row * K + i] = static_cast<int8_t>(codes_q8(make_float4(v, 0.0f, 0.0f, 0.0f), a, db));
                 if ((i & 31) == 0) d[(row * K + i) / 32] = db;
             }
         }
@@ -83,10 +148,39 @@ void rmsnorm_kernel(const float* x, const float* r, const float* __restrict__ w,
 hipError_t launch_rmsnorm(const float* x, const float* r, const float* w, float* z, float* y, int8_t* q, float* d,
                           int64_t K, int64_t M, float eps, hipStream_t stream) {
     const dim3 grid(static_cast<unsigned>(M));
-    if (q)
-        hipLaunchKernelGGL((rmsnorm_kernel<1024, true>), grid, dim3(1024), 0, stream, x, r, w, z, y, q, d, K, eps);
-    else
-        hipLaunchKernelGGL((rmsnorm_kernel<1024, false>), grid, dim3(1024), 0, stream, x, r, w, z, y, q, d, K, eps);
+    // One float4 a thread at a time gives a single row the most lanes; many
+    // rows fill the CUs anyway and do better with four in flight a thread.
+    const int64_t Q = K / 4;
+    const int64_t least = M >= 512 ? 4 : 1;
+    int64_t vpt = (Q + 1023) / 1024;
+    vpt = vpt > least ? vpt : least;
+    vpt = vpt <= 1 ? 1 : vpt <= 2 ? 2 : vpt <= 4 ? 4 : 8;
+    if (K % 4 != 0 || Q > 8 * 1024) {
+        if (q)
+            hipLaunchKernelGGL((rmsnorm_kernel<1024, true>), grid, dim3(1024), 0, stream, x, r, w, z, y, q, d, K, eps);
+        else
+            hipLaunchKernelGGL((rmsnorm_kernel<1024, false>), grid, dim3(1024), 0, stream, x, r, w, z, y, q, d, K, eps);
+        return hipGetLastError();
+    }
+    const uintptr_t all = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(r) | reinterpret_cast<uintptr_t>(w) |
+                          reinterpret_cast<uintptr_t>(z) | reinterpret_cast<uintptr_t>(y);
+    const bool vec = (all & 15) == 0;
+    const int64_t threads = ((Q + vpt - 1) / vpt + kWave - 1) / kWave * kWave;
+    const dim3 block(static_cast<unsigned>(threads));
+#define ROW(V)                                                                                                     \
+    do {                                                                                                           \
+        if (q)                                                                                                     \
+            hipLaunchKernelGGL((rmsnorm_row_kernel<V, true>), grid, block, 0, stream, x, r, w, z, y, q, d,         \
+                               static_cast<int>(Q), eps, vec);                                                     \
+        else                                                                                                       \
+            hipLaunchKernelGGL((rmsnorm_row_kernel<V, false>), grid, block, 0, stream, x, r, w, z, y, q, d,        \
+                               static_cast<int>(Q), eps, vec);                                                     \
+    } while (0)
+    if (vpt == 1) ROW(1);
+    else if (vpt == 2) ROW(2);
+    else if (vpt == 4) ROW(4);
+    else ROW(8);
+#undef ROW
     return hipGetLastError();
 }
 

@@ -1,0 +1,83 @@
+// Device-side helpers shared by the decode-step kernels (gfx950, wave64).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "qmv_device.h"
+
+namespace qmv {
+
+// |v| as an unsigned pattern: its maximum over a row orders finite numbers,
+// infinity and NaN, so a row that is not finite ends at or above infinity's.
+__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// The scale of a row or block whose largest pattern is `a`: max|x| / 127, NaN
+// if it is not finite.
+__device__ __forceinline__ float scale_q8(uint32_t a) {
+    return a < 0x7f800000u ? __uint_as_float(a) / 127.0f : __uint_as_float(0x7fc00000u);
+}
+
+// Four codes x / d, rounded half away from zero; 0 for a row of zeros or one
+// that is not finite.
+__device__ __forceinline__ uint32_t codes_q8(const float4& x, uint32_t a, float d) {
+    if (a == 0u || a >= 0x7f800000u) return 0u;
+    const float v[4] = {x.x, x.y, x.z, x.w};
+    uint32_t packed = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float r = fminf(fmaxf(roundf(v[e] / d), -127.0f), 127.0f);
+        packed |= (static_cast<uint32_t>(static_cast<int>(r)) & 0xffu) << (8 * e);
+    }
+    return packed;
+}
+
+__device__ __forceinline__ uint32_t mag_bits4(const float4& x) {
+    return max(max(mag_bits(x.x), mag_bits(x.y)), max(mag_bits(x.z), mag_bits(x.w)));
+}
+
+// Four floats at p; vec: p is 16-byte aligned.
+__device__ __forceinline__ float4 load4(const float* p, bool vec) {
+    if (vec) return *reinterpret_cast<const float4*>(p);
+    return make_float4(p[0], p[1], p[2], p[3]);
+}
+
+__device__ __forceinline__ void store4(float* p, float4 v, bool vec) {
+    if (vec) {
+        *reinterpret_cast<float4*>(p) = v;
+    } else {
+        p[0] = v.x; p[1] = v.y; p[2] = v.z; p[3] = v.w;
+    }
+}
+
+// A double of another lane by a DPP pattern (0 where the pattern has none).
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ double dpp_f64(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, ROW_MASK, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, ROW_MASK, 0xF, false);
+    return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+}
+
+__device__ __forceinline__ double lane_f64(double v, int lane) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(b), lane);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(b >> 32), lane);
+    return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+}
+
+// Inclusive sum over the lanes, in lane order: within rows of 16 lanes
+// (row_shr 1, 2, 4, 8), then across them (row_bcast 15 and 31).
+__device__ __forceinline__ double wave_prefix(double v) {
+    v += dpp_f64<0x111, 0xF>(v);
+    v += dpp_f64<0x112, 0xF>(v);
+    v += dpp_f64<0x114, 0xF>(v);
+    v += dpp_f64<0x118, 0xF>(v);
+    v += dpp_f64<0x142, 0xA>(v);
+    v += dpp_f64<0x143, 0xC>(v);
+    return v;
+}
+
+__device__ __forceinline__ double wave_add(double v) { return lane_f64(wave_prefix(v), kWave - 1); }
+
+}  // namespace qmv

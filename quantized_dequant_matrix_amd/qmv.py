@@ -87,6 +87,10 @@ KV_Q8, KV_F16 = 0, 1
 QMV_OK, QMV_ERR_NULL, QMV_ERR_SHAPE, QMV_ERR_ALIGN, QMV_ERR_WORKSPACE, QMV_ERR_LAUNCH, QMV_ERR_ARG = range(7)
 
 
+_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 class QmvError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -107,7 +111,7 @@ def _ptr(t):
 
 def _stream(s):
     if s is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_device())  # torch's current stream of the current GPU
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -270,7 +274,7 @@ def _gpu(t):
     """Address of a tensor that the current GPU's kernels can use (a raw address is the caller's word)."""
     if t is None or isinstance(t, int):
         return t
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != _device():
         raise ValueError(f"a tensor on {t.device} was given to a kernel of the current GPU")
     return t.data_ptr()
 
