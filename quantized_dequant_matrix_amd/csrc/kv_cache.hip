@@ -137,7 +137,9 @@ void kv_write_kernel(KvView view, KvPlanes c, const float* __restrict__ k, int64
                 packed.x = __builtin_bit_cast(uint16_t, f[0]) | (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, f[1])) << 16);
                 packed.y = __builtin_bit_cast(uint16_t, f[2]) | (static_cast<uint32_t>(__builtin_bit_cast(uint16_t, f[3])) << 16);
                 if (a >= 0x7f800000u) packed = make_uint2(0x7e007e00u, 0x7e007e00u);
-                if (slot >= 0) reinterpret_cast<uint2*>(codes)[cell * L + sub] = packed;
+                if (slot >= 0)
+                    __builtin_nontemporal_store(packed.x | static_cast<uint64_t>(packed.y) << 32,
+                                                reinterpret_cast<uint64_t*>(codes) + cell * L + sub);
             } else {
                 uint32_t a = mag_bits4(x[i]);
 #pragma unroll
@@ -145,8 +147,8 @@ void kv_write_kernel(KvView view, KvPlanes c, const float* __restrict__ k, int64
                 const float d = scale_q8(a);
                 const uint32_t packed = codes_q8(x[i], a, d);
                 if (slot >= 0) {
-                    reinterpret_cast<uint32_t*>(codes)[cell * L + sub] = packed;
-                    if (sub == 0) scales[cell] = d;
+                    __builtin_nontemporal_store(packed, reinterpret_cast<uint32_t*>(codes) + cell * L + sub);
+                    if (sub == 0) __builtin_nontemporal_store(d, scales + cell);
                 }
             }
         }
@@ -201,7 +203,7 @@ void kv_read_kernel(KvView view, KvPlanes c, float* __restrict__ k, int64_t ldk,
                 x = make_float4(sbyte<0>(p[i].x) * d[i], sbyte<1>(p[i].x) * d[i], sbyte<2>(p[i].x) * d[i],
                                 sbyte<3>(p[i].x) * d[i]);
             }
-            store4(dst + (first + row[i]) * ld + 4 * q[i], x, vec);
+            stream4(dst + (first + row[i]) * ld + 4 * q[i], x, vec);
         }
     }
 }

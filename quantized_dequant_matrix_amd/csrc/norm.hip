@@ -36,8 +36,8 @@ __device__ __forceinline__ float rstd_of(double sum, int64_t K, float eps) {
 
 // One workgroup a row of K = 4 Q elements, the whole row in registers: thread
 // t holds the float4 t, t + threads, ... .  Memory bounds it: 8 bytes in and 8
-// (5.1 with codes) out an element, each once.  2048 rows of 5376: 52 us when
-// the second pass read the row again 4 bytes at a time.
+// (5.1 with codes) out an element, each once.  2048 rows of 5376 take 30 us,
+// 5.9 TB/s (52 us with a second read 4 bytes at a time and plain stores).
 template <int VPT, bool Q8>
 __global__ __launch_bounds__(1024)
 void rmsnorm_row_kernel(const float* x, const float* r, const float* __restrict__ w, float* z, float* __restrict__ y,
@@ -72,7 +72,7 @@ void rmsnorm_row_kernel(const float* x, const float* r, const float* __restrict_
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int i = t + j * threads;
-        if (z && i < Q) store4(z + 4 * (row + i), v[j], vec);
+        if (z && i < Q) stream4(z + 4 * (row + i), v[j], vec);
         const double e[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
         for (int c = 0; c < 4; ++c) sum = fma(e[c], e[c], sum);
@@ -92,11 +92,11 @@ void rmsnorm_row_kernel(const float* x, const float* r, const float* __restrict_
             for (int s = 4; s > 0; s >>= 1) a = max(a, static_cast<uint32_t>(__shfl_xor(static_cast<int>(a), s, 8)));
             if (in) {
                 const float db = scale_q8(a);
-                reinterpret_cast<uint32_t*>(q)[row + i] = codes_q8(o, a, db);
+                __builtin_nontemporal_store(codes_q8(o, a, db), reinterpret_cast<uint32_t*>(q) + row + i);
                 if ((i & 7) == 0) d[(row + i) >> 3] = db;
             }
         } else {
-            if (in) store4(y + 4 * (row + i), o, vec);
+            if (in) stream4(y + 4 * (row + i), o, vec);
         }
     }
 }
@@ -148,13 +148,9 @@ void rmsnorm_kernel(const float* x, const float* r, const float* __restrict__ w,
 hipError_t launch_rmsnorm(const float* x, const float* r, const float* w, float* z, float* y, int8_t* q, float* d,
                           int64_t K, int64_t M, float eps, hipStream_t stream) {
     const dim3 grid(static_cast<unsigned>(M));
-    // One float4 a thread at a time gives a single row the most lanes; many
-    // rows fill the CUs anyway and do better with four in flight a thread.
-    const int64_t Q = K / 4;
-    const int64_t least = M >= 512 ? 4 : 1;
-    int64_t vpt = (Q + 1023) / 1024;
-    vpt = vpt > least ? vpt : least;
-    vpt = vpt <= 1 ? 1 : vpt <= 2 ? 2 : vpt <= 4 ? 4 : 8;
+    // Four float4 a thread where a workgroup holds the row that way: two or
+    // eight differ by less than 10% from it, for one row as for thousands.
+    const int64_t Q = K / 4, vpt = Q <= 4 * 1024 ? 4 : 8;
     if (K % 4 != 0 || Q > 8 * 1024) {
         if (q)
             hipLaunchKernelGGL((rmsnorm_kernel<1024, true>), grid, dim3(1024), 0, stream, x, r, w, z, y, q, d, K, eps);
@@ -176,9 +172,7 @@ hipError_t launch_rmsnorm(const float* x, const float* r, const float* w, float*
             hipLaunchKernelGGL((rmsnorm_row_kernel<V, false>), grid, block, 0, stream, x, r, w, z, y, q, d,        \
                                static_cast<int>(Q), eps, vec);                                                     \
     } while (0)
-    if (vpt == 1) ROW(1);
-    else if (vpt == 2) ROW(2);
-    else if (vpt == 4) ROW(4);
+    if (vpt == 4) ROW(4);
     else ROW(8);
 #undef ROW
     return hipGetLastError();

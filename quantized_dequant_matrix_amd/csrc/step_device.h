@@ -42,11 +42,19 @@ __device__ __forceinline__ float4 load4(const float* p, bool vec) {
     return make_float4(p[0], p[1], p[2], p[3]);
 }
 
-__device__ __forceinline__ void store4(float* p, float4 v, bool vec) {
+// Stores of results that this kernel does not read again, past the L2: a
+// result left dirty there has to be written back when the kernel ends anyway,
+// since the next kernel's readers sit on other XCDs.  The norm of 2048 rows of
+// 5376 takes 30 us with them and 49 us with plain stores.
+typedef float f32x4_nt __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void stream4(float* p, float4 v, bool vec) {
     if (vec) {
-        *reinterpret_cast<float4*>(p) = v;
+        __builtin_nontemporal_store(f32x4_nt{v.x, v.y, v.z, v.w}, reinterpret_cast<f32x4_nt*>(p));
     } else {
-        p[0] = v.x; p[1] = v.y; p[2] = v.z; p[3] = v.w;
+        __builtin_nontemporal_store(v.x, p);
+        __builtin_nontemporal_store(v.y, p + 1);
+        __builtin_nontemporal_store(v.z, p + 2);
+        __builtin_nontemporal_store(v.w, p + 3);
     }
 }
 
