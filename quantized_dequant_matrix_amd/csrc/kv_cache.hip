@@ -7,8 +7,8 @@
 // 4 bytes in and 1 (2) out an element for the write, the reverse for the
 // read.
 //
-// Work split: blockIdx.x is one row of the batch or eight, blockIdx.y keys or
-// values.  D / 4 lanes hold a head's row, four elements each, so that the
+// Work split: blockIdx.x is one row of the batch or a few, blockIdx.y keys
+// or values.  D / 4 lanes hold a head's row, four elements each, so that the
 // row's maximum is a few lane exchanges and a wave writes whole rows of codes.
 #include <stdint.h>
 
@@ -215,24 +215,26 @@ bool vec_rows(const void* k, int64_t ldk, const void* v, int64_t ldv) {
 
 }  // namespace
 
-// A workgroup takes one row of a few, eight rows of many (their places are
-// found together, and more loads are in flight).
-constexpr int kManyRows = 2048, kRowsOfMany = 8;
+// Rows of a workgroup: one of a few; of many, four wide ones or sixteen
+// narrow ones (a row's places are found together, and the rows that a
+// workgroup moves are about 2048 float4).  Whole sequences of 16 heads of 128,
+// 20,527 rows: 69.5 us with four rows, 75.7 with eight, 88.1 with sixteen;
+// 8693 rows of 3 heads of 64: 9.1, 7.4, 7.1 us.
+inline int rows_of(int64_t T, int quads) { return T < 1024 ? 1 : quads >= 256 ? 4 : 16; }
 
-#define KV_LAUNCH(kernel, D, ...)                                                                                      \
-    do {                                                                                                               \
-        const dim3 one(static_cast<unsigned>(b.T), 2), many(static_cast<unsigned>((b.T + kRowsOfMany - 1) / kRowsOfMany), 2); \
-        if (b.T < kManyRows) {                                                                                         \
-            if (c.format == QMV_KV_F16)                                                                                \
-                hipLaunchKernelGGL((kernel<D, true, 1>), one, dim3(kBlockThreads), 0, stream, __VA_ARGS__);            \
-            else                                                                                                       \
-                hipLaunchKernelGGL((kernel<D, false, 1>), one, dim3(kBlockThreads), 0, stream, __VA_ARGS__);           \
-        } else {                                                                                                       \
-            if (c.format == QMV_KV_F16)                                                                                \
-                hipLaunchKernelGGL((kernel<D, true, kRowsOfMany>), many, dim3(kBlockThreads), 0, stream, __VA_ARGS__); \
-            else                                                                                                       \
-                hipLaunchKernelGGL((kernel<D, false, kRowsOfMany>), many, dim3(kBlockThreads), 0, stream, __VA_ARGS__); \
-        }                                                                                                              \
+#define KV_LAUNCH(kernel, D, ...)                                                                               \
+    do {                                                                                                        \
+        const int rows = rows_of(b.T, c.kv_heads * (D / 4));                                                    \
+        const dim3 grid(static_cast<unsigned>((b.T + rows - 1) / rows), 2);                                     \
+        if (c.format == QMV_KV_F16) {                                                                           \
+            if (rows == 1) hipLaunchKernelGGL((kernel<D, true, 1>), grid, dim3(kBlockThreads), 0, stream, __VA_ARGS__); \
+            else if (rows == 4) hipLaunchKernelGGL((kernel<D, true, 4>), grid, dim3(kBlockThreads), 0, stream, __VA_ARGS__); \
+            else hipLaunchKernelGGL((kernel<D, true, 16>), grid, dim3(kBlockThreads), 0, stream, __VA_ARGS__);  \
+        } else {                                                                                                \
+            if (rows == 1) hipLaunchKernelGGL((kernel<D, false, 1>), grid, dim3(kBlockThreads), 0, stream, __VA_ARGS__); \
+            else if (rows == 4) hipLaunchKernelGGL((kernel<D, false, 4>), grid, dim3(kBlockThreads), 0, stream, __VA_ARGS__); \
+            else hipLaunchKernelGGL((kernel<D, false, 16>), grid, dim3(kBlockThreads), 0, stream, __VA_ARGS__); \
+        }                                                                                                       \
     } while (0)
 
 hipError_t launch_kv_write(const qmv_kv_cache& c, const qmv_kv_batch& b, const float* k, int64_t ldk, const float* v,

@@ -19,17 +19,32 @@ __device__ __forceinline__ float scale_q8(uint32_t a) {
 }
 
 // Four codes x / d, rounded half away from zero; 0 for a row of zeros or one
-// that is not finite.
+// that is not finite.  The quotient is taken as x times 1 / d, which is off by
+// at most 127 2^-22 (2 roundings): that decides the code unless the quotient
+// lies within 1e-4 of a border between two, where the wave divides.  (Dividing
+// always: 25.7 against 21.5 us for 3222 rows of 16 heads of 128.)
 __device__ __forceinline__ uint32_t codes_q8(const float4& x, uint32_t a, float d) {
-    if (a == 0u || a >= 0x7f800000u) return 0u;
+    const bool none = a == 0u || a >= 0x7f800000u;
     const float v[4] = {x.x, x.y, x.z, x.w};
+    const float inv = 1.0f / d;
+    float r[4];
+    bool near = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        r[e] = fabsf(v[e] * inv);
+        near |= !(fabsf(__builtin_amdgcn_fractf(r[e]) - 0.5f) > 1e-4f);  // also where 1 / d is no number
+    }
+    if (__ballot(near && !none) != 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[e] = roundf(fabsf(v[e] / d));
+    }
     uint32_t packed = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float r = fminf(fmaxf(roundf(v[e] / d), -127.0f), 127.0f);
-        packed |= (static_cast<uint32_t>(static_cast<int>(r)) & 0xffu) << (8 * e);
+        const int q = static_cast<int>(fminf(r[e] + 0.5f, 127.0f));
+        packed |= (static_cast<uint32_t>(v[e] < 0.0f ? -q : q) & 0xffu) << (8 * e);
     }
-    return packed;
+    return none ? 0u : packed;
 }
 
 __device__ __forceinline__ uint32_t mag_bits4(const float4& x) {
