@@ -67,7 +67,7 @@ constexpr float kInf = __builtin_inff();
 constexpr int kTile = 32;                        // keys of one wave's step
 constexpr int kStep = kTile * kWavesPerBlock;    // keys of the workgroup's step
 constexpr int kUnitShift = 7;                    // a unit of work is one step (more for huge tables)
-constexpr float kQParts = 127.0f * 16384.0f;     // largest |q| in parts: 127 2^14
+constexpr float kQParts = 127.0f * 16384.0f;     // largest |q| in parts: 127 2^14 (its digits: 127, 0, 0)
 constexpr float kSlack = 3.0f;                   // p may reach 2^3 before the maximum moves
 
 struct AttnArgs {
@@ -275,7 +275,8 @@ __device__ __forceinline__ void load_words(uint32_t (&r)[WORDS], const uint8_t* 
 // The two 16-key halves of a tile: the pages they lie in.
 struct Pages {
     int64_t cell[2];  // index of the half's first row in the planes
-    bool ok[2];       // the half has a page
+    bool has[2];      // the half has a page; without one page 0 is read and not seen
+    __device__ __forceinline__ bool ok(int i) const { return has[i]; }
 };
 
 __device__ __forceinline__ Pages pages_of(const AttnArgs& A, int b, int h, int key) {
@@ -286,9 +287,8 @@ __device__ __forceinline__ Pages pages_of(const AttnArgs& A, int b, int h, int k
         const int j = pos >> A.view.page_shift;
         int page = -1;
         if (j < A.view.max_pages) page = A.view.table[static_cast<int64_t>(b) * A.view.max_pages + j];
-        p.ok[i] = page >= 0 && page < A.view.num_pages;
-        page = p.ok[i] ? page : 0;  // read but not seen
-        p.cell[i] = ((static_cast<int64_t>(page) * A.view.heads + h) << A.view.page_shift) +
+        p.has[i] = page >= 0 && page < A.view.num_pages;
+        p.cell[i] = ((static_cast<int64_t>(p.has[i] ? page : 0) * A.view.heads + h) << A.view.page_shift) +
                     (pos & ((1 << A.view.page_shift) - 1));
     }
     return p;
@@ -305,10 +305,11 @@ __device__ __forceinline__ void load_keys(const AttnArgs& A, const Pages& p, KvR
     const int lane = threadIdx.x & (kWave - 1), n = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        const uint8_t* kp = A.k + p.cell[u] * kRow + (n * kRow + g * 16);
+        const int64_t cell = p.cell[u];
+        const uint8_t* kp = A.k + cell * kRow + (n * kRow + g * 16);
 #pragma unroll
         for (int s = 0; s < T::kKLoads; ++s) r.k[u][s] = *reinterpret_cast<const u32x4*>(kp + 64 * s);
-        if constexpr (!F16) r.ks[u] = *reinterpret_cast<const f32x4*>(A.ks + p.cell[u] + 4 * g);
+        if constexpr (!F16) r.ks[u] = *reinterpret_cast<const f32x4*>(A.ks + cell + 4 * g);
     }
 }
 
@@ -319,8 +320,9 @@ __device__ __forceinline__ void load_values(const AttnArgs& A, const Pages& p, K
     const int lane = threadIdx.x & (kWave - 1), n = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        if constexpr (!F16) r.vs[u] = *reinterpret_cast<const f32x4*>(A.vs + p.cell[u] + 4 * g);
-        const uint8_t* vp = A.v + p.cell[u] * kRow + (4 * g * kRow + n * (kRow / 16));
+        const int64_t cell = p.cell[u];
+        if constexpr (!F16) r.vs[u] = *reinterpret_cast<const f32x4*>(A.vs + cell + 4 * g);
+        const uint8_t* vp = A.v + cell * kRow + (4 * g * kRow + n * (kRow / 16));
 #pragma unroll
         for (int e = 0; e < 4; ++e) load_words(r.v[4 * u + e], vp + e * kRow);
     }
@@ -390,20 +392,18 @@ __device__ __forceinline__ void prepare_rows(const AttnArgs& A, Queries<D, F16, 
         const bool real = Q.pos[r] != INT32_MIN;
         W.pos[r] = real ? Q.pos[r] : -1;
         float(&x)[T::kQ][kPer] = Q.x[r];
-        float amax = 0.0f;
-        bool broken = false;
+        // the largest magnitude by its bits: infinity and NaN come out on top
+        uint32_t top = 0;
 #pragma unroll
         for (int s = 0; s < T::kQ; ++s)
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-                if (!real) x[s][e] = 0.0f;
-                amax = fmaxf(amax, fabsf(x[s][e]));
-                broken |= !(fabsf(x[s][e]) < kInf);
-            }
-        amax = row_max(amax);
-        // whole row scaled by a power of two first: amax in [1/2, 1)
-        int k = 0;
-        if (amax > 0.0f && amax < kInf) k = __builtin_amdgcn_frexp_expf(amax);
+            for (int e = 0; e < kPer; ++e) top = max(top, __float_as_uint(x[s][e]) & 0x7fffffffu);
+        top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16, kWave)));
+        top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32, kWave)));
+        W.broken[r] = real && top >= 0x7f800000u;
+        const float amax = top < 0x7f800000u ? __uint_as_float(top) : 0.0f;
+        // the row scaled by a power of two first: amax in [1/2, 1)
+        const int k = amax > 0.0f ? __builtin_amdgcn_frexp_expf(amax) : 0;
         const float an = __builtin_amdgcn_ldexpf(amax, -k);
         float inv, back;
         if constexpr (F16) {
@@ -414,14 +414,11 @@ __device__ __forceinline__ void prepare_rows(const AttnArgs& A, Queries<D, F16, 
             back = an * (1.0f / kQParts);
         }
         W.qs[r] = __builtin_amdgcn_ldexpf(back * A.scale_log2, k);
-        // all scores equal (a zero query or scale), or a row that will be NaN:
-        // zero parts with a factor that keeps masked scores at -infinity
-        W.broken[r] = row_max(broken ? 1.0f : 0.0f) != 0.0f;
-        const bool flat = W.broken[r] || !(W.qs[r] > 0.0f);
-        if (flat) {
-            W.qs[r] = 1.0f;
-            inv = 0.0f;
-        }
+        // all scores equal (a zero query or scale), a row that will be NaN or
+        // one past the item's: zero parts, with a factor that keeps masked
+        // scores at -infinity
+        const bool flat = !real || !(W.qs[r] > 0.0f);
+        if (flat) W.qs[r] = 1.0f;
         inv *= A.sign;
 #pragma unroll
         for (int s = 0; s < T::kQ; ++s) {
@@ -429,33 +426,48 @@ __device__ __forceinline__ void prepare_rows(const AttnArgs& A, Queries<D, F16, 
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
-                    const float a = flat ? 0.0f : __builtin_amdgcn_ldexpf(x[s][e], -k) * inv;
-                    const float b = flat ? 0.0f : __builtin_amdgcn_ldexpf(x[s][e + 1], -k) * inv;
+                    const float a = __builtin_amdgcn_ldexpf(x[s][e], -k) * inv;
+                    const float b = __builtin_amdgcn_ldexpf(x[s][e + 1], -k) * inv;
                     const f16x2 f = {static_cast<_Float16>(a), static_cast<_Float16>(b)};
                     hi[e / 2] = __builtin_bit_cast(uint32_t, f);
                     const f16x2 d = {static_cast<_Float16>(a - static_cast<float>(f[0])),
                                      static_cast<_Float16>(b - static_cast<float>(f[1]))};
                     lo[e / 2] = __builtin_bit_cast(uint32_t, d);
                 }
-                W.q[r][0][s] = u32x4{hi[0], hi[1], hi[2], hi[3]};
-                W.q[r][1][s] = u32x4{lo[0], lo[1], lo[2], lo[3]};
+                W.q[r][0][s] = flat ? u32x4{0, 0, 0, 0} : u32x4{hi[0], hi[1], hi[2], hi[3]};
+                W.q[r][1][s] = flat ? u32x4{0, 0, 0, 0} : u32x4{lo[0], lo[1], lo[2], lo[3]};
             } else {
-                u32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0}, c = {0, 0, 0, 0};
+                // round(x) = a 2^14 + b 2^7 + c with a in [-128, 127], b and c
+                // in [-64, 63]: adding 2^23 + 128 2^14 + 64 2^7 + 64 rounds x
+                // and makes the digits the unsigned bit fields of the
+                // mantissa, each its value plus 128 or 64.
+                constexpr float kDigits = 8388608.0f + 128.0f * 16384.0f + 64.0f * 128.0f + 64.0f;
+                u32x4 a, b, c;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    // x = a 2^14 + b 2^7 + c, b and c in [-64, 63]
-                    const int v = flat ? 0 : static_cast<int>(rintf(__builtin_amdgcn_ldexpf(x[s][e], -k) * inv));
-                    const int vc = ((v + 64) & 127) - 64;
-                    const int v1 = (v - vc) >> 7;
-                    const int vb = ((v1 + 64) & 127) - 64;
-                    const int va = (v1 - vb) >> 7;
-                    a[e / 4] |= (static_cast<uint32_t>(va) & 0xffu) << (8 * (e % 4));
-                    b[e / 4] |= (static_cast<uint32_t>(vb) & 0xffu) << (8 * (e % 4));
-                    c[e / 4] |= (static_cast<uint32_t>(vc) & 0xffu) << (8 * (e % 4));
+                for (int e = 0; e < 16; e += 4) {
+                    uint32_t v[4], w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[i] = __float_as_uint(fmaf(__builtin_amdgcn_ldexpf(x[s][e + i], -k), inv, kDigits));
+                        w[i] = v[i] << 2;  // a in byte 2, b in bits 1 .. 7 of byte 1
+                    }
+                    // the same byte of four words
+                    auto bytes = [](const uint32_t(&x)[4], uint32_t sel) {
+                        return __builtin_amdgcn_perm(__builtin_amdgcn_perm(x[3], x[2], sel),
+                                                     __builtin_amdgcn_perm(x[1], x[0], sel), 0x05040100u);
+                    };
+                    // a 7-bit field u as the byte u - 64
+                    auto minus64 = [](uint32_t u) {
+                        u ^= 0x40404040u;
+                        return u | ((u & 0x40404040u) << 1);
+                    };
+                    a[e / 4] = bytes(w, 0x0c0c0602u) ^ 0x80808080u;
+                    b[e / 4] = minus64((bytes(w, 0x0c0c0501u) >> 1) & 0x7f7f7f7fu);
+                    c[e / 4] = minus64(bytes(v, 0x0c0c0400u) & 0x7f7f7f7fu);
                 }
-                W.q[r][0][s] = a;
-                W.q[r][1][s] = b;
-                W.q[r][2][s] = c;
+                W.q[r][0][s] = flat ? u32x4{0, 0, 0, 0} : a;
+                W.q[r][1][s] = flat ? u32x4{0, 0, 0, 0} : b;
+                W.q[r][2][s] = flat ? u32x4{0, 0, 0, 0} : c;
             }
         }
         W.m[r] = -kInf;
@@ -652,8 +664,15 @@ __device__ __forceinline__ void store_row(const AttnArgs& A, const Seq& S, int h
     }
 }
 
+// Waves a SIMD that the registers have to allow: two (256 registers each),
+// one for 256-wide heads, whose keys, values, queries and results take 32 to 64
+// each (held to 256 registers, a decode step of 8-bit ones takes 32.7 us
+// instead of 30.3).
+template <int D>
+constexpr int kWavesPerSimd = D == 256 ? 1 : 2;
+
 template <int D, bool F16, int R, bool SPLIT>
-__global__ __launch_bounds__(kBlockThreads)
+__global__ __launch_bounds__(kBlockThreads, kWavesPerSimd<D>)
 void attn_kernel(AttnArgs A) {
     constexpr int kRows = 16 * R;
     constexpr int kPad = D + 4;
@@ -734,6 +753,9 @@ void attn_kernel(AttnArgs A) {
         }
         key += wave * kTile;
 
+        // The next tile's pages are looked up, and their addresses formed, a
+        // whole step ahead: formed where the loads start they cost 7% (32
+        // sequences of up to 16384: 247 against 231 us).
         KvRegs<D, F16> kv;
         Pages pg = {};
         const bool any = key < end;
@@ -749,10 +771,11 @@ void attn_kernel(AttnArgs A) {
             for (;;) {
                 const bool more = end - key > kStep;
                 const Pages pt = pages_of(A, b, h, end - key > 2 * kStep ? key + 2 * kStep : key);
-                const bool edge = !(pg.ok[0] && pg.ok[1] && key + kTile <= hi_all && key >= lo_all);
+                const bool edge = !(pg.ok(0) && pg.ok(1) && key + kTile <= hi_all && key >= lo_all);
                 tile_step<D, F16, R>(
-                    A, kv, rows, key, edge, pg.ok[0], pg.ok[1], hi_any, lo_any,
-                    [&] { if (more) load_keys<D, F16>(A, pn, kv); }, [&] { if (more) load_values<D, F16>(A, pn, kv); });
+                    A, kv, rows, key, edge, pg.ok(0), pg.ok(1), hi_any, lo_any,
+                    [&] { if (more) load_keys<D, F16>(A, pn, kv); },
+                    [&] { if (more) load_values<D, F16>(A, pn, kv); });
                 if (!more) break;
                 key += kStep;
                 pg = pn;
@@ -824,7 +847,7 @@ void attn_kernel(AttnArgs A) {
 // blockIdx.x is an item (row tile, head), every kJoinRows-th of its rows from
 // blockIdx.y on is this workgroup's.  D / 4 threads hold a row's dimensions,
 // 1024 / D groups of them share the parts.
-constexpr int kJoinRows = 4;
+constexpr int kJoinRows = 8;
 
 template <int D>
 __global__ __launch_bounds__(kBlockThreads)

@@ -274,7 +274,8 @@ def _gpu(t):
     """Address of a tensor that the current GPU's kernels can use (a raw address is the caller's word)."""
     if t is None or isinstance(t, int):
         return t
-    if not t.is_cuda or t.get_device() != _device():
+    d = t.get_device()  # -1: host memory
+    if d < 0 or d != _device():
         raise ValueError(f"a tensor on {t.device} was given to a kernel of the current GPU")
     return t.data_ptr()
 
