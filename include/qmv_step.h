@@ -110,8 +110,8 @@ int kv_read(const qmv_kv_cache* cache, const qmv_kv_batch* batch, float* k, int6
  * row_start[B] are left as they were.  Positions that a row does not see
  * have no effect on it, whatever they hold.  A row that sees a key or value
  * that is not finite gets NaN in every dimension of the heads that see it.
- * q_heads: a multiple of kv_heads, at most 64 times as many.  scale finite;
- * window >= 0 (0: none).
+ * q_heads: a multiple of kv_heads, at most 64 times as many, and
+ * T * q_heads / 16 + B * kv_heads < 2^24.  scale finite; window >= 0 (0: none).
  * ws: attn_paged_ws_bytes(cache, batch, q_heads) bytes, 16-byte aligned,
  * contents overwritten; the size depends on the descriptors' numbers only,
  * not on the arrays, and is 0 for invalid ones. */

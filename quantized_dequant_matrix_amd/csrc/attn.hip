@@ -863,8 +863,10 @@ void attn_join_kernel(AttnArgs A) {
     const Seq S = sequence<kRows, false>(A, b);
     const int tile = x - first_tile<kRows>(A, b);
     if (tile < 0 || tile >= S.tiles) return;
+    // the item's first workgroup wrote them in this call; a workspace that two
+    // calls share by mistake must not send this one out of it
+    if (own.x < 0 || own.y >= A.workgroups || own.x >= own.y) return;  // (equal: one workgroup, written already)
     const int w0 = own.x, parts = own.y - own.x + 1;
-    if (parts == 1) return;
     const int rows = min(kRows, S.n * A.group - tile * kRows);
     const int share = threadIdx.x / kQuads, quad = threadIdx.x % kQuads;
     const int i0 = parts * share / kShares, i1 = parts * (share + 1) / kShares;
@@ -880,7 +882,7 @@ void attn_join_kernel(AttnArgs A) {
         };
 #pragma unroll 2
         for (int i = i0; i < i1; ++i) {
-            const float* slot = A.part + (2 * static_cast<int64_t>(w0 + i) + (i == 0 ? own.z : 0)) * kSlotFloats<D, R>;
+            const float* slot = A.part + (2 * static_cast<int64_t>(w0 + i) + (i == 0 ? own.z & 1 : 0)) * kSlotFloats<D, R>;
             add(slot[kRows * D + row], slot[kRows * D + kRows + row],
                 *reinterpret_cast<const f32x4*>(slot + row * D + 4 * quad));
         }
@@ -913,7 +915,7 @@ struct AttnPlan {
 // allow no more.
 constexpr int kRound = 512, kRoundWide = 256;
 
-AttnPlan plan_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, int q_heads) {
+AttnPlan plan_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, int q_heads, int window) {
     AttnPlan p;
     const int64_t group = q_heads / c.kv_heads;
     const int64_t seqs = b.B < b.T ? b.B : b.T;
@@ -924,8 +926,19 @@ AttnPlan plan_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, int q_heads) {
         return (x < y ? x : y) * c.kv_heads;
     };
     const int round = c.head_dim == 256 ? kRoundWide : kRound;
-    int64_t items = items_of(16);
-    p.split = items < 2 * round;
+    const int64_t items = items_of(16);
+    // keys of the longest item there can be, and the workgroup's steps over them
+    const int64_t keys = static_cast<int64_t>(b.max_pages) * c.page_size;
+    const int64_t span = window > 0 && window < keys - 64 ? window + 64 : keys;
+    const int64_t steps = (span + kStep - 1) / kStep;
+    // Runs of units cost the second kernel and, where items are many, the
+    // change from one to the next; whole items cost the wait for the longest.
+    // Measured (runs / whole, us): 16 items of 4 steps 11.2 / 8.8, of 8 11.0 /
+    // 13.0; 128 of 8 23 / 16, of 16 24.6 / 24.6; 256 of 8 21 / 17, of 16 26.5 /
+    // 28.4; 512 of 16 47 / 39, of 32 73 / 73, of 64 124 / 138.  Chunks of many
+    // rows have many items of one length and stay whole.
+    const bool chunk = items >= 2 * round && b.T * group >= 64 * seqs;
+    p.split = !chunk && steps * 20 > 80 + items;
     if (!p.split) {
         // Two row tiles share the keys' and values' loads and conversions.
         // Two prompts of 1024 new tokens over 6000, 8 heads of 128: 275 us
@@ -939,7 +952,6 @@ AttnPlan plan_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, int q_heads) {
     p.tiles = b.T * group / 16 + b.B;
     p.workgroups = round;
     // unit numbers fit 31 bits whatever the lengths
-    const int64_t keys = static_cast<int64_t>(b.max_pages) * c.page_size;
     while (items * ((keys >> p.unit_shift) + 1) >= (int64_t{1} << 31)) ++p.unit_shift;
     p.part_bytes = static_cast<size_t>(2 * p.workgroups) * static_cast<size_t>(16 * (c.head_dim + 2)) * sizeof(float);
     p.owner_bytes = static_cast<size_t>(p.tiles * c.kv_heads) * sizeof(int4);
@@ -948,14 +960,15 @@ AttnPlan plan_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, int q_heads) {
 
 }  // namespace
 
+// The size is the same for every window: a window only shortens the items.
 size_t attn_ws_bytes(const qmv_kv_cache& c, const qmv_kv_batch& b, int q_heads) {
-    const AttnPlan p = plan_attn(c, b, q_heads);
+    const AttnPlan p = plan_attn(c, b, q_heads, 0);
     return p.split ? p.part_bytes + p.owner_bytes : 256;
 }
 
 hipError_t launch_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, const float* q, int64_t ldq, float* out,
                        int64_t ldo, int q_heads, float scale, int window, void* ws, hipStream_t stream) {
-    const AttnPlan p = plan_attn(c, b, q_heads);
+    const AttnPlan p = plan_attn(c, b, q_heads, window);
     AttnArgs A;
     A.view = view_of(c, b);
     A.k = static_cast<const uint8_t*>(c.k);

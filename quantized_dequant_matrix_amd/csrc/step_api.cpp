@@ -58,9 +58,11 @@ int check_rows(const void* p, int64_t ld, int64_t width, int64_t T) {
     return aligned(p, 4) ? QMV_OK : QMV_ERR_ALIGN;
 }
 
-int check_q_heads(const qmv_kv_cache& c, int32_t q_heads) {
+int check_q_heads(const qmv_kv_cache& c, const qmv_kv_batch& b, int32_t q_heads) {
     if (q_heads < 1 || q_heads % c.kv_heads != 0 || q_heads / c.kv_heads > 64) return QMV_ERR_SHAPE;
-    return QMV_OK;
+    // a workgroup of 256 threads for every 16 rows of a head and every sequence
+    const int64_t tiles = b.T * (q_heads / c.kv_heads) / 16 + b.B;
+    return tiles * c.kv_heads <= kMaxT ? QMV_OK : QMV_ERR_SHAPE;
 }
 
 int check_norm(const float* x, const float* r, const float* w, const float* z, int64_t K, int64_t M, float eps) {
@@ -99,7 +101,7 @@ int kv_read(const qmv_kv_cache* cache, const qmv_kv_batch* batch, float* k, int6
 
 size_t attn_paged_ws_bytes(const qmv_kv_cache* cache, const qmv_kv_batch* batch, int32_t q_heads) {
     if (!cache || !batch || check_cache_shape(*cache) || check_batch_shape(*cache, *batch) ||
-        check_q_heads(*cache, q_heads))
+        check_q_heads(*cache, *batch, q_heads))
         return 0;
     return qmv::attn_ws_bytes(*cache, *batch, q_heads);
 }
@@ -109,7 +111,7 @@ int attn_paged(const qmv_kv_cache* cache, const qmv_kv_batch* batch, const float
                hipStream_t stream) {
     if (!q || !out || !ws) return QMV_ERR_NULL;
     int rc = check_kv(cache, batch);
-    if (!rc) rc = check_q_heads(*cache, q_heads);
+    if (!rc) rc = check_q_heads(*cache, *batch, q_heads);
     const int64_t width = rc ? 0 : static_cast<int64_t>(q_heads) * cache->head_dim;
     if (!rc) rc = check_rows(q, ldq, width, batch->T);
     if (!rc) rc = check_rows(out, ldo, width, batch->T);

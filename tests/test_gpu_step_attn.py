@@ -1,6 +1,11 @@
 """attn_paged against the plain form in 64 bits, with the error bound that
 step_ref.attention derives: head layouts, page sizes, ragged batches, windows,
-rows that see nothing, what masked places may hold, strides, graphs, streams."""
+rows that see nothing, what masked places may hold, strides, graphs, streams.
+
+A batch whose table is short is computed an item (sequence, rows, head) a
+workgroup; one whose table is long (`wide`: 10,000 positions) in pieces that a
+second kernel joins.  The lengths in the table do not matter for that, so both
+ways are run on the same sequences."""
 import math
 
 import numpy as np
@@ -11,6 +16,7 @@ import step_ref as R
 from gpu_util import DEV, assert_within, dev, host, say
 
 pytestmark = pytest.mark.gpu
+both = pytest.mark.parametrize("wide", [False, True], ids=["whole", "pieces"])
 
 
 def _qmv():
@@ -26,8 +32,10 @@ class Call:
     """A batch over a paged cache on both sides."""
 
     def __init__(self, lens, new, Hq, heads, dim, page, fmt, seed=0, window=0, pad=0, off=0, tail=0, q_scale=1.2,
-                 scale=None, spread=1.0, max_pages=None):
+                 scale=None, spread=1.0, max_pages=None, wide=False):
         rng = np.random.default_rng(seed)
+        if wide:
+            max_pages = 10000 // page
         self.P = R.Pages(lens, heads, dim, page, fmt, rng, spread=spread, max_pages=max_pages)
         self.lens, self.new, self.Hq, self.dim, self.window = lens, new, Hq, dim, window
         self.T, self.width, self.ld, self.off = sum(new) + tail, Hq * dim, Hq * dim + pad, off
@@ -77,31 +85,35 @@ class Call:
         return assert_within(got[:n, : self.width].reshape(ref.shape), ref, tol, what)
 
 
+@both
 @pytest.mark.parametrize("fmt", ["q8", "f16"])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("length", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 257, 700])
-def test_single_token(fmt, dim, length):
-    Call([length], [1], 4, 2, dim, 16, fmt, seed=length).check(f"{fmt} D {dim} length {length}")
+def test_single_token(fmt, dim, length, wide):
+    Call([length], [1], 4, 2, dim, 16, fmt, seed=length, wide=wide).check(f"{fmt} D {dim} length {length}")
 
 
+@both
 @pytest.mark.parametrize("Hq,heads", [(1, 1), (2, 1), (3, 1), (7, 1), (8, 1), (16, 1), (17, 1), (64, 1), (32, 16),
                                       (24, 8), (5, 5), (33, 3)])
 @pytest.mark.parametrize("fmt", ["q8", "f16"])
-def test_head_layouts(Hq, heads, fmt):
-    Call([200, 3], [1, 2], Hq, heads, 64, 32, fmt, seed=Hq).check(f"{fmt} {Hq} over {heads} heads")
+def test_head_layouts(Hq, heads, fmt, wide):
+    Call([200, 3], [1, 2], Hq, heads, 64, 32, fmt, seed=Hq, wide=wide).check(f"{fmt} {Hq} over {heads} heads")
 
 
+@both
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 1024])
 @pytest.mark.parametrize("fmt,dim", [("q8", 128), ("f16", 64)])
-def test_page_sizes(page, fmt, dim):
-    Call([300, 16, 1, 129], [1, 4, 1, 1], 4, 2, dim, page, fmt, seed=page).check(f"{fmt} page {page}")
+def test_page_sizes(page, fmt, dim, wide):
+    Call([300, 16, 1, 129], [1, 4, 1, 1], 4, 2, dim, page, fmt, seed=page, wide=wide).check(f"{fmt} page {page}")
 
 
+@both
 @pytest.mark.parametrize("new,lens", [([8, 8], [8, 700]), ([1, 5, 16, 17], [900, 64, 16, 100]), ([40], [1000]),
                                       ([33, 1, 0, 64], [33, 500, 77, 64]), ([150, 2], [300, 2]), ([300], [300])])
 @pytest.mark.parametrize("fmt,dim", [("q8", 128), ("q8", 64), ("q8", 256), ("f16", 128), ("f16", 256)])
-def test_chunks(new, lens, fmt, dim):
-    Call(lens, new, 4, 2, dim, 32, fmt, seed=sum(new)).check(f"{fmt} D {dim} chunks {new} over {lens}")
+def test_chunks(new, lens, fmt, dim, wide):
+    Call(lens, new, 4, 2, dim, 32, fmt, seed=sum(new), wide=wide).check(f"{fmt} D {dim} chunks {new} over {lens}")
 
 
 @pytest.mark.parametrize("window", [1, 2, 16, 31, 64, 100, 513, 5000])
@@ -111,48 +123,73 @@ def test_windows(window, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["q8", "f16"])
+@pytest.mark.parametrize("window", [1000, 2047])
+def test_long_windows(fmt, window):
+    Call([3000, 90, 2500], [3, 2, 1], 4, 2, 64, 16, fmt, seed=window, window=window).check(f"{fmt} window {window}")
+
+
+@pytest.mark.parametrize("fmt,heads,group", [("q8", 16, 4), ("f16", 16, 4), ("q8", 20, 3)])
+def test_chunks_of_many_rows(fmt, heads, group):
+    """Two row tiles a workgroup (head size 128, many rows a sequence)."""
+    Call([330, 71, 40], [270, 71, 5], heads * group, heads, 128, 32, fmt, seed=heads).check(f"{fmt} {heads} x {group} heads")
+
+
+@pytest.mark.parametrize("dim", [64, 256])
+def test_many_items(dim):
+    """More items than two rounds of workgroups, not of the two-tile kind."""
+    Call([150, 60], [130, 30], 64, 16, dim, 16, "q8", seed=dim).check(f"D {dim}")
+
+
+@pytest.mark.parametrize("fmt", ["q8", "f16"])
 def test_long_context(fmt):
     Call([20011], [1], 4, 2, 128, 64, fmt, seed=1).check(f"{fmt} 20011 positions")
     Call([9000, 40], [3, 3], 2, 1, 128, 64, fmt, seed=2).check(f"{fmt} 9000 and 40 positions")
 
 
+@both
 @pytest.mark.parametrize("fmt", ["q8", "f16"])
-def test_many_short_sequences(fmt):
+def test_many_short_sequences(fmt, wide):
+    """More sequences than a workgroup has threads, empty ones among them."""
     rng = np.random.default_rng(3)
-    lens = rng.integers(1, 60, 150).tolist()
-    Call(lens, [1] * 150, 2, 1, 64, 16, fmt, seed=4).check(f"{fmt} 150 sequences")
+    lens = rng.integers(1, 60, 600).tolist()
+    new = [int(n > 0) for n in rng.integers(0, 4, 600)]
+    Call(lens, new, 2, 1, 64, 16, fmt, seed=4, wide=wide).check(f"{fmt} 600 sequences")
 
 
+@both
 @pytest.mark.parametrize("fmt", ["q8", "f16"])
-def test_empty_sequences_and_rows_behind_the_last(fmt):
+def test_empty_sequences_and_rows_behind_the_last(fmt, wide):
     """No new tokens, no cached tokens, and rows that belong to nobody."""
-    Call([5, 0, 90, 0, 33], [1, 0, 0, 0, 2], 4, 2, 64, 16, fmt, tail=3).check(f"{fmt} empty sequences")
+    Call([5, 0, 90, 0, 33], [1, 0, 0, 0, 2], 4, 2, 64, 16, fmt, tail=3, wide=wide).check(f"{fmt} empty sequences")
 
 
-def test_rows_that_see_nothing():
+@both
+def test_rows_that_see_nothing(wide):
     """More new rows than positions: the first rows' positions are negative.  Their output is zero."""
-    c = Call([3, 20], [6, 1], 4, 2, 64, 16, "q8", seed=5)
+    c = Call([3, 20], [6, 1], 4, 2, 64, 16, "q8", seed=5, wide=wide)
     c.check("negative positions")
     assert (c.result()[:3, : c.width] == 0).all()
-    c = Call([0, 20], [2, 1], 4, 2, 64, 16, "f16", seed=6)
+    c = Call([0, 20], [2, 1], 4, 2, 64, 16, "f16", seed=6, wide=wide)
     c.check("no positions")
     assert (c.result()[:2, : c.width] == 0).all()
 
 
+@both
 @pytest.mark.parametrize("pad,off", [(4, 0), (3, 0), (0, 1), (5, 3)])
-def test_strides_and_alignment(pad, off):
-    Call([100, 33], [2, 1], 4, 2, 128, 16, "q8", seed=7, pad=pad, off=off).check(f"ld + {pad}, base + {off}")
+def test_strides_and_alignment(pad, off, wide):
+    Call([100, 33], [2, 1], 4, 2, 128, 16, "q8", seed=7, pad=pad, off=off, wide=wide).check(f"ld + {pad}, base + {off}")
 
 
+@both
 @pytest.mark.parametrize("fmt", ["q8", "f16"])
-def test_what_masked_places_hold(fmt):
+def test_what_masked_places_hold(fmt, wide):
     """Later tokens of the chunk and tokens before the window hold NaN: rows that do not see them
     are as without, rows that see them are NaN in whole heads."""
     lens, new, window = [90], [40], 30
-    clean = Call(lens, new, 2, 1, 64, 16, fmt, seed=8, window=window)
+    clean = Call(lens, new, 2, 1, 64, 16, fmt, seed=8, window=window, wide=wide)
     ref, tol = clean.reference()
     for j in (10, 55, 70, 89):
-        c = Call(lens, new, 2, 1, 64, 16, fmt, seed=8, window=window)
+        c = Call(lens, new, 2, 1, 64, 16, fmt, seed=8, window=window, wide=wide)
         pg, at = c.P.table[0, j // 16], j % 16
         if fmt == "q8":
             (c.P.vs if j % 2 else c.P.ks)[pg, 0, at] = np.nan
@@ -167,9 +204,10 @@ def test_what_masked_places_hold(fmt):
         assert_within(got[~sees], ref[~sees], tol[~sees], f"{fmt} NaN at {j}")
 
 
+@both
 @pytest.mark.parametrize("fmt", ["q8", "f16"])
-def test_infinite_values_in_masked_places(fmt):
-    c = Call([64], [20], 2, 1, 64, 16, fmt, seed=18)
+def test_infinite_values_in_masked_places(fmt, wide):
+    c = Call([64], [20], 2, 1, 64, 16, fmt, seed=18, wide=wide)
     ref, tol = c.reference()
     pg, at = c.P.table[0, 3], 63 % 16
     if fmt == "q8":
@@ -184,8 +222,9 @@ def test_infinite_values_in_masked_places(fmt):
     assert_within(got[:19], ref[:19], tol[:19], "rows before the infinite one")
 
 
-def test_queries_that_are_not_finite():
-    c = Call([50], [3], 4, 2, 64, 16, "q8", seed=9)
+@both
+def test_queries_that_are_not_finite(wide):
+    c = Call([50], [3], 4, 2, 64, 16, "q8", seed=9, wide=wide)
     ref, tol = c.reference()
     c.q[1, 5] = np.nan           # head 0 of row 1
     c.q[1, 3 * 64 + 1] = np.inf  # head 3
@@ -197,42 +236,46 @@ def test_queries_that_are_not_finite():
     assert_within(got, ref, tol, "heads beside broken ones")
 
 
+@both
 @pytest.mark.parametrize("fmt", ["q8", "f16"])
 @pytest.mark.parametrize("q_scale,scale,spread", [(30.0, 1.0, 1.0), (1e-4, 1.0, 1.0), (1.2, 0.0, 1.0), (1.2, -0.3, 1.0),
                                                   (1.2, 0.1, 1e-3), (1e4, 1e-4, 100.0), (0.0, 1.0, 1.0)])
-def test_magnitudes(fmt, q_scale, scale, spread):
+def test_magnitudes(fmt, q_scale, scale, spread, wide):
     """Sharp and flat softmaxes, tiny and large keys and values, a zero query."""
     Call([500, 40], [2, 1], 4, 2, 128, 16, fmt, seed=10, q_scale=q_scale, scale=scale,
-         spread=spread).check(f"{fmt} q {q_scale} scale {scale} kv {spread}")
+         spread=spread, wide=wide).check(f"{fmt} q {q_scale} scale {scale} kv {spread}")
 
 
-def test_scales_far_apart():
+@both
+def test_scales_far_apart(wide):
     """Values whose scales differ by 10^6 from token to token (a token with tiny values that takes the
     attention, beside tokens with large ones)."""
-    c = Call([300], [2], 4, 2, 64, 16, "q8", seed=11)
+    c = Call([300], [2], 4, 2, 64, 16, "q8", seed=11, wide=wide)
     rng = np.random.default_rng(12)
     fine = ~np.isnan(c.P.vs)
     c.P.vs[fine] *= 10.0 ** rng.uniform(-6, 0, fine.sum()).astype(np.float32)
     c.check("value scales over six decades")
-    c = Call([300], [2], 4, 2, 64, 16, "q8", seed=11)
+    c = Call([300], [2], 4, 2, 64, 16, "q8", seed=11, wide=wide)
     fine = ~np.isnan(c.P.vs)
     c.P.vs[fine] = 0.0
     c.check("all values zero")
 
 
-def test_rising_scores():
+@both
+def test_rising_scores(wide):
     """The running maximum rises at every run of keys, and the weights of the first keys vanish."""
     for sign in (1.0, -1.0):
-        c = Call([800], [1], 1, 1, 64, 16, "f16", seed=13, scale=1.0)
+        c = Call([800], [1], 1, 1, 64, 16, "f16", seed=13, scale=1.0, wide=wide)
         for j in range(800):
             c.P.k[c.P.table[0, j // 16], 0, j % 16] = np.float16(sign * j / 64.0)
         c.q[:] = 0.2
         c.check(f"scores rising {sign}")
 
 
-def test_pages_outside_the_cache_are_not_seen():
+@both
+def test_pages_outside_the_cache_are_not_seen(wide):
     """Positions on a page number outside [0, num_pages) hold nothing."""
-    c = Call([64, 20], [1, 1], 2, 1, 64, 16, "q8", seed=14)
+    c = Call([64, 20], [1, 1], 2, 1, 64, 16, "q8", seed=14, wide=wide)
     hole = list(range(16, 32))
     k, v = c.P.rows("k", 0), c.P.rows("v", 0)
     c.P.table[0, 1] = c.P.num
@@ -292,8 +335,9 @@ def test_cache_beyond_32_bit_offsets():
     assert_within(host(out).reshape(1, heads, dim), ref, tol, "far pages")
 
 
-def test_same_bits_every_time():
-    c = Call([3000, 100, 900], [4, 1, 9], 8, 2, 128, 32, "q8", seed=17).upload()
+@both
+def test_same_bits_every_time(wide):
+    c = Call([3000, 100, 900], [4, 1, 9], 8, 2, 128, 32, "q8", seed=17, wide=wide).upload()
     c.enqueue()
     first = c.result().copy()
     for _ in range(3):

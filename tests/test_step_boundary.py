@@ -124,6 +124,10 @@ def test_attn_arguments():
     assert with_(7, float("nan")) == ARG and with_(7, float("inf")) == ARG and with_(8, -1) == ARG
     assert with_(2, FAKE + 2) == ALIGN and with_(4, FAKE + 2) == ALIGN and with_(9, FAKE + 8) == ALIGN
     assert with_(10, need - 1) == WS
+    big = cache(kv_heads=64)
+    assert call("attn_paged_ws_bytes", ref(big), ref(batch(T=2 ** 23, B=2)), 4096) == 0  # too many workgroups
+    assert call("attn_paged", ref(big), ref(batch(T=2 ** 23, B=2)), FAKE, 2 ** 19, FAKE, 2 ** 19, 4096, 0.1, 0, FAKE, BIG,
+                S) == SHAPE
     for heads in (0, 6, 4 * 65, -4):
         assert call("attn_paged_ws_bytes", ref(c), ref(b), heads) == 0
 
