@@ -32,6 +32,14 @@ CASES = [  # heads, dim, page, fmt, cached before, new rows, ld padding, misalig
     (2, 256, 16, "f16", [15, 16, 17], [18, 1, 30], 0, True),
     (4, 64, 1024, "q8", [1000], [200], 0, False),
     (1, 128, 16, "f16", [0], [300], 0, False),
+    # from 1024 rows on a workgroup takes several: four wide ones, sixteen narrow ones
+    (8, 128, 128, "q8", [3, 0, 700], [1021, 1, 30], 0, False),
+    (5, 256, 64, "f16", [0, 20], [1000, 45], 3, True),
+    (17, 64, 256, "q8", [1, 1], [700, 324], 8, False),
+    (3, 64, 32, "f16", [7, 0, 0, 31], [500, 0, 1, 601], 4, True),
+    (1, 64, 16, "q8", [0, 100], [1030, 17], 0, True),
+    (7, 128, 64, "q8", [50], [1100], 0, False),
+    (3, 256, 16, "f16", [0, 0, 9], [1, 1050, 2], 0, False),
 ]
 
 
@@ -178,6 +186,52 @@ def test_rows_that_are_not_finite_become_nan(fmt):
     for t in (a, c):
         h = host(t).reshape(6, 2, 64)
         assert np.array_equal(np.isnan(h).all(axis=2), bad) and np.array_equal(np.isnan(h).any(axis=2), bad)
+
+
+def test_rows_without_a_place_among_many():
+    """More rows than positions, positions behind the table, rows behind the last sequence, with the
+    rows shared by workgroups: zeros, and rows as they were."""
+    qmv = _qmv()
+    rng = np.random.default_rng(6)
+    for heads in (1, 16):  # sixteen rows a workgroup, four
+        P = R.Pages([640, 640, 640], heads, 64, 64, "q8", rng, max_pages=10)
+        cache, table = P.to_gpu(DEV)
+        new, lens = [500, 451, 300], [397, 1001, 640]
+        T, width = 1260, heads * 64
+        x = rng.normal(0, 1, (T, width)).astype(np.float32)
+        batch = qmv.KVBatch(table, _ints(R.starts(new)), _ints(lens), T)
+        qmv.kv_write(cache, batch, dev(x), width, dev(-x), width)
+        a, c = torch.full((T, width), 3.0, device=DEV), torch.full((T, width), 3.0, device=DEV)
+        qmv.kv_read(cache, batch, a, width, c, width)
+        want = np.full((T, width), 3.0, np.float32)
+        codes, d = R.quantize_rows(x.reshape(T, heads, 64))
+        back = (codes.astype(np.float32) * d[..., None]).reshape(T, width)
+        r = 0
+        for n, L in zip(new, lens):
+            for i in range(n):
+                want[r] = back[r] if 0 <= L - n + i < 640 else 0.0
+                r += 1
+        assert np.array_equal(host(a), want)
+        want[:1251] *= -1.0
+        assert np.array_equal(host(c), want)
+
+
+def test_subnormal_rows():
+    """Rows whose scale has no reciprocal in float32 (below 2^-128)."""
+    qmv = _qmv()
+    rng = np.random.default_rng(7)
+    P = R.Pages([8], 2, 64, 16, "q8", rng)
+    cache, table = P.to_gpu(DEV)
+    x = rng.uniform(0.01, 1.0, (8, 2, 64)) * np.where(rng.random((8, 2, 64)) < 0.5, -1, 1)
+    x *= 10.0 ** -np.array([35.0, 36, 37, 38, 38.5, 39, 40, 41])[:, None, None]
+    x = x.astype(np.float32)
+    assert (x != 0).all()
+    qmv.kv_write(cache, qmv.KVBatch(table, _ints([0, 8]), _ints([8]), 8), dev(x.reshape(8, 128)), 128,
+                 dev(x.reshape(8, 128)), 128)
+    codes, d = R.quantize_rows(x)
+    assert (d > 0).all()
+    for got, want in zip([host(t) for t in cache.tensors], (codes, codes, d, d)):
+        assert np.array_equal(got[P.table[0, 0]][:, :8].swapaxes(0, 1), want)
 
 
 def test_many_sequences():
