@@ -45,8 +45,8 @@
 // itself.  A run covers pieces of items; a piece that is a whole item is
 // written as it is, the first and the last piece of a run may be parts, go to
 // the workspace (two slots a workgroup) and are joined by a second kernel in
-// a fixed order.  Where there are more items than two rounds of workgroups a
-// unit is a whole item and there is no second kernel.
+// a fixed order.  Short tables, many items and chunks of many rows are computed
+// an item a workgroup instead, without a second kernel (plan_attn says where).
 #include <stdint.h>
 
 #include "kv_device.h"
@@ -751,7 +751,9 @@ void attn_kernel(AttnArgs A) {
             const int64_t k0 = S.lo + (static_cast<int64_t>(c0) << A.unit_shift);
             if (k0 > key) key = static_cast<int>(k0 < end ? k0 : end);
         }
-        key += wave * kTile;
+        // a length near 2^31 with a window starts behind every table: there
+        // the first key is `end`, so that nothing below can pass 31 bits
+        key = min(key, max(end, 0)) + wave * kTile;
 
         // The next tile's pages are looked up, and their addresses formed, a
         // whole step ahead: formed where the loads start they cost 7% (32

@@ -307,6 +307,28 @@ def test_lengths_that_lie_are_harmless():
     torch.cuda.synchronize()
 
 
+@both
+@pytest.mark.parametrize("window", [1, 40, 2 ** 31 - 1])
+def test_lengths_near_the_largest_integer(window, wide):
+    """Positions far behind the table: a window there sees nothing, no window (or one of 2^31 - 1) the whole table."""
+    c = Call([64, 64], [1, 3], 4, 2, 64, 16, "q8", seed=24, window=window, max_pages=4, wide=wide)
+    if wide:  # the table's other pages do not exist
+        assert c.P.max_pages * 16 == 10000
+    c.upload()
+    for lens in ([2 ** 31 - 1, 2 ** 31 - 1], [2 ** 31 - 97, 2 ** 31 - 33]):
+        c.out.fill_(9.5)
+        c.len.copy_(_ints(lens))
+        c.enqueue()
+        got = c.result()[:, : c.width].reshape(4, 4, 64)
+        if window < 2 ** 31 - 1:
+            assert (got == 0.0).all()
+            continue
+        q = c.q[:, : c.width].astype(np.float64).reshape(4, 4, 64)
+        for r, b, back in ((0, 0, 1), (1, 1, 3), (2, 1, 2), (3, 1, 1)):
+            ref, tol = R.attention(q[r:r + 1], c.P.rows("k", b), c.P.rows("v", b), [lens[b] - back], c.scale, window)
+            assert_within(got[r:r + 1], ref, tol, f"row {r}")
+
+
 def test_cache_beyond_32_bit_offsets():
     """A cache of more than 2^31 elements, with the sequence's pages at its end."""
     qmv = _qmv()
