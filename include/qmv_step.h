@@ -43,7 +43,9 @@ extern "C" {
  *   an all-zero row has d = 0 and q = 0.
  * QMV_KV_F16: IEEE float16 elements (k_scale and v_scale unused, NULL).
  * A row that holds a NaN or infinity (or a magnitude float16 rounds to
- * infinity) is stored as NaN in whole.
+ * infinity) is stored as NaN in whole.  Pages filled by other means have to
+ * follow this: scales not negative, finite or NaN, rows of float16 finite or
+ * NaN in whole.
  * head_dim is 64, 128 or 256; page_size a power of two in [16, 1024].
  * k, v, k_scale and v_scale are 16-byte aligned. */
 enum { QMV_KV_Q8 = 0, QMV_KV_F16 = 1 };
@@ -73,7 +75,8 @@ typedef struct qmv_kv_cache {
  * to no sequence.  A sequence's positions end with its table: positions
  * from max_pages * page_size on have no place.  The contents of the three
  * arrays are checked where they are used, on the device: a page number
- * outside [0, num_pages) is never followed, its positions hold nothing.
+ * outside [0, num_pages) is never followed, its positions hold nothing, and
+ * row starts out of order leave some or all rows undefined.
  * 1 <= T < 2^24, 1 <= B <= 65535, max_pages * page_size <= 2^30. */
 typedef struct qmv_kv_batch {
     const int32_t* page_table;
@@ -109,7 +112,9 @@ int kv_read(const qmv_kv_cache* cache, const qmv_kv_batch* batch, float* k, int6
  * head_dim).  A row that sees nothing gets zeros; rows at or behind
  * row_start[B] are left as they were.  Positions that a row does not see
  * have no effect on it, whatever they hold.  A row that sees a key or value
- * that is not finite gets NaN in every dimension of the heads that see it.
+ * stored as NaN gets NaN in every dimension of the heads that see it, and so
+ * does a query that is not finite.  Scores are formed from the codes before
+ * they are scaled: 8-bit keys of 2^96 and more may overflow there and give NaN.
  * q_heads: a multiple of kv_heads, at most 64 times as many, and
  * T * q_heads / 16 + B * kv_heads < 2^24.  scale finite; window >= 0 (0: none).
  * ws: attn_paged_ws_bytes(cache, batch, q_heads) bytes, 16-byte aligned,
@@ -169,7 +174,8 @@ int qmm_q4_0_q8(const void* W, const int8_t* q, const float* d, float* y, int64_
  * largest float32.  A drafted token outside [0, V) is not accepted.  Where
  * p_a has no weight at all the drawn token is -1.
  * 1 <= B <= 65535, 1 <= G <= 64, 1 <= V < 2^31, temperature > 0 and finite,
- * softcap >= 0 and finite.
+ * softcap in [0, 65536] (its tanh is taken to 2^-42 of softcap; a larger cap
+ * would lose the logits' last bits, and 0 means none).
  * ws: draft_verify_ws_bytes(B, G, V) bytes, 16-byte aligned, overwritten. */
 size_t draft_verify_ws_bytes(int64_t B, int32_t G, int64_t V);
 int draft_verify(const float* target, int64_t ldt, const float* draft, int64_t ldd, const int32_t* draft_tokens,

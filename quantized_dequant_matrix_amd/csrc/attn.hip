@@ -179,23 +179,27 @@ struct Place {
 };
 
 // Units are numbered by sequence, row tile, head, position.  All 256 threads
-// sum the sequences' units, 256 sequences at a time.
+// sum the sequences' units, 256 sequences at a time.  Row starts that are out
+// of order could make more units than there are numbers: then there is no run.
 template <int ROWS>
 __device__ Place locate(const AttnArgs& A, int w, int* lds /* 5 */, Place* found) {
     const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave;
     const bool one = A.view.B <= kBlockThreads;
     int total = 0;
+    bool ordered = true;  // the same in every thread
     if (t == 0) found->b = A.view.B;
     for (int pass = one ? 1 : 0; pass < 2; ++pass) {  // the sum, then the place
         int base = 0;
         for (int b0 = 0; b0 < A.view.B; b0 += kBlockThreads) {
             Seq s = {};
             int mine = 0;
+            bool disorder = false;
             if (b0 + t < A.view.B) {
                 s = sequence<ROWS, true>(A, b0 + t);
                 mine = s.tiles * A.view.heads * s.units;
+                disorder = A.view.row_start[b0 + t] > A.view.row_start[b0 + t + 1];
             }
-            const int scan = wave_scan(mine);
+            const int scan = __ballot(disorder) == 0 ? wave_scan(mine) : -1;
             __syncthreads();
             if (lane == kWave - 1) lds[wave] = scan;
             __syncthreads();
@@ -203,9 +207,11 @@ __device__ Place locate(const AttnArgs& A, int w, int* lds /* 5 */, Place* found
             for (int i = 0; i < kWavesPerBlock; ++i) {
                 if (i < wave) before += lds[i];
                 base += lds[i];
+                ordered &= lds[i] >= 0;
             }
             if (pass == 0) continue;
             if (one) total = base;
+            if (!ordered) continue;
             const Runs R(total, A.workgroups);
             const int key = w < R.runs ? R.start(w) : -1;
             const int begin = before + scan - mine;

@@ -13,6 +13,8 @@ namespace {
 constexpr int64_t kMaxInt = (int64_t{1} << 31) - 1;
 // one workgroup of 256 threads a row: a grid holds fewer than 2^32 threads
 constexpr int64_t kMaxT = (int64_t{1} << 24) - 1;
+// softcap: tanh is taken to 2^-42, so that a level is off by 2^-26 at most
+constexpr float kMaxCap = 65536.0f;
 constexpr float kMaxFloat = 3.4028234663852886e38f;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -169,7 +171,7 @@ int draft_verify(const float* target, int64_t ldt, const float* draft, int64_t l
     if (!rc) rc = check_rows(draft, ldd, V, B * G);
     if (rc) return rc;
     if (!(temperature > 0.0f) || !(temperature <= kMaxFloat)) return QMV_ERR_ARG;
-    if (!(softcap >= 0.0f) || !(softcap <= kMaxFloat)) return QMV_ERR_ARG;
+    if (!(softcap >= 0.0f) || !(softcap <= kMaxCap)) return QMV_ERR_ARG;
     if (!aligned(draft_tokens, 4) || !aligned(n_draft, 4) || !aligned(u, 4) || !aligned(accepted, 4) ||
         !aligned(tokens, 4) || !aligned(ws, 16))
         return QMV_ERR_ALIGN;

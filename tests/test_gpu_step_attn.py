@@ -307,6 +307,26 @@ def test_lengths_that_lie_are_harmless():
     torch.cuda.synchronize()
 
 
+def test_row_starts_that_make_too_much_work_are_harmless():
+    """Every second sequence claims all rows: more pieces than 31 bits can number, and none is computed."""
+    qmv = _qmv()
+    heads, T, B, pages = 64, 60, 65535, 64
+    k = torch.zeros(1, heads, 1024, 64, dtype=torch.float16, device=DEV)
+    cache = qmv.KVCache(k, k.clone())
+    start = np.zeros(B + 1, np.int32)
+    start[1::2] = T
+    batch = qmv.KVBatch(torch.zeros(B, pages, dtype=torch.int32, device=DEV), _ints(start),
+                        _ints(np.full(B, 2 ** 31 - 1)), T)
+    q = torch.zeros(T, heads * 64, device=DEV)
+    out = torch.empty_like(q)
+    wsb = qmv.attn_paged_ws_bytes(cache, batch, heads)
+    assert wsb > 2 ** 24  # computed in pieces
+    ws = torch.zeros(wsb, dtype=torch.uint8, device=DEV)
+    say("rows claimed by 32768 sequences")
+    qmv.attn_paged(cache, batch, q, heads * 64, out, heads * 64, heads, 0.1, 0, ws, wsb)
+    torch.cuda.synchronize()
+
+
 @both
 @pytest.mark.parametrize("window", [1, 40, 2 ** 31 - 1])
 def test_lengths_near_the_largest_integer(window, wide):

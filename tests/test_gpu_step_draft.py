@@ -66,6 +66,17 @@ def test_plain(B, G, V, T, cap):
     _check(_problem(B, G, V, B + G + V), T, cap)
 
 
+@pytest.mark.parametrize("cap", [0.01, 1000.0, 65536.0])
+def test_small_and_large_caps(cap):
+    """A level cap(y) / T is off by at most 2^-42 cap, so a weight by 2^-42 cap relative to the
+    others and p - q by as much of p: decisions are asked for that lie 8 times that far from a border."""
+    args = _problem(12, 3, 700, 31)
+    acc, out, margin = R.draft_verify(*args[:3], None, args[3], 1.0, cap)
+    assert margin.min() > max(1e-12, cap * 2.0 ** -39)
+    got = _run(*args[:3], None, args[3], 1.0, cap)
+    assert np.array_equal(got[0], acc) and np.array_equal(got[1], out)
+
+
 def test_some_accept_all_and_some_none():
     acc = _check(_problem(200, 3, 500, 9, noise=0.7))
     assert set(acc.tolist()) == {0, 1, 2, 3}

@@ -215,6 +215,13 @@ def test_draft_arguments():
     assert call("draft_verify_ws_bytes", 2, 4, 0) == 0
 
 
+@pytest.mark.parametrize("cap,ok", [(65536.0, True), (65537.0, False), (1e9, False), (3e38, False)])
+def test_draft_softcap_has_a_largest_value(cap, ok):
+    # the workspace is checked last: a call that gets there has passed the cap
+    rc = call("draft_verify", FAKE, 1000, FAKE, 1000, FAKE, FAKE, FAKE, FAKE, FAKE, 2, 4, 1000, 1.0, cap, FAKE, 1, S)
+    assert rc == (WS if ok else ARG)
+
+
 def test_binding_refuses_tensors_of_the_host():
     """An address in host memory would fault the GPU."""
     t = torch.zeros(64)
