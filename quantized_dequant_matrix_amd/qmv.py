@@ -238,11 +238,12 @@ class KVCache:
             raise ValueError("int8 codes need k_scale and v_scale, float32 [num_pages][kv_heads][page_size]")
         if not q8 and any(s is not None for s in scales):
             raise ValueError("a float16 cache has no scales")
-        self.tensors = tuple(t for t in (k, v, *scales) if t is not None)
-        _on_gpu(*self.tensors)
+        self.tensors = tensors = tuple(t for t in (k, v, *scales) if t is not None)
+        _on_gpu(*tensors)
         self.struct = _KVCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.shape[0], k.shape[1], k.shape[3],
                                k.shape[2], KV_Q8 if q8 else KV_F16)
         self.ref = ctypes.addressof(self.struct)
+        self.device = tensors[0].get_device()
 
 
 class KVBatch:
@@ -260,6 +261,7 @@ class KVBatch:
         self.tensors = tensors
         self.struct = _KVBatch(_ptr(page_table), _ptr(row_start), _ptr(kv_len), T, B, page_table.shape[1])
         self.ref = ctypes.addressof(self.struct)
+        self.device = tensors[0].get_device()
 
 
 def _on_gpu(*tensors):
@@ -280,12 +282,20 @@ def _gpu(t):
     return t.data_ptr()
 
 
+def _desc(cache, batch):
+    """Addresses of the two descriptors, whose tensors are on the current GPU."""
+    d = _device()
+    if cache.device != d or batch.device != d:
+        raise ValueError("the descriptors' tensors are on another GPU than the current one")
+    return cache.ref, batch.ref
+
+
 def kv_write(cache, batch, k, ldk, v, ldv, stream=None):
-    _call("kv_write", cache.ref, batch.ref, _gpu(k), ldk, _gpu(v), ldv, _stream(stream))
+    _call("kv_write", *_desc(cache, batch), _gpu(k), ldk, _gpu(v), ldv, _stream(stream))
 
 
 def kv_read(cache, batch, k, ldk, v, ldv, stream=None):
-    _call("kv_read", cache.ref, batch.ref, _gpu(k), ldk, _gpu(v), ldv, _stream(stream))
+    _call("kv_read", *_desc(cache, batch), _gpu(k), ldk, _gpu(v), ldv, _stream(stream))
 
 
 def attn_paged_ws_bytes(cache, batch, q_heads) -> int:
@@ -293,8 +303,8 @@ def attn_paged_ws_bytes(cache, batch, q_heads) -> int:
 
 
 def attn_paged(cache, batch, q, ldq, out, ldo, q_heads, scale, window, ws, ws_bytes, stream=None):
-    _call("attn_paged", cache.ref, batch.ref, _gpu(q), ldq, _gpu(out), ldo, q_heads, scale, window, _gpu(ws), ws_bytes,
-          _stream(stream))
+    _call("attn_paged", *_desc(cache, batch), _gpu(q), ldq, _gpu(out), ldo, q_heads, scale, window, _gpu(ws),
+          ws_bytes, _stream(stream))
 
 
 def rmsnorm_add(x, r, w, z, y, K, M, eps, stream=None):

@@ -248,3 +248,22 @@ def test_binding_checks_descriptors():
     for args in ((t.long(), i, i[:2]), (t, i[:2], i[:2]), (t, i, i), (t[0], i, i[:2])):
         with pytest.raises(ValueError, match="int32|entries"):
             qmv.KVBatch(*args, 1)
+
+
+def test_binding_refuses_descriptors_of_another_gpu(monkeypatch):
+    """Made while one GPU was current, used while another is."""
+    monkeypatch.setattr(qmv, "_device", lambda: 0)
+    objects = []
+    for cls, device in ((qmv.KVCache, 0), (qmv.KVCache, 1), (qmv.KVBatch, 0), (qmv.KVBatch, 1)):
+        o = cls.__new__(cls)
+        o.ref, o.device = FAKE, device
+        objects.append(o)
+    c0, c1, b0, b1 = objects
+    assert qmv._desc(c0, b0) == (FAKE, FAKE)
+    for c, b in ((c1, b0), (c0, b1), (c1, b1)):
+        with pytest.raises(ValueError, match="another GPU"):
+            qmv.kv_write(c, b, FAKE, 64, FAKE, 64, stream=0)
+        with pytest.raises(ValueError, match="another GPU"):
+            qmv.kv_read(c, b, FAKE, 64, FAKE, 64, stream=0)
+        with pytest.raises(ValueError, match="another GPU"):
+            qmv.attn_paged(c, b, FAKE, 64, FAKE, 64, 1, 1.0, 0, FAKE, 256, stream=0)
