@@ -41,3 +41,14 @@ def test_api_argument_checks_under_sanitizers(tmp_path):
                 os.path.join(HERE, "native", "api_host_driver.cpp"),
                 os.path.join(ROOT, "quantized_dequant_matrix_amd", "csrc", "qmv_api.cpp"), "-o", str(exe)], exe, tmp_path)
     assert "api host driver: ok" in out
+
+
+@pytest.mark.skipif(shutil.which("g++") is None or not os.path.isdir("/opt/rocm/include"),
+                    reason="g++ or the HIP headers not available")
+def test_step_argument_checks_under_sanitizers(tmp_path):
+    exe = tmp_path / "step_host_driver"
+    out = _run(["g++", "-std=c++17", *SAN, "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include",
+                "-I" + os.path.join(ROOT, "include"), "-I" + os.path.join(ROOT, "quantized_dequant_matrix_amd", "csrc"),
+                os.path.join(HERE, "native", "step_host_driver.cpp"),
+                os.path.join(ROOT, "quantized_dequant_matrix_amd", "csrc", "step_api.cpp"), "-o", str(exe)], exe, tmp_path)
+    assert "step host driver: ok" in out
