@@ -114,7 +114,8 @@ int kv_read(const qmv_kv_cache* cache, const qmv_kv_batch* batch, float* k, int6
  * have no effect on it, whatever they hold.  A row that sees a key or value
  * stored as NaN gets NaN in every dimension of the heads that see it, and so
  * does a query that is not finite.  Scores are formed from the codes before
- * they are scaled: 8-bit keys of 2^96 and more may overflow there and give NaN.
+ * they are scaled: 8-bit keys of 2^96 and more may overflow there and give
+ * NaN; 8-bit values outside [2^-70, 2^100] lose accuracy.
  * q_heads: a multiple of kv_heads, at most 64 times as many, and
  * T * q_heads / 16 + B * kv_heads < 2^24.  scale finite; window >= 0 (0: none).
  * ws: attn_paged_ws_bytes(cache, batch, q_heads) bytes, 16-byte aligned,

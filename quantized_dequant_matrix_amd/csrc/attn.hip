@@ -587,15 +587,24 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
         if (__ballot(grow) != 0) {
             top = row_max(top);
             const float mn = fmaxf(W.m[r], top);
-            float alpha = W.m[r] == -kInf ? 0.0f : __builtin_amdgcn_exp2f((W.m[r] - mn) * W.qs[r]);
+            const float alpha = W.m[r] == -kInf ? 0.0f : __builtin_amdgcn_exp2f((W.m[r] - mn) * W.qs[r]);
             if constexpr (!F16) {
                 big = max(big, static_cast<uint32_t>(__shfl_xor(static_cast<int>(big), 16, kWave)));
                 big = max(big, static_cast<uint32_t>(__shfl_xor(static_cast<int>(big), 32, kWave)));
                 if (big > W.lim[r]) {
-                    // factor 2^10 / 2^floor(log2 big), good up to four times that power
+                    // factor 2^10 / 2^floor(log2 big), good up to four times that
+                    // power; at most 2^90, so that 2^30 weights of up to 2^3
+                    // times it have a sum
                     const int e = static_cast<int>(big >> 23);
-                    const float lc = static_cast<float>(min(max(137 - e, -117), 127));
-                    alpha *= W.lim[r] == 0 ? 1.0f : __builtin_amdgcn_exp2f(lc - W.lc[r]);
+                    const float lc = static_cast<float>(min(137 - e, 90));
+                    if (W.lim[r] != 0) {
+                        const int by = static_cast<int>(lc - W.lc[r]);  // as far as -207: no float factor
+                        W.l[r] = __builtin_amdgcn_ldexpf(W.l[r], by);
+#pragma unroll
+                        for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) W.o[r][t][i] = __builtin_amdgcn_ldexpf(W.o[r][t][i], by);
+                    }
                     W.lc[r] = lc;
                     W.lim[r] = static_cast<uint32_t>(min(max(e, 1) + 2, 254)) << 23;
                 }

@@ -262,6 +262,25 @@ def test_scales_far_apart(wide):
 
 
 @both
+@pytest.mark.parametrize("first", [1e-36, 1e-30, 0.0, 1e30])
+def test_first_values_of_another_magnitude(first, wide):
+    """A sequence that opens with rows of tiny, zero or huge values, in all waves' tiles."""
+    c = Call([700], [2], 4, 2, 128, 16, "q8", seed=25, wide=wide)
+    for j in range(20):
+        c.P.vs[c.P.table[0, j]] *= np.float32(first)
+    c.check(f"320 rows of values times {first}")
+
+
+@both
+def test_values_from_the_smallest_to_the_largest(wide):
+    """Tiny values whose weights must still count when huge ones follow."""
+    c = Call([700], [2], 4, 2, 128, 16, "q8", seed=26, wide=wide)
+    for j in range(44):
+        c.P.vs[c.P.table[0, j]] *= np.float32(1e-28 if j < 20 else 1e28)
+    c.check("values over 56 decades")
+
+
+@both
 def test_rising_scores(wide):
     """The running maximum rises at every run of keys, and the weights of the first keys vanish."""
     for sign in (1.0, -1.0):
