@@ -597,14 +597,12 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
                     // times it have a sum
                     const int e = static_cast<int>(big >> 23);
                     const float lc = static_cast<float>(min(137 - e, 90));
-                    if (W.lim[r] != 0) {
-                        const int by = static_cast<int>(lc - W.lc[r]);  // as far as -207: no float factor
-                        W.l[r] = __builtin_amdgcn_ldexpf(W.l[r], by);
+                    const int by = static_cast<int>(lc - W.lc[r]);  // as far as -207: no float factor
+                    W.l[r] = __builtin_amdgcn_ldexpf(W.l[r], by);
 #pragma unroll
-                        for (int t = 0; t < D / 16; ++t)
+                    for (int t = 0; t < D / 16; ++t)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) W.o[r][t][i] = __builtin_amdgcn_ldexpf(W.o[r][t][i], by);
-                    }
+                        for (int i = 0; i < 4; ++i) W.o[r][t][i] = __builtin_amdgcn_ldexpf(W.o[r][t][i], by);
                     W.lc[r] = lc;
                     W.lim[r] = static_cast<uint32_t>(min(max(e, 1) + 2, 254)) << 23;
                 }

@@ -271,6 +271,15 @@ def test_first_values_of_another_magnitude(first, wide):
     c.check(f"320 rows of values times {first}")
 
 
+@pytest.mark.parametrize("first", [1e-36, 0.0, 1e30])
+def test_first_values_of_another_magnitude_in_one_pass(first):
+    """... where a wave goes over several of a row's tiles."""
+    c = Call([500], [2], 4, 2, 128, 16, "q8", seed=27)
+    for j in range(20):
+        c.P.vs[c.P.table[0, j]] *= np.float32(first)
+    c.check(f"320 rows of values times {first}")
+
+
 @both
 def test_values_from_the_smallest_to_the_largest(wide):
     """Tiny values whose weights must still count when huge ones follow."""
