@@ -35,6 +35,7 @@ constexpr int kPickThreads = 512, kPickWaves = kPickThreads / kWave;
 constexpr int kStep = 2048;                      // logits of one step of a workgroup of the pick kernel
 constexpr int kGroup = kStep / kPickWaves;       // 256: a wave's share of a step
 constexpr int kDrawThreads = kGroup, kDrawWaves = kDrawThreads / kWave;
+constexpr int kHeld = 4;
 constexpr int kMaxRows = 2 * 64 + 1;        // rows of a sequence: G + 1 target rows, G draft rows
 constexpr double kLog2e = 1.4426950408889634074;
 constexpr float kNegInf = -__builtin_inff();
@@ -373,8 +374,18 @@ void draft_draw_kernel(DraftView D) {
         const double* s = (pass == 0 ? D.rest : D.whole) + b * D.groups;
         double mine = 0.0, total;
         int tail = -1;
+        // a thread's first sums stay in registers for the search (all of
+        // them up to 262,144 logits)
+        double held[kHeld];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) held[i] = g0 + i < g1 ? s[g0 + i] : 0.0;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            mine += held[i];
+            tail = held[i] > 0.0 ? g0 + i : tail;
+        }
 #pragma unroll 4
-        for (int g = g0; g < g1; ++g) {
+        for (int g = g0 + kHeld; g < g1; ++g) {
             const double v = s[g];
             mine += v;
             tail = v > 0.0 ? g : tail;
@@ -392,16 +403,24 @@ void draft_draw_kernel(DraftView D) {
         __syncthreads();
         int hit = INT32_MAX;
         double from = run;
-        if (run + mine > target)
-            for (int g = g0; g < g1; ++g) {
+        if (run + mine > target) {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+                if (hit == INT32_MAX && held[i] > 0.0 && run + held[i] > target) {
+                    hit = g0 + i;
+                    from = run;
+                }
+                run += held[i];
+            }
+            for (int g = g0 + kHeld; g < g1 && hit == INT32_MAX; ++g) {
                 const double v = s[g];
                 if (v > 0.0 && run + v > target) {
                     hit = g;
                     from = run;
-                    break;
                 }
                 run += v;
             }
+        }
         if (hit != INT32_MAX) atomicMin(&found, hit);
         if (tail >= 0) atomicMax(&last, tail);
         __syncthreads();

@@ -60,7 +60,9 @@ def _check(args, T=1.0, cap=0.0, n_draft=None, **kw):
                                          (5, 2, 4096, 0.5, 0.0), (4, 5, 4097, 1.3, 20.0), (2, 8, 50257, 1.0, 0.0),
                                          (40, 3, 1000, 0.7, 30.0), (1, 64, 300, 1.0, 5.0), (300, 2, 65, 1.0, 0.0),
                                          # many sequences of many logits: four steps a workgroup of the second kernel
-                                         (210, 1, 20001, 0.9, 0.0), (150, 2, 28676, 1.0, 30.0)])
+                                         (210, 1, 20001, 0.9, 0.0), (150, 2, 28676, 1.0, 30.0),
+                                         # more groups than the draw's threads hold in registers
+                                         (6, 1, 700001, 1.0, 0.0), (1, 2, 2000000, 1.5, 30.0)])
 def test_plain(B, G, V, T, cap):
     say(f"draft_verify B {B} G {G} V {V} T {T} cap {cap}")
     _check(_problem(B, G, V, B + G + V), T, cap)
