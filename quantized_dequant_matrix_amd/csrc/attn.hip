@@ -956,8 +956,8 @@ AttnPlan plan_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, int q_heads, in
     p.split = !chunk && steps * 20 > 80 + items;
     if (!p.split) {
         // Two row tiles share the keys' and values' loads and conversions.
-        // Two prompts of 1024 new tokens over 6000, 8 heads of 128: 275 us
-        // against 376 us (float16: 309 against 517); 64 wide 129 against
+        // Two prompts of 1024 new tokens over 6000, 8 heads of 128: 290 us
+        // against 393 us (float16: 303 against 517); 64 wide 129 against
         // 126 us, 256 wide 176 against 130 us (registers), and with fewer
         // items than a round (256 new tokens of one prompt) no difference.
         p.r = c.head_dim == 128 && items_of(32) >= kRound && b.T * group >= 64 * seqs ? 2 : 1;
