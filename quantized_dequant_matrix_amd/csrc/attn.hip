@@ -684,13 +684,15 @@ __device__ __forceinline__ void store_row(const AttnArgs& A, const Seq& S, int h
 template <int D>
 constexpr int kWavesPerSimd = D == 256 ? 1 : 2;
 
-template <int D, bool F16, int R, bool SPLIT>
-__global__ __launch_bounds__(kBlockThreads, kWavesPerSimd<D>)
+template <int D, bool F16, int R, bool SPLIT, int WAVES = kWavesPerBlock>
+__global__ __launch_bounds__(WAVES * kWave, kWavesPerSimd<D>)
 void attn_kernel(AttnArgs A) {
     constexpr int kRows = 16 * R;
     constexpr int kPad = D + 4;
-    __shared__ __align__(16) float so[kWavesPerBlock * 16 * kPad];
-    __shared__ float sm[kWavesPerBlock][kRows], sl[kWavesPerBlock][kRows];
+    constexpr int kThreads = WAVES * kWave;
+    constexpr int kStep = kTile * WAVES;  // keys of the workgroup's step
+    __shared__ __align__(16) float so[WAVES * 16 * kPad];
+    __shared__ float sm[WAVES][kRows], sl[WAVES][kRows];
     __shared__ int sums[kWavesPerBlock];
     __shared__ Place place;
     const int lane = threadIdx.x & (kWave - 1), n = lane & 15, g = lane >> 4;
@@ -817,7 +819,7 @@ void attn_kernel(AttnArgs A) {
             __syncthreads();
             float M = -kInf;
 #pragma unroll
-            for (int i = 0; i < kWavesPerBlock; ++i) M = fmaxf(M, sm[i][16 * r + n]);
+            for (int i = 0; i < WAVES; ++i) M = fmaxf(M, sm[i][16 * r + n]);
             const float f = __builtin_amdgcn_exp2f(mq[r] - (M == -kInf ? 0.0f : M) - (F16 ? 10.0f : rows.lc[r])) *
                             (F16 ? 1.0f : 512.0f);
             float* dst = so + (wave * 16 + n) * kPad + 4 * g * (D / 16);
@@ -828,19 +830,19 @@ void attn_kernel(AttnArgs A) {
                     *reinterpret_cast<f32x4*>(dst + e * (D / 16) + t) =
                         f32x4{rows.o[r][t][e], rows.o[r][t + 1][e], rows.o[r][t + 2][e], rows.o[r][t + 3][e]} * f;
             __syncthreads();
-            for (int x = threadIdx.x; x < 16 * (D / 4); x += kBlockThreads) {
+            for (int x = threadIdx.x; x < 16 * (D / 4); x += kThreads) {
                 const int row = x / (D / 4), d = x % (D / 4) * 4;
                 const int rho = (tile * R + r) * 16 + row;
                 if (rho >= S.n * A.group) continue;
                 f32x4 v = *reinterpret_cast<const f32x4*>(so + row * kPad + d);
 #pragma unroll
-                for (int i = 1; i < kWavesPerBlock; ++i)
+                for (int i = 1; i < WAVES; ++i)
                     v += *reinterpret_cast<const f32x4*>(so + (i * 16 + row) * kPad + d);
                 float Mr = -kInf, L = 0.0f;
 #pragma unroll
-                for (int i = 0; i < kWavesPerBlock; ++i) Mr = fmaxf(Mr, sm[i][16 * r + row]);
+                for (int i = 0; i < WAVES; ++i) Mr = fmaxf(Mr, sm[i][16 * r + row]);
 #pragma unroll
-                for (int i = 0; i < kWavesPerBlock; ++i)
+                for (int i = 0; i < WAVES; ++i)
                     L += sl[i][16 * r + row] * __builtin_amdgcn_exp2f(sm[i][16 * r + row] - (Mr == -kInf ? 0.0f : Mr));
                 if (!SPLIT || whole) {
                     store_row<D>(A, S, h, rho, d, v, L);
@@ -920,6 +922,7 @@ void attn_join_kernel(AttnArgs A) {
 struct AttnPlan {
     int r = 1;             // 16-row tiles of a workgroup
     bool split = true;     // units of keys and a second kernel; else whole items
+    int waves = kWavesPerBlock;  // of a workgroup (whole items)
     int unit_shift = kUnitShift;
     int workgroups = 0;    // of the split
     int64_t tiles = 0;     // numbers of row tiles (first_tile)
@@ -948,12 +951,18 @@ AttnPlan plan_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, int q_heads, in
     const int64_t steps = (span + kStep - 1) / kStep;
     // Runs of units cost the second kernel and, where items are many, the
     // change from one to the next; whole items cost the wait for the longest.
-    // Measured (runs / whole, us): 16 items of 4 steps 11.2 / 8.8, of 8 11.0 /
-    // 13.0; 128 of 8 23 / 16, of 16 24.6 / 24.6; 256 of 8 21 / 17, of 16 26.5 /
-    // 28.4; 512 of 16 47 / 39, of 32 73 / 73, of 64 124 / 138.  Chunks of many
+    // One item a CU, or fewer, take eight waves (two on 64-wide heads, whose
+    // registers allow it): 256 items of 9 steps 14.1 us against 18.8 with
+    // four, of 17 21.3 against 30.0, but 320 of 9 22.0 against 18.6.
+    // Runs / whole with eight waves, us: 16 items of 5 steps 10.9 / 9.6, of 9
+    // 11.9 / 12.5, of 17 12.9 / 18.7; 32 of 9 12.2 / 13.1; 128 of 9 19.2 /
+    // 13.5, of 17 20.8 / 19.7, of 33 26.9 / 32.1; 256 of 17 29.5 / 21.3, of 33
+    // 45.7 / 42.1.  With four: 320 of 9 27.2 / 18.6, of 17 32.0 / 30.5, of 33
+    // 52.5 / 62.0; 512 of 17 48.5 / 41.3, of 33 76.0 / 76.6.  Chunks of many
     // rows have many items of one length and stay whole.
     const bool chunk = items >= 2 * round && b.T * group >= 64 * seqs;
-    p.split = !chunk && steps * 20 > 80 + items;
+    const bool eight = c.head_dim <= 128 && items <= (c.head_dim == 64 ? 512 : 256);
+    p.split = !chunk && (eight ? steps * 8 > 36 + items : steps * 20 > 80 + items);
     if (!p.split) {
         // Two row tiles share the keys' and values' loads and conversions.
         // Two prompts of 1024 new tokens over 6000, 8 heads of 128: 290 us
@@ -961,6 +970,7 @@ AttnPlan plan_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, int q_heads, in
         // 126 us, 256 wide 176 against 130 us (registers), and with fewer
         // items than a round (256 new tokens of one prompt) no difference.
         p.r = c.head_dim == 128 && items_of(32) >= kRound && b.T * group >= 64 * seqs ? 2 : 1;
+        p.waves = eight && steps > kWavesPerBlock ? 8 : kWavesPerBlock;
         p.tiles = b.T * group / (16 * p.r) + b.B;
         return p;
     }
@@ -1011,6 +1021,8 @@ hipError_t launch_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, const float
         if (p.split) {                                                                                               \
             hipLaunchKernelGGL((attn_kernel<D, F16, 1, true>), runs, dim3(kBlockThreads), 0, stream, A);             \
             hipLaunchKernelGGL((attn_join_kernel<D>), dim3(items.x, kJoinRows), dim3(kBlockThreads), 0, stream, A);  \
+        } else if (D <= 128 && p.waves == 8) {                                                                       \
+            hipLaunchKernelGGL((attn_kernel<D == 64 ? 64 : 128, F16, 1, false, 8>), items, dim3(8 * kWave), 0, stream, A); \
         } else if (D == 128 && p.r == 2) {                                                                           \
             hipLaunchKernelGGL((attn_kernel<128, F16, 2, false>), items, dim3(kBlockThreads), 0, stream, A);         \
         } else {                                                                                                     \

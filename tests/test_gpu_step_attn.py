@@ -3,9 +3,10 @@ step_ref.attention derives: head layouts, page sizes, ragged batches, windows,
 rows that see nothing, what masked places may hold, strides, graphs, streams.
 
 A batch whose table is short is computed an item (sequence, rows, head) a
-workgroup; one whose table is long (`wide`: 10,000 positions) in pieces that a
-second kernel joins.  The lengths in the table do not matter for that, so both
-ways are run on the same sequences."""
+workgroup, with eight waves where the table is not quite so short (`wide`: 640
+positions) and items are few; one whose table is long (10,000 positions) in
+pieces that a second kernel joins.  The lengths in the table do not matter for
+that, so all ways are run on the same sequences."""
 import math
 
 import numpy as np
@@ -16,7 +17,7 @@ import step_ref as R
 from gpu_util import DEV, assert_within, dev, host, say
 
 pytestmark = pytest.mark.gpu
-both = pytest.mark.parametrize("wide", [False, True], ids=["whole", "pieces"])
+both = pytest.mark.parametrize("wide", [False, 640, True], ids=["whole", "eight", "pieces"])
 
 
 def _qmv():
@@ -34,8 +35,10 @@ class Call:
     def __init__(self, lens, new, Hq, heads, dim, page, fmt, seed=0, window=0, pad=0, off=0, tail=0, q_scale=1.2,
                  scale=None, spread=1.0, max_pages=None, wide=False):
         rng = np.random.default_rng(seed)
-        if wide:
+        if wide is True:
             max_pages = 10000 // page
+        elif wide:
+            max_pages = max(wide, max(lens)) // page + 1
         self.P = R.Pages(lens, heads, dim, page, fmt, rng, spread=spread, max_pages=max_pages)
         self.lens, self.new, self.Hq, self.dim, self.window = lens, new, Hq, dim, window
         self.T, self.width, self.ld, self.off = sum(new) + tail, Hq * dim, Hq * dim + pad, off
@@ -335,6 +338,18 @@ def test_lengths_that_lie_are_harmless():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("fmt,dim,group,window", [("q8", 128, 1, 0), ("q8", 128, 4, 300), ("f16", 128, 2, 0), ("q8", 64, 2, 0),
+                                                  ("f16", 64, 1, 1000), ("q8", 64, 16, 0)])
+def test_eight_waves_over_long_sequences(fmt, dim, group, window):
+    """Few items of up to 17 steps: whole, some waves with several tiles and some with none."""
+    rng = np.random.default_rng(dim + group)
+    lens = rng.integers(1, 2100, 20).tolist()
+    lens[3], lens[11] = 2100, 0
+    new = [min(n, 1 + i % 3) for i, n in enumerate(lens)]
+    Call(lens, new, 8 * group, 8, dim, 64, fmt, seed=group, window=window, tail=2).check(
+        f"{fmt} 20 sequences, {group} x 8 heads of {dim}, window {window}")
+
+
 def test_row_starts_that_make_too_much_work_are_harmless():
     """Every second sequence claims all rows: more pieces than 31 bits can number, and none is computed."""
     qmv = _qmv()
@@ -360,7 +375,7 @@ def test_row_starts_that_make_too_much_work_are_harmless():
 def test_lengths_near_the_largest_integer(window, wide):
     """Positions far behind the table: a window there sees nothing, no window (or one of 2^31 - 1) the whole table."""
     c = Call([64, 64], [1, 3], 4, 2, 64, 16, "q8", seed=24, window=window, max_pages=4, wide=wide)
-    if wide:  # the table's other pages do not exist
+    if wide is True:  # the table's other pages do not exist
         assert c.P.max_pages * 16 == 10000
     c.upload()
     for lens in ([2 ** 31 - 1, 2 ** 31 - 1], [2 ** 31 - 97, 2 ** 31 - 33]):
