@@ -685,7 +685,7 @@ template <int D>
 constexpr int kWavesPerSimd = D == 256 ? 1 : 2;
 
 template <int D, bool F16, int R, bool SPLIT, int WAVES = kWavesPerBlock>
-__global__ __launch_bounds__(WAVES * kWave, kWavesPerSimd<D>)
+__global__ __launch_bounds__(WAVES * kWave, WAVES == 8 ? 2 : kWavesPerSimd<D>)
 void attn_kernel(AttnArgs A) {
     constexpr int kRows = 16 * R;
     constexpr int kPad = D + 4;
@@ -953,7 +953,9 @@ AttnPlan plan_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, int q_heads, in
     // change from one to the next; whole items cost the wait for the longest.
     // One item a CU, or fewer, take eight waves (two on 64-wide heads, whose
     // registers allow it): 256 items of 9 steps 14.1 us against 18.8 with
-    // four, of 17 21.3 against 30.0, but 320 of 9 22.0 against 18.6.
+    // four, of 17 21.3 against 30.0, but 320 of 9 22.0 against 18.6; 256-wide
+    // heads, 256 of 17, 38.5 against 54.0, as float16 (whose registers spill
+    // with two waves a SIMD) 129 against 71.
     // Runs / whole with eight waves, us: 16 items of 5 steps 10.9 / 9.6, of 9
     // 11.9 / 12.5, of 17 12.9 / 18.7; 32 of 9 12.2 / 13.1; 128 of 9 19.2 /
     // 13.5, of 17 20.8 / 19.7, of 33 26.9 / 32.1; 256 of 17 29.5 / 21.3, of 33
@@ -961,7 +963,7 @@ AttnPlan plan_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, int q_heads, in
     // 52.5 / 62.0; 512 of 17 48.5 / 41.3, of 33 76.0 / 76.6.  Chunks of many
     // rows have many items of one length and stay whole.
     const bool chunk = items >= 2 * round && b.T * group >= 64 * seqs;
-    const bool eight = c.head_dim <= 128 && items <= (c.head_dim == 64 ? 512 : 256);
+    const bool eight = !(c.head_dim == 256 && c.format == QMV_KV_F16) && items <= (c.head_dim == 64 ? 512 : 256);
     p.split = !chunk && (eight ? steps * 8 > 36 + items : steps * 20 > 80 + items);
     if (!p.split) {
         // Two row tiles share the keys' and values' loads and conversions.
@@ -1021,8 +1023,8 @@ hipError_t launch_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, const float
         if (p.split) {                                                                                               \
             hipLaunchKernelGGL((attn_kernel<D, F16, 1, true>), runs, dim3(kBlockThreads), 0, stream, A);             \
             hipLaunchKernelGGL((attn_join_kernel<D>), dim3(items.x, kJoinRows), dim3(kBlockThreads), 0, stream, A);  \
-        } else if (D <= 128 && p.waves == 8) {                                                                       \
-            hipLaunchKernelGGL((attn_kernel<D == 64 ? 64 : 128, F16, 1, false, 8>), items, dim3(8 * kWave), 0, stream, A); \
+        } else if (p.waves == 8) {                                                                                   \
+            hipLaunchKernelGGL((attn_kernel<D, F16 && D != 256, 1, false, 8>), items, dim3(8 * kWave), 0, stream, A); \
         } else if (D == 128 && p.r == 2) {                                                                           \
             hipLaunchKernelGGL((attn_kernel<128, F16, 2, false>), items, dim3(kBlockThreads), 0, stream, A);         \
         } else {                                                                                                     \

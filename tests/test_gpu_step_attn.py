@@ -339,7 +339,7 @@ def test_lengths_that_lie_are_harmless():
 
 
 @pytest.mark.parametrize("fmt,dim,group,window", [("q8", 128, 1, 0), ("q8", 128, 4, 300), ("f16", 128, 2, 0), ("q8", 64, 2, 0),
-                                                  ("f16", 64, 1, 1000), ("q8", 64, 16, 0)])
+                                                  ("f16", 64, 1, 1000), ("q8", 64, 16, 0), ("q8", 256, 1, 0), ("f16", 256, 1, 0)])
 def test_eight_waves_over_long_sequences(fmt, dim, group, window):
     """Few items of up to 17 steps: whole, some waves with several tiles and some with none."""
     rng = np.random.default_rng(dim + group)
