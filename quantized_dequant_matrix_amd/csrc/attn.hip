@@ -512,7 +512,14 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[r][4 * u + e] = a[e];
             } else {
-                i32x4 a[3] = {};
+                // sums begin at the bits of 1.5 2^23: as float32 that is 1.5
+                // 2^23 + sum, exactly (|sum| <= 128 127 256 < 2^22), and
+                //   (a - 1.5 2^23 (1 + 129 / 2^14)) 2^14 + (b 2^7 + c)
+                // is a 2^14 + b 2^7 + c, rounded by 2^6 at most inside (a
+                // digit's rounding in the query costs more)
+                constexpr float kBias = 12582912.0f, kOff = kBias + 129.0f * (kBias / 16384.0f);
+                const int c = __float_as_int(kBias);
+                i32x4 a[3] = {i32x4{c, c, c, c}, i32x4{c, c, c, c}, i32x4{c, c, c, c}};
 #pragma unroll
                 for (int i = 0; i < T::kQ; ++i)
 #pragma unroll
@@ -522,8 +529,9 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
                                                                         0, 0, 0);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    s[r][4 * u + e] = fmaf(static_cast<float>(a[0][e]), 16384.0f,
-                                           static_cast<float>((a[1][e] << 7) + a[2][e])) * kv.ks[u][e];
+                    s[r][4 * u + e] = fmaf(__int_as_float(a[0][e]) - kOff, 16384.0f,
+                                           fmaf(__int_as_float(a[1][e]), 128.0f, __int_as_float(a[2][e]))) *
+                                      kv.ks[u][e];
             }
         }
     }
