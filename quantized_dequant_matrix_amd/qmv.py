@@ -87,7 +87,8 @@ KV_Q8, KV_F16 = 0, 1
 QMV_OK, QMV_ERR_NULL, QMV_ERR_SHAPE, QMV_ERR_ALIGN, QMV_ERR_WORKSPACE, QMV_ERR_LAUNCH, QMV_ERR_ARG = range(7)
 
 
-_device = torch._C._cuda_getDevice
+# without a GPU: no tensor's device, so that host tensors are refused as such
+_device = torch._C._cuda_getDevice if torch.cuda.device_count() else lambda: -2
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -266,36 +267,51 @@ class KVBatch:
 
 def _on_gpu(*tensors):
     """The descriptors' tensors are contiguous and on the current GPU."""
+    _gpu(_device(), *tensors)
+    if not all(t.is_contiguous() for t in tensors):
+        raise ValueError("the tensors of a descriptor are contiguous")
+
+
+def _gpu(d, *tensors):
+    """Addresses of tensors that GPU d's kernels can use (a raw address is the caller's word).  The calls below are
+    counted in single microseconds, and d is asked for once in each."""
+    out = []
     for t in tensors:
-        _gpu(t)
-        if not t.is_contiguous():
-            raise ValueError("the tensors of a descriptor are contiguous")
+        if t is None or isinstance(t, int):
+            out.append(t)
+        elif t.get_device() == d:  # -1: host memory
+            out.append(t.data_ptr())
+        else:
+            raise ValueError(f"a tensor on {t.device} was given to a kernel of the current GPU")
+    return out
 
 
-def _gpu(t):
-    """Address of a tensor that the current GPU's kernels can use (a raw address is the caller's word)."""
-    if t is None or isinstance(t, int):
-        return t
-    d = t.get_device()  # -1: host memory
-    if d < 0 or d != _device():
-        raise ValueError(f"a tensor on {t.device} was given to a kernel of the current GPU")
-    return t.data_ptr()
+def _step(name, d, stream, *args):
+    rc = getattr(lib, name)(*args, _raw_stream(d) if stream is None else _stream(stream))
+    if rc != QMV_OK:
+        raise QmvError(rc, name)
 
 
-def _desc(cache, batch):
-    """Addresses of the two descriptors, whose tensors are on the current GPU."""
-    d = _device()
+def _desc(cache, batch, d=None):
+    """Addresses of the two descriptors, whose tensors are on GPU d (the current one)."""
+    d = _device() if d is None else d
     if cache.device != d or batch.device != d:
         raise ValueError("the descriptors' tensors are on another GPU than the current one")
     return cache.ref, batch.ref
 
 
 def kv_write(cache, batch, k, ldk, v, ldv, stream=None):
-    _call("kv_write", *_desc(cache, batch), _gpu(k), ldk, _gpu(v), ldv, _stream(stream))
+    d = _device()
+    c, b = _desc(cache, batch, d)
+    k, v = _gpu(d, k, v)
+    _step("kv_write", d, stream, c, b, k, ldk, v, ldv)
 
 
 def kv_read(cache, batch, k, ldk, v, ldv, stream=None):
-    _call("kv_read", *_desc(cache, batch), _gpu(k), ldk, _gpu(v), ldv, _stream(stream))
+    d = _device()
+    c, b = _desc(cache, batch, d)
+    k, v = _gpu(d, k, v)
+    _step("kv_read", d, stream, c, b, k, ldk, v, ldv)
 
 
 def attn_paged_ws_bytes(cache, batch, q_heads) -> int:
@@ -303,16 +319,20 @@ def attn_paged_ws_bytes(cache, batch, q_heads) -> int:
 
 
 def attn_paged(cache, batch, q, ldq, out, ldo, q_heads, scale, window, ws, ws_bytes, stream=None):
-    _call("attn_paged", *_desc(cache, batch), _gpu(q), ldq, _gpu(out), ldo, q_heads, scale, window, _gpu(ws),
-          ws_bytes, _stream(stream))
+    d = _device()
+    c, b = _desc(cache, batch, d)
+    q, out, ws = _gpu(d, q, out, ws)
+    _step("attn_paged", d, stream, c, b, q, ldq, out, ldo, q_heads, scale, window, ws, ws_bytes)
 
 
 def rmsnorm_add(x, r, w, z, y, K, M, eps, stream=None):
-    _call("rmsnorm_add", _gpu(x), _gpu(r), _gpu(w), _gpu(z), _gpu(y), K, M, eps, _stream(stream))
+    d = _device()
+    _step("rmsnorm_add", d, stream, *_gpu(d, x, r, w, z, y), K, M, eps)
 
 
 def rmsnorm_add_q8(x, r, w, z, q, d, K, M, eps, stream=None):
-    _call("rmsnorm_add_q8", _gpu(x), _gpu(r), _gpu(w), _gpu(z), _gpu(q), _gpu(d), K, M, eps, _stream(stream))
+    dev = _device()
+    _step("rmsnorm_add_q8", dev, stream, *_gpu(dev, x, r, w, z, q, d), K, M, eps)
 
 
 def qmm_q4_0_q8_ws_bytes(N, K, M) -> int:
@@ -320,7 +340,9 @@ def qmm_q4_0_q8_ws_bytes(N, K, M) -> int:
 
 
 def qmm_q4_0_q8(W, q, d, y, N, K, M, ws, ws_bytes, stream=None):
-    _call("qmm_q4_0_q8", _gpu(W), _gpu(q), _gpu(d), _gpu(y), N, K, M, _gpu(ws), ws_bytes, _stream(stream))
+    dev = _device()
+    W, q, d, y, ws = _gpu(dev, W, q, d, y, ws)
+    _step("qmm_q4_0_q8", dev, stream, W, q, d, y, N, K, M, ws, ws_bytes)
 
 
 def draft_verify_ws_bytes(B, G, V) -> int:
@@ -329,5 +351,8 @@ def draft_verify_ws_bytes(B, G, V) -> int:
 
 def draft_verify(target, ldt, draft, ldd, draft_tokens, n_draft, u, accepted, tokens, B, G, V, temperature, softcap, ws,
                  ws_bytes, stream=None):
-    _call("draft_verify", _gpu(target), ldt, _gpu(draft), ldd, _gpu(draft_tokens), _gpu(n_draft), _gpu(u), _gpu(accepted),
-          _gpu(tokens), B, G, V, temperature, softcap, _gpu(ws), ws_bytes, _stream(stream))
+    d = _device()
+    target, draft, draft_tokens, n_draft, u, accepted, tokens, ws = _gpu(d, target, draft, draft_tokens, n_draft, u,
+                                                                         accepted, tokens, ws)
+    _step("draft_verify", d, stream, target, ldt, draft, ldd, draft_tokens, n_draft, u, accepted, tokens, B, G, V,
+          temperature, softcap, ws, ws_bytes)
