@@ -49,6 +49,7 @@
 // an item a workgroup instead, without a second kernel (plan_attn says where).
 #include <stdint.h>
 
+#include "attn_plan.h"
 #include "kv_device.h"
 #include "qmv_internal.h"
 #include "step_internal.h"
@@ -64,9 +65,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_inff();
-constexpr int kTile = 32;                        // keys of one wave's step
-constexpr int kStep = kTile * kWavesPerBlock;    // keys of the workgroup's step
-constexpr int kUnitShift = 7;                    // a unit of work is one step (more for huge tables)
+static_assert(kAttnWaves == kWavesPerBlock && kWaveThreads == kWave && kOwnerBytes == sizeof(int4));
 constexpr float kQParts = 127.0f * 16384.0f;     // largest |q| in parts: 127 2^14 (its digits: 127, 0, 0)
 constexpr float kSlack = 3.0f;                   // p may reach 2^3 before the maximum moves
 
@@ -926,73 +925,6 @@ void attn_join_kernel(AttnArgs A) {
     }
 }
 
-// Everything about a call that depends on the descriptors' numbers.
-struct AttnPlan {
-    int r = 1;             // 16-row tiles of a workgroup
-    bool split = true;     // units of keys and a second kernel; else whole items
-    int waves = kWavesPerBlock;  // of a workgroup (whole items)
-    int unit_shift = kUnitShift;
-    int workgroups = 0;    // of the split
-    int64_t tiles = 0;     // numbers of row tiles (first_tile)
-    size_t part_bytes = 0, owner_bytes = 0;
-};
-
-// Workgroups of one round: two on each of 256 CUs, one where the registers
-// allow no more.
-constexpr int kRound = 512, kRoundWide = 256;
-
-AttnPlan plan_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, int q_heads, int window) {
-    AttnPlan p;
-    const int64_t group = q_heads / c.kv_heads;
-    const int64_t seqs = b.B < b.T ? b.B : b.T;
-    // the items that there can be with `rows` rows a tile: sum of
-    // ceil(n group / rows) over the sequences, for any split of T rows
-    auto items_of = [&](int64_t rows) {
-        const int64_t x = b.T * ((group + rows - 1) / rows), y = (b.T * group + seqs * (rows - 1)) / rows;
-        return (x < y ? x : y) * c.kv_heads;
-    };
-    const int round = c.head_dim == 256 ? kRoundWide : kRound;
-    const int64_t items = items_of(16);
-    // keys of the longest item there can be, and the workgroup's steps over them
-    const int64_t keys = static_cast<int64_t>(b.max_pages) * c.page_size;
-    const int64_t span = window > 0 && window < keys - 64 ? window + 64 : keys;
-    const int64_t steps = (span + kStep - 1) / kStep;
-    // Runs of units cost the second kernel and, where items are many, the
-    // change from one to the next; whole items cost the wait for the longest.
-    // One item a CU, or fewer, take eight waves (two on 64-wide heads, whose
-    // registers allow it): 256 items of 9 steps 14.1 us against 18.8 with
-    // four, of 17 21.3 against 30.0, but 320 of 9 22.0 against 18.6; 256-wide
-    // heads, 256 of 17, 38.5 against 54.0, as float16 (whose registers spill
-    // with two waves a SIMD) 129 against 71.
-    // Runs / whole with eight waves, us: 16 items of 5 steps 10.9 / 9.6, of 9
-    // 11.9 / 12.5, of 17 12.9 / 18.7; 32 of 9 12.2 / 13.1; 128 of 9 19.2 /
-    // 13.5, of 17 20.8 / 19.7, of 33 26.9 / 32.1; 256 of 17 29.5 / 21.3, of 33
-    // 45.7 / 42.1.  With four: 320 of 9 27.2 / 18.6, of 17 32.0 / 30.5, of 33
-    // 52.5 / 62.0; 512 of 17 48.5 / 41.3, of 33 76.0 / 76.6.  Chunks of many
-    // rows have many items of one length and stay whole.
-    const bool chunk = items >= 2 * round && b.T * group >= 64 * seqs;
-    const bool eight = !(c.head_dim == 256 && c.format == QMV_KV_F16) && items <= (c.head_dim == 64 ? 512 : 256);
-    p.split = !chunk && (eight ? steps * 8 > 36 + items : steps * 20 > 80 + items);
-    if (!p.split) {
-        // Two row tiles share the keys' and values' loads and conversions.
-        // Two prompts of 1024 new tokens over 6000, 8 heads of 128: 290 us
-        // against 393 us (float16: 303 against 517); 64 wide 129 against
-        // 126 us, 256 wide 176 against 130 us (registers), and with fewer
-        // items than a round (256 new tokens of one prompt) no difference.
-        p.r = c.head_dim == 128 && items_of(32) >= kRound && b.T * group >= 64 * seqs ? 2 : 1;
-        p.waves = eight && steps > kWavesPerBlock ? 8 : kWavesPerBlock;
-        p.tiles = b.T * group / (16 * p.r) + b.B;
-        return p;
-    }
-    p.tiles = b.T * group / 16 + b.B;
-    p.workgroups = round;
-    // unit numbers fit 31 bits whatever the lengths
-    while (items * ((keys >> p.unit_shift) + 1) >= (int64_t{1} << 31)) ++p.unit_shift;
-    p.part_bytes = static_cast<size_t>(2 * p.workgroups) * static_cast<size_t>(16 * (c.head_dim + 2)) * sizeof(float);
-    p.owner_bytes = static_cast<size_t>(p.tiles * c.kv_heads) * sizeof(int4);
-    return p;
-}
-
 }  // namespace
 
 // The size is the same for every window: a window only shortens the items.
@@ -1024,19 +956,19 @@ hipError_t launch_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, const float
     A.workgroups = p.workgroups;
     A.vec_q = (reinterpret_cast<uintptr_t>(q) & 15) == 0 && ldq % 4 == 0;
     A.vec_o = (reinterpret_cast<uintptr_t>(out) & 15) == 0 && ldo % 4 == 0;
-    const dim3 items(static_cast<unsigned>(p.tiles * c.kv_heads));
-    const dim3 runs(static_cast<unsigned>(p.workgroups));
+    const dim3 grid(static_cast<unsigned>(p.blocks(c))), threads(static_cast<unsigned>(p.threads()));
+    const dim3 join(static_cast<unsigned>(p.join_blocks(c)), kJoinRows);
 #define ATTN(D, F16)                                                                                                 \
     do {                                                                                                             \
         if (p.split) {                                                                                               \
-            hipLaunchKernelGGL((attn_kernel<D, F16, 1, true>), runs, dim3(kBlockThreads), 0, stream, A);             \
-            hipLaunchKernelGGL((attn_join_kernel<D>), dim3(items.x, kJoinRows), dim3(kBlockThreads), 0, stream, A);  \
+            hipLaunchKernelGGL((attn_kernel<D, F16, 1, true>), grid, threads, 0, stream, A);                         \
+            hipLaunchKernelGGL((attn_join_kernel<D>), join, dim3(kBlockThreads), 0, stream, A);                      \
         } else if (p.waves == 8) {                                                                                   \
-            hipLaunchKernelGGL((attn_kernel<D, F16 && D != 256, 1, false, 8>), items, dim3(8 * kWave), 0, stream, A); \
+            hipLaunchKernelGGL((attn_kernel<D, F16 && D != 256, 1, false, 8>), grid, threads, 0, stream, A);         \
         } else if (D == 128 && p.r == 2) {                                                                           \
-            hipLaunchKernelGGL((attn_kernel<128, F16, 2, false>), items, dim3(kBlockThreads), 0, stream, A);         \
+            hipLaunchKernelGGL((attn_kernel<128, F16, 2, false>), grid, threads, 0, stream, A);                      \
         } else {                                                                                                     \
-            hipLaunchKernelGGL((attn_kernel<D, F16, 1, false>), items, dim3(kBlockThreads), 0, stream, A);           \
+            hipLaunchKernelGGL((attn_kernel<D, F16, 1, false>), grid, threads, 0, stream, A);                        \
         }                                                                                                            \
     } while (0)
     if (c.format == QMV_KV_F16) {

@@ -63,6 +63,7 @@ int check_rows(const void* p, int64_t ld, int64_t width, int64_t T) {
 int check_q_heads(const qmv_kv_cache& c, const qmv_kv_batch& b, int32_t q_heads) {
     if (q_heads < 1 || q_heads % c.kv_heads != 0 || q_heads / c.kv_heads > 64) return QMV_ERR_SHAPE;
     // a workgroup of 256 threads for every 16 rows of a head and every sequence
+    // (one of 512 only where those fit a launch too: plan_attn)
     const int64_t tiles = b.T * (q_heads / c.kv_heads) / 16 + b.B;
     return tiles * c.kv_heads <= kMaxT ? QMV_OK : QMV_ERR_SHAPE;
 }

@@ -1,0 +1,45 @@
+"""Calls at the edges of the documented ranges: they are computed, not refused."""
+import numpy as np
+import pytest
+import torch
+
+import step_ref as R
+from gpu_util import DEV, assert_within, dev, host, say
+
+pytestmark = pytest.mark.gpu
+
+
+def _qmv():
+    from quantized_dequant_matrix_amd import qmv
+    return qmv
+
+
+def _ints(a):
+    return torch.from_numpy(np.asarray(a, dtype=np.int32)).to(DEV)
+
+
+@pytest.mark.parametrize("T,heads,dim,fmt,length", [(1, 255, 128, "q8", 1024), (2, 130, 64, "f16", 700)])
+def test_attention_of_few_rows_among_very_many_sequences(T, heads, dim, fmt, length):
+    """65,535 sequences of which one or two have rows: few items, and a workgroup for every sequence and head."""
+    qmv = _qmv()
+    say(f"attn T {T}, 65535 sequences, {heads} heads of {dim} {fmt}")
+    rng = np.random.default_rng(heads)
+    B, page = 65535, 16
+    P = R.Pages([length], heads, dim, page, fmt, rng, max_pages=64)
+    t = [None if a is None else dev(a) for a in (P.k, P.v, P.ks, P.vs)]
+    cache = qmv.KVCache(*t)
+    at = 40000  # the sequence that has the rows
+    table = np.full((B, 64), -1, np.int32)
+    table[at] = P.table[0]
+    start, lens = np.zeros(B + 1, np.int32), np.zeros(B, np.int32)
+    start[at + 1:] = T
+    lens[at] = length
+    batch = qmv.KVBatch(_ints(table), _ints(start), _ints(lens), T)
+    q = rng.normal(0, 1.2, (T, heads * dim)).astype(np.float32)
+    out = torch.full((T, heads * dim), 9.5, device=DEV)
+    wsb = qmv.attn_paged_ws_bytes(cache, batch, heads)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=DEV)
+    qmv.attn_paged(cache, batch, dev(q), heads * dim, out, heads * dim, heads, dim ** -0.5, 0, ws, wsb)
+    ref, tol = R.attention(q.astype(np.float64).reshape(T, heads, dim), P.rows("k", 0), P.rows("v", 0),
+                           [length - T + i for i in range(T)], dim ** -0.5, 0)
+    assert_within(host(out).reshape(ref.shape), ref, tol, "few rows, many sequences")
