@@ -3,7 +3,7 @@
 //   s_j = scale q . k_j over the visible positions j,
 //   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(s_j - max s)
 //
-// One pass over keys and values with the running maximum and sum of the
+// One pass over keys and values with a running reference and sum of the
 // softmax.  For few rows the cache's bytes bound it, for a chunk of many rows
 // the matrix instructions and the conversions that feed them.
 //
@@ -32,9 +32,13 @@
 //     (v_mfma_i32_16x16x64_i8, no conversion of K at all); the key's scale
 //     multiplies the finished score.
 //   float16 keys: q as two float16 terms (22 bits).
-//   p: two float16 terms.  The scale of a value row is multiplied into p
-//     before the split, relative to a power of two near the largest scale
-//     the row has seen (float16 has too few exponents for it otherwise).
+//   p: two float16 terms, the scale of a value row multiplied in before the
+//     split.  float16 has few exponents, so what is split is p dv 2^-c with a
+//     reference c of the row's own, a whole number: where c moves, the
+//     largest p dv comes to lie in [2^10, 2^12), and it may grow to 2^15
+//     before c moves again.  The second term ends at 2^-24, 2^-34 of the
+//     largest product of a weight and a value's scale: a large value that
+//     weighs nothing takes nothing from the others.
 //     8-bit codes become float16 exactly: a byte u = code + 128 read as a
 //     float16 is u 2^-24, and one fused multiply-add makes it
 //     (u - 128) 2^-9.
@@ -67,7 +71,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_inff();
 static_assert(kAttnWaves == kWavesPerBlock && kWaveThreads == kWave && kOwnerBytes == sizeof(int4));
 constexpr float kQParts = 127.0f * 16384.0f;     // largest |q| in parts: 127 2^14 (its digits: 127, 0, 0)
-constexpr float kSlack = 3.0f;                   // p may reach 2^3 before the maximum moves
+// Weights are exp2(score - c), c the row's reference (tile_step):
+constexpr float kTop = 10.0f;                    // log2 of the largest p dv where c is set, rounded down
+constexpr float kTopMax = 15.0f;                 // ... and without a move: float16 holds it
+constexpr float kPTop = 80.0f, kPMax = 90.0f;    // the same of p itself (values of zero would ask for any)
+constexpr float kNoRef = -3.4028234663852886e38f;  // c before any key: the first weight is infinite and sets it
 
 struct AttnArgs {
     KvView view;
@@ -245,6 +253,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+__device__ __forceinline__ float largest(const float (&x)[8]) {
+    return fmaxf(max3(x[0], x[1], max3(x[2], x[3], x[4])), max3(x[5], x[6], x[7]));
+}
+
 __device__ __forceinline__ uint32_t pk(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
 }
@@ -333,6 +345,11 @@ __device__ __forceinline__ void load_values(const AttnArgs& A, const Pages& p, K
     }
 }
 
+// What sums under reference `from` are multiplied by, as a power of two, to
+// stand under `to`.  A factor of 2^-150 is met (tiny values before huge ones)
+// and its sums still count: float32 holds the results but not the factor.
+__device__ __forceinline__ int rebase(float from, float to) { return static_cast<int>(fmaxf(from - to, -1000.0f)); }
+
 // The rows of a workgroup as each wave holds them.
 template <int D, bool F16, int R>
 struct Rows {
@@ -343,10 +360,8 @@ struct Rows {
     bool broken[R];  // the query is not finite
     int pos[R];    // position of the lane's row, -1 for a row past the item's
     f32x4 o[R][D / 16];
-    float m[R];    // running maximum, before qs
-    float l[R];    // this lane's share of the sum
-    float lc[R];   // 8-bit values: log2 of the power of two in every p
-    uint32_t lim[R];  // ... and the largest value scale it is good for, as bits
+    float c[R];    // reference of the weights, log2: a whole number, so that changing it rounds nothing
+    float l[R];    // this lane's share of their sum
 };
 
 // q of the lane's rows, 16 (8 for float16) dimensions at a time as the
@@ -475,10 +490,8 @@ __device__ __forceinline__ void prepare_rows(const AttnArgs& A, Queries<D, F16, 
                 W.q[r][2][s] = flat ? u32x4{0, 0, 0, 0} : c;
             }
         }
-        W.m[r] = -kInf;
+        W.c[r] = kNoRef;
         W.l[r] = 0.0f;
-        W.lc[r] = 0.0f;
-        W.lim[r] = 0;
 #pragma unroll
         for (int t = 0; t < D / 16; ++t) W.o[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
@@ -561,6 +574,16 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
         }
     }
 
+    // how far above the reference a score may lie: p dv within float16, and p
+    // so that 2^30 of them have a sum
+    float limit = kTopMax;
+    if constexpr (!F16) {
+        float vs[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) vs[e] = kv.vs[e >> 2][e & 3];
+        limit = fminf(kTopMax - __builtin_amdgcn_logf(largest(vs)), kPMax);
+    }
+
     uint32_t ph[R][4], pl[R][4];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -581,50 +604,36 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
                 }
             }
         }
-        float top = fmaxf(max3(s[r][0], s[r][1], max3(s[r][2], s[r][3], s[r][4])), max3(s[r][5], s[r][6], s[r][7]));
-        // scales are never negative: they compare as their bits (NaN above all)
-        uint32_t big = 0;
-        if constexpr (!F16) {
+        // The reference moves only when a row has outgrown it, or could have by
+        // the lane's largest score and value scale.  (NaN is never above: it
+        // stays in the sum or the products.)
+        if (__ballot(fmaf(largest(s[r]), W.qs[r], -W.c[r]) > limit) != 0) {
+            // the largest p dv becomes 2^10 .. 2^12 (log2 dv rounded down to the
+            // exponent), unless p itself would pass 2^81
+            float cn = W.c[r];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) big = max(big, __float_as_uint(dv[e]));
-        }
-        // The maximum and the factor of the value scales move only when a
-        // row has outgrown them: p and its products stay within float16.
-        const bool grow = (top - W.m[r]) * W.qs[r] > kSlack || big > W.lim[r];
-        if (__ballot(grow) != 0) {
-            top = row_max(top);
-            const float mn = fmaxf(W.m[r], top);
-            const float alpha = W.m[r] == -kInf ? 0.0f : __builtin_amdgcn_exp2f((W.m[r] - mn) * W.qs[r]);
-            if constexpr (!F16) {
-                big = max(big, static_cast<uint32_t>(__shfl_xor(static_cast<int>(big), 16, kWave)));
-                big = max(big, static_cast<uint32_t>(__shfl_xor(static_cast<int>(big), 32, kWave)));
-                if (big > W.lim[r]) {
-                    // factor 2^10 / 2^floor(log2 big), good up to four times that
-                    // power; at most 2^90, so that 2^30 weights of up to 2^3
-                    // times it have a sum
-                    const int e = static_cast<int>(big >> 23);
-                    const float lc = static_cast<float>(min(137 - e, 90));
-                    const int by = static_cast<int>(lc - W.lc[r]);  // as far as -207: no float factor
-                    W.l[r] = __builtin_amdgcn_ldexpf(W.l[r], by);
-#pragma unroll
-                    for (int t = 0; t < D / 16; ++t)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) W.o[r][t][i] = __builtin_amdgcn_ldexpf(W.o[r][t][i], by);
-                    W.lc[r] = lc;
-                    W.lim[r] = static_cast<uint32_t>(min(max(e, 1) + 2, 254)) << 23;
+            for (int e = 0; e < 8; ++e) {
+                const float x = s[r][e] * W.qs[r];
+                if constexpr (F16) {
+                    cn = fmaxf(cn, x - kTop);
+                } else {
+                    const int exponent = static_cast<int>(__float_as_uint(dv[e]) >> 23) - 127;
+                    cn = fmaxf(cn, fmaxf(x + (static_cast<float>(exponent) - kTop), x - kPTop));
                 }
             }
-            W.m[r] = mn;
-            W.l[r] *= alpha;
+            cn = floorf(row_max(cn));
+            const int by = rebase(W.c[r], cn);
+            W.c[r] = cn;
+            W.l[r] = __builtin_amdgcn_ldexpf(W.l[r], by);
 #pragma unroll
-            for (int t = 0; t < D / 16; ++t) W.o[r][t] *= alpha;
+            for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) W.o[r][t][i] = __builtin_amdgcn_ldexpf(W.o[r][t][i], by);
         }
-        // p, with the factor in it
-        const float shift = (W.m[r] == -kInf ? 0.0f : W.m[r] * W.qs[r]) - (F16 ? 10.0f : W.lc[r]);
         float p[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            p[e] = __builtin_amdgcn_exp2f(fmaf(s[r][e], W.qs[r], -shift));
+            p[e] = __builtin_amdgcn_exp2f(fmaf(s[r][e], W.qs[r], -W.c[r]));
             W.l[r] += p[e];
             if constexpr (!F16) p[e] *= dv[e];
         }
@@ -666,7 +675,8 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
     reload_values();
 }
 
-// Floats of one partial slot: 16 R rows of D sums, then their maxima, then sums.
+// Floats of one partial slot: 16 R rows of D sums, then their references, then
+// the sums of their weights.
 template <int D, int R>
 constexpr int kSlotFloats = 16 * R * (D + 2);
 
@@ -807,15 +817,13 @@ void attn_kernel(AttnArgs A) {
             }
         }
 
-        // join the four waves, 16 rows at a time
-        float mq[R];
+        // join the waves, 16 rows at a time
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            mq[r] = rows.m[r] == -kInf ? -kInf : rows.m[r] * rows.qs[r];
-            float l = row_sum(rows.l[r]) * __builtin_amdgcn_exp2f(F16 ? -10.0f : -rows.lc[r]);
-            if (rows.broken[r] && rows.m[r] != -kInf) l = __uint_as_float(0x7fc00000u);
+            float l = row_sum(rows.l[r]);
+            if (rows.broken[r] && l != 0.0f) l = __uint_as_float(0x7fc00000u);
             if (g == 0) {
-                sm[wave][16 * r + n] = mq[r];
+                sm[wave][16 * r + n] = rows.c[r];
                 sl[wave][16 * r + n] = l;
             }
         }
@@ -824,18 +832,18 @@ void attn_kernel(AttnArgs A) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             __syncthreads();
-            float M = -kInf;
+            float M = kNoRef;
 #pragma unroll
             for (int i = 0; i < WAVES; ++i) M = fmaxf(M, sm[i][16 * r + n]);
-            const float f = __builtin_amdgcn_exp2f(mq[r] - (M == -kInf ? 0.0f : M) - (F16 ? 10.0f : rows.lc[r])) *
-                            (F16 ? 1.0f : 512.0f);
+            const int f = rebase(rows.c[r], M) + (F16 ? 0 : 9);
             float* dst = so + (wave * 16 + n) * kPad + 4 * g * (D / 16);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
                 for (int t = 0; t < D / 16; t += 4)
                     *reinterpret_cast<f32x4*>(dst + e * (D / 16) + t) =
-                        f32x4{rows.o[r][t][e], rows.o[r][t + 1][e], rows.o[r][t + 2][e], rows.o[r][t + 3][e]} * f;
+                        f32x4{__builtin_amdgcn_ldexpf(rows.o[r][t][e], f), __builtin_amdgcn_ldexpf(rows.o[r][t + 1][e], f),
+                              __builtin_amdgcn_ldexpf(rows.o[r][t + 2][e], f), __builtin_amdgcn_ldexpf(rows.o[r][t + 3][e], f)};
             __syncthreads();
             for (int x = threadIdx.x; x < 16 * (D / 4); x += kThreads) {
                 const int row = x / (D / 4), d = x % (D / 4) * 4;
@@ -845,12 +853,12 @@ void attn_kernel(AttnArgs A) {
 #pragma unroll
                 for (int i = 1; i < WAVES; ++i)
                     v += *reinterpret_cast<const f32x4*>(so + (i * 16 + row) * kPad + d);
-                float Mr = -kInf, L = 0.0f;
+                float Mr = kNoRef, L = 0.0f;
 #pragma unroll
                 for (int i = 0; i < WAVES; ++i) Mr = fmaxf(Mr, sm[i][16 * r + row]);
 #pragma unroll
                 for (int i = 0; i < WAVES; ++i)
-                    L += sl[i][16 * r + row] * __builtin_amdgcn_exp2f(sm[i][16 * r + row] - (Mr == -kInf ? 0.0f : Mr));
+                    L += __builtin_amdgcn_ldexpf(sl[i][16 * r + row], rebase(sm[i][16 * r + row], Mr));
                 if (!SPLIT || whole) {
                     store_row<D>(A, S, h, rho, d, v, L);
                 } else {
@@ -895,13 +903,14 @@ void attn_join_kernel(AttnArgs A) {
     const int share = threadIdx.x / kQuads, quad = threadIdx.x % kQuads;
     const int i0 = parts * share / kShares, i1 = parts * (share + 1) / kShares;
     for (int row = blockIdx.y; row < rows; row += kJoinRows) {
-        float M = -kInf, L = 0.0f;
+        float M = kNoRef, L = 0.0f;
         f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
         auto add = [&](float m, float l, f32x4 o) {
-            const float mn = fmaxf(M, m), use = mn == -kInf ? 0.0f : mn;
-            const float fa = __builtin_amdgcn_exp2f(M - use), fb = __builtin_amdgcn_exp2f(m - use);
-            L = L * fa + l * fb;
-            v = v * fa + o * fb;
+            const float mn = fmaxf(M, m);
+            const int fa = rebase(M, mn), fb = rebase(m, mn);
+            L = __builtin_amdgcn_ldexpf(L, fa) + __builtin_amdgcn_ldexpf(l, fb);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_ldexpf(v[e], fa) + __builtin_amdgcn_ldexpf(o[e], fb);
             M = mn;
         };
 #pragma unroll 2
