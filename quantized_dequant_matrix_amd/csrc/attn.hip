@@ -525,11 +525,15 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
                 for (int e = 0; e < 4; ++e) s[r][4 * u + e] = a[e];
             } else {
                 // sums begin at the bits of 1.5 2^23: as float32 that is 1.5
-                // 2^23 + sum, exactly (|sum| <= 128 127 256 < 2^22), and
-                //   (a - 1.5 2^23 (1 + 129 / 2^14)) 2^14 + (b 2^7 + c)
-                // is a 2^14 + b 2^7 + c, rounded by 2^6 at most inside (a
-                // digit's rounding in the query costs more)
-                constexpr float kBias = 12582912.0f, kOff = kBias + 129.0f * (kBias / 16384.0f);
+                // 2^23 + sum, exactly (|sum| <= 128 128 256 = 2^22), and
+                //   (a - 1.5 2^23 (1 + 1 / 2^14)) 2^14 + ((b - 1.5 2^23) 2^7 + c)
+                // is a 2^14 + b 2^7 + c.  Both differences are exact, and so is
+                // the inner sum while it lies below 2^24: rows of small codes
+                // round once, at the end.  (With b's bias left in it, and taken
+                // from a, a subtraction is saved and every score rounded to a
+                // multiple of 2^6: 1 part in 2^15 of one key code of 1.  It was worth 1%
+                // of a prefill chunk.)
+                constexpr float kBias = 12582912.0f, kOff = kBias + kBias / 16384.0f;
                 const int c = __float_as_int(kBias);
                 i32x4 a[3] = {i32x4{c, c, c, c}, i32x4{c, c, c, c}, i32x4{c, c, c, c}};
 #pragma unroll
@@ -542,7 +546,7 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     s[r][4 * u + e] = fmaf(__int_as_float(a[0][e]) - kOff, 16384.0f,
-                                           fmaf(__int_as_float(a[1][e]), 128.0f, __int_as_float(a[2][e]))) *
+                                           fmaf(__int_as_float(a[1][e]) - kBias, 128.0f, __int_as_float(a[2][e]))) *
                                       kv.ks[u][e];
             }
         }
