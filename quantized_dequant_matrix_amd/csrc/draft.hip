@@ -251,6 +251,15 @@ __device__ __forceinline__ void join_row(const DraftView& D, int64_t b, int r, d
 
 __device__ __forceinline__ double inverse(double sum) { return sum > 0.0 ? 1.0 / sum : 0.0; }
 
+// max(p - q, 0) of two weights and their rows' 1 / sums.  Both products are
+// rounded before the difference: equal rows leave zero, and not the rounding
+// of a product that one fused multiply-add would leave.
+__device__ __forceinline__ double residual(double wp, double p_inv, double wq, double q_inv) {
+#pragma clang fp contract(off)
+    const double p = wp * p_inv, q = wq * q_inv;
+    return fmax(p - q, 0.0);
+}
+
 template <bool CAP, int STEPS>
 __global__ __launch_bounds__(kPickThreads)
 void draft_pick_kernel(DraftView D) {
@@ -321,9 +330,9 @@ void draft_pick_kernel(DraftView D) {
         double x = 0.0, y = 0.0;
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-            const double p = D.w.template weight<CAP>(clean(vp[i][e]), P.p_level) * P.p_inv;
-            y += p;
-            if (P.residual) x += fmax(p - D.w.template weight<CAP>(clean(vq[i][e]), P.q_level) * P.q_inv, 0.0);
+            const double w = D.w.template weight<CAP>(clean(vp[i][e]), P.p_level);
+            y += w * P.p_inv;
+            if (P.residual) x += residual(w, P.p_inv, D.w.template weight<CAP>(clean(vq[i][e]), P.q_level), P.q_inv);
         }
         y = wave_add(y);
         x = P.residual ? wave_add(x) : y;
@@ -440,8 +449,8 @@ void draft_draw_kernel(DraftView D) {
         if (at_v < D.a.V) {
             const float yp = clean(D.row(b, P.accepted)[at_v]);
             const float yq = minus ? clean(D.row(b, G + 1 + P.accepted)[at_v]) : 0.0f;
-            weight = D.w.template weight<CAP>(yp, P.p_level) * P.p_inv;
-            if (minus) weight = fmax(weight - D.w.template weight<CAP>(yq, P.q_level) * P.q_inv, 0.0);
+            const double w = D.w.template weight<CAP>(yp, P.p_level);
+            weight = minus ? residual(w, P.p_inv, D.w.template weight<CAP>(yq, P.q_level), P.q_inv) : w * P.p_inv;
         }
         const double run = before_group + block_prefix(weight, sums, &total) + weight;
         if (t == 0) {
