@@ -40,7 +40,7 @@ extern "C" {
  *   of the activation quantizer over the row's head_dim elements:
  *   d = max|x| / 127 (IEEE float32 division),
  *   q = clamp(round_half_away_from_zero(x / d), -127, 127), x ~ q * d;
- *   an all-zero row has d = 0 and q = 0.
+ *   a row whose d is 0 (all zeros, or no magnitude above 63 2^-149) has q = 0.
  * QMV_KV_F16: IEEE float16 elements (k_scale and v_scale unused, NULL).
  * A row that holds a NaN or infinity (or a magnitude float16 rounds to
  * infinity) is stored as NaN in whole.  Pages filled by other means have to
@@ -140,7 +140,8 @@ int rmsnorm_add(const float* x, const float* r, const float* w, float* z, float*
 
 /* The same with y quantized as qmm_q4_0_q8act quantizes its activations:
  * codes int8 [M][K] (4-byte aligned) and scales float32 [M][K / 32].  A
- * block that is not finite gets the scale NaN. */
+ * block that is not finite gets the scale NaN, one whose scale is 0 the codes
+ * 0 (as in the cache; its products are 0 whatever the codes). */
 int rmsnorm_add_q8(const float* x, const float* r, const float* w, float* z, int8_t* q, float* d, int64_t K,
                    int64_t M, float eps, hipStream_t stream);
 
