@@ -51,6 +51,7 @@
 // the workspace (two slots a workgroup) and are joined by a second kernel in
 // a fixed order.  Short tables, many items and chunks of many rows are computed
 // an item a workgroup instead, without a second kernel (plan_attn says where).
+#include <cmath>
 #include <stdint.h>
 
 #include "attn_plan.h"
@@ -89,7 +90,8 @@ struct AttnArgs {
     int4* owners;      // of item (tile slot, head): first and last workgroup, slot of the first
     int64_t ldq, ldo;
     int group;         // query heads of a key/value head
-    float scale_log2;  // |scale| log2(e)
+    float scale_log2;  // |scale| log2(e) without scale's exponent: in [0.72, 1.45), or 0
+    int scale_exp;     // ... and that, added to the query's: neither leaves float32 alone
     float sign;        // of scale
     int window;
     int unit_shift;    // log2 of a unit's keys (split only)
@@ -433,7 +435,7 @@ __device__ __forceinline__ void prepare_rows(const AttnArgs& A, Queries<D, F16, 
             inv = an > 0.0f ? kQParts / an : 0.0f;
             back = an * (1.0f / kQParts);
         }
-        W.qs[r] = __builtin_amdgcn_ldexpf(back * A.scale_log2, k);
+        W.qs[r] = __builtin_amdgcn_ldexpf(back * A.scale_log2, k + A.scale_exp);
         // all scores equal (a zero query or scale), a row that will be NaN or
         // one past the item's: zero parts, with a factor that keeps masked
         // scores at -infinity
@@ -962,7 +964,7 @@ hipError_t launch_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, const float
     A.ldq = ldq;
     A.ldo = ldo;
     A.group = q_heads / c.kv_heads;
-    A.scale_log2 = (scale < 0.0f ? -scale : scale) * kLog2e;
+    A.scale_log2 = std::frexp(scale < 0.0f ? -scale : scale, &A.scale_exp) * kLog2e;
     A.sign = scale < 0.0f ? -1.0f : 1.0f;
     A.window = window;
     A.unit_shift = p.unit_shift;

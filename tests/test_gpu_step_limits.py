@@ -43,3 +43,30 @@ def test_attention_of_few_rows_among_very_many_sequences(T, heads, dim, fmt, len
     ref, tol = R.attention(q.astype(np.float64).reshape(T, heads, dim), P.rows("k", 0), P.rows("v", 0),
                            [length - T + i for i in range(T)], dim ** -0.5, 0)
     assert_within(host(out).reshape(ref.shape), ref, tol, "few rows, many sequences")
+
+
+@pytest.mark.parametrize("scale,q_scale", [(1e-38, 1e37), (3e-39, 1e38), (1e-30, 1e30), (3.4e38, 1e-39), (2.5e38, 4e-39),
+                                           (-3e38, 3e-39), (1e20, 1e-20), (1.2e-38, 2e37)])
+@pytest.mark.parametrize("fmt", ["q8", "f16"])
+def test_scales_at_the_ends_of_float32(fmt, scale, q_scale):
+    """Scale and query are far from 1, their product is not: neither may overflow or lose bits by itself.  (Queries
+    below 2^-126 have fewer bits, which the plain form is given too.)"""
+    qmv = _qmv()
+    say(f"attn {fmt} scale {scale} queries {q_scale}")
+    rng = np.random.default_rng(7)
+    heads, Hq, dim, lens, new = 2, 4, 64, [200, 33], [2, 1]
+    P = R.Pages(lens, heads, dim, 16, fmt, rng)
+    q = (rng.uniform(0.5, 1.0, (3, Hq, dim)) * np.where(rng.random((3, Hq, dim)) < 0.5, -1, 1) * q_scale).astype(np.float32)
+    cache, table = P.to_gpu(DEV)
+    batch = qmv.KVBatch(table, _ints(R.starts(new)), _ints(lens), 3)
+    out = torch.empty(3, Hq * dim, device=DEV)
+    wsb = qmv.attn_paged_ws_bytes(cache, batch, Hq)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=DEV)
+    qmv.attn_paged(cache, batch, dev(q.reshape(3, -1)), Hq * dim, out, Hq * dim, Hq, scale, 0, ws, wsb)
+    got, at = host(out).reshape(q.shape), 0
+    for b, (n, L) in enumerate(zip(new, lens)):
+        rows = slice(at, at + n)
+        ref, tol = R.attention(q[rows].astype(np.float64), P.rows("k", b), P.rows("v", b), [L - n + i for i in range(n)],
+                               float(np.float32(scale)), 0)
+        assert_within(got[rows], ref, tol, f"scale {scale}, sequence {b}")
+        at += n
