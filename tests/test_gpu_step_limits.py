@@ -70,3 +70,31 @@ def test_scales_at_the_ends_of_float32(fmt, scale, q_scale):
                                float(np.float32(scale)), 0)
         assert_within(got[rows], ref, tol, f"scale {scale}, sequence {b}")
         at += n
+
+
+@pytest.mark.parametrize("fmt,window", [("q8", 0), ("f16", 0), ("q8", 300)])
+def test_units_of_more_than_one_step(fmt, window):
+    """So many items and so long a table that units of 128 keys could not be numbered in 31 bits: 1100 sequences
+    that share their first page, 16 heads, tables of 2^24 positions."""
+    qmv = _qmv()
+    say(f"attn {fmt} 1100 sequences, tables of 2^24 positions, window {window}")
+    rng = np.random.default_rng(9)
+    B, heads, dim, page, longest = 1100, 16, 64, 1024, 900
+    P = R.Pages([longest], heads, dim, page, fmt, rng)
+    cache, _ = P.to_gpu(DEV)
+    table = torch.full((B, 16384), -1, dtype=torch.int32, device=DEV)
+    table[:, 0] = int(P.table[0, 0])
+    lens = rng.integers(1, longest + 1, B)
+    lens[[0, 500, B - 1]] = [longest, 0, 257]
+    batch = qmv.KVBatch(table, _ints(np.arange(B + 1)), _ints(lens), B)
+    q = rng.normal(0, 1.2, (B, heads, dim)).astype(np.float32)
+    out = torch.full((B, heads * dim), 9.5, device=DEV)
+    wsb = qmv.attn_paged_ws_bytes(cache, batch, heads)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=DEV)
+    qmv.attn_paged(cache, batch, dev(q.reshape(B, -1)), heads * dim, out, heads * dim, heads, 0.1, window, ws, wsb)
+    got, k, v = host(out).reshape(q.shape), P.rows("k", 0), P.rows("v", 0)
+    assert np.isfinite(got).all() and (got[500] == 0).all() and not (got == 9.5).any()
+    for b in [0, 1, 77, 500, 801, B - 1]:
+        n = int(lens[b])
+        ref, tol = R.attention(q[b:b + 1].astype(np.float64), k[:n], v[:n], [n - 1], 0.1, window)
+        assert_within(got[b:b + 1], ref, tol, f"sequence {b} of {n}")
