@@ -107,20 +107,33 @@ int kv_read(const qmv_kv_cache* cache, const qmv_kv_batch* batch, float* k, int6
  *   s_j = scale * q . k_j    for the visible positions j: j <= p, and with
  *                            window > 0 also j > p - window
  *   out = sum_j exp(s_j - max s) v_j / sum_j exp(s_j - max s)
- * in float32 (the softmax over one pass, running maximum and sum).  Row r of
- * q at q + r * ldq, of out at out + r * ldo (ldq, ldo >= q_heads *
+ * Row r of q at q + r * ldq, of out at out + r * ldo (ldq, ldo >= q_heads *
  * head_dim).  A row that sees nothing gets zeros; rows at or behind
  * row_start[B] are left as they were.  Positions that a row does not see
  * have no effect on it, whatever they hold.  A row that sees a key or value
  * stored as NaN gets NaN in every dimension of the heads that see it, and so
- * does a query that is not finite.  Scores are formed from the codes before
- * they are scaled: 8-bit keys of 2^96 and more may overflow there and give
- * NaN; 8-bit values outside [2^-70, 2^100] lose accuracy.
+ * does a query that is not finite.
+ * Accuracy: one pass over the keys, with scores, weights p, sums and results
+ * in float32, but narrower operands of the products.  A query element is held
+ * to 2^-22 of its row's largest magnitude (a score is off by as much of
+ * scale * max|q| * sum|k_j|).  A weight is held to 2^-20 of itself, or
+ *   8-bit values:   2^-34 of the row's largest weight times value scale, so
+ *     that a value which weighs nothing takes nothing from the others; weights
+ *     below 2^-114 of the largest may count as zero
+ *   float16 values: 2^-34 of the row's largest weight, whatever the values:
+ *     each position may be off by 2^-34 |v_j|, which matters where values are
+ *     seen that are 2^10 or more times those that hold the weight
+ * Scores are formed from the codes before they are scaled: 8-bit keys of 2^96
+ * and more may overflow there and give NaN, and a row whose scale * max|q| is
+ * below 2^-104 loses accuracy (beside keys below 2^72 its scores are 0 to
+ * float32 anyway).  8-bit values outside [2^-70, 2^100] lose accuracy.
  * q_heads: a multiple of kv_heads, at most 64 times as many, and
  * T * q_heads / 16 + B * kv_heads < 2^24.  scale finite; window >= 0 (0: none).
  * ws: attn_paged_ws_bytes(cache, batch, q_heads) bytes, 16-byte aligned,
  * contents overwritten; the size depends on the descriptors' numbers only,
- * not on the arrays, and is 0 for invalid ones. */
+ * not on the arrays, and is 0 for invalid ones.  So does the split of the
+ * work: it takes every sequence to be as long as max_pages allows (or the
+ * window), and a table cut to the longest sequence can be a third faster. */
 size_t attn_paged_ws_bytes(const qmv_kv_cache* cache, const qmv_kv_batch* batch, int32_t q_heads);
 int attn_paged(const qmv_kv_cache* cache, const qmv_kv_batch* batch, const float* q, int64_t ldq, float* out,
                int64_t ldo, int32_t q_heads, float scale, int32_t window, void* ws, size_t ws_bytes,
@@ -166,9 +179,10 @@ int qmm_q4_0_q8(const void* W, const int8_t* q, const float* d, float* y, int64_
  *     that is all zero), from p_n if a == n: the first index whose running
  *     sum exceeds u[b][G] times the whole sum
  *   tokens[b] = t_0 .. t_{a-1}, the drawn token, then -1
- * so that the tokens are distributed as the target's own.  Probabilities and
- * sums are taken in 64 bits: neither the order of a sum nor a launch changes
- * a token.  cap(y) = softcap * tanh(y / softcap), or y with softcap 0.
+ * so that the tokens are distributed as the target's own.  Everything is
+ * computed in 64 bits; an exponential is taken to 2^-42 of itself, so that
+ * decisions within about that of their border may fall either way.
+ * cap(y) = softcap * tanh(y / softcap), or y with softcap 0.
  * target: float32 [B][G + 1] rows of V logits, rows ldt elements apart;
  * draft: [B][G] rows, ldd apart; draft_tokens int32 [B][G]; u float32
  * [B][G + 1], each in [0, 1); accepted int32 [B]; tokens int32 [B][G + 1].

@@ -76,10 +76,12 @@ inline AttnPlan plan_attn(const qmv_kv_cache& c, const qmv_kv_batch& b, int q_he
     p.split = !chunk && (eight ? steps * 8 > 36 + items : steps * 20 > 80 + items);
     if (!p.split) {
         // Two row tiles share the keys' and values' loads and conversions.
-        // Two prompts of 1024 new tokens over 6000, 8 heads of 128: 290 us
-        // against 393 us (float16: 303 against 517); 64 wide 129 against
-        // 126 us, 256 wide 176 against 130 us (registers), and with fewer
-        // items than a round (256 new tokens of one prompt) no difference.
+        // Two prompts of 1024 new tokens over 6000, 8 heads of 128: 260 us
+        // against 375-397 us (float16: 298 against 505-516); with fewer items
+        // than a round (256 new tokens of one prompt over 2048) 32.8 against
+        // 32.3.  In an earlier state of the kernel 64-wide heads took 129 us
+        // with two against 126 with one, 256-wide ones 176 against 130
+        // (registers), in a smaller case.
         p.r = c.head_dim == 128 && items_of(32) >= kRound && b.T * group >= 64 * seqs ? 2 : 1;
         p.waves = eight && steps > kAttnWaves ? 8 : kAttnWaves;
         p.tiles = b.T * group / (16 * p.r) + b.B;

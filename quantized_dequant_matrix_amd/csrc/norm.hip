@@ -36,8 +36,8 @@ __device__ __forceinline__ float rstd_of(double sum, int64_t K, float eps) {
 
 // One workgroup a row of K = 4 Q elements, the whole row in registers: thread
 // t holds the float4 t, t + threads, ... .  Memory bounds it: 8 bytes in and 8
-// (5.1 with codes) out an element, each once.  2048 rows of 5376 take 30 us,
-// 5.9 TB/s (52 us with a second read 4 bytes at a time and plain stores).
+// (5.1 with codes) out an element, each once.  2048 rows of 5376 take 27-32
+// us, 5.5-6.5 TB/s (52 us with a second read 4 bytes at a time and plain stores).
 template <int VPT, bool Q8>
 __global__ __launch_bounds__(1024)
 void rmsnorm_row_kernel(const float* x, const float* r, const float* __restrict__ w, float* z, float* __restrict__ y,
