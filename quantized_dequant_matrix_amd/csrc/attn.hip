@@ -580,14 +580,17 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
         }
     }
 
-    // how far above the reference a score may lie: p dv within float16, and p
-    // so that 2^30 of them have a sum
-    float limit = kTopMax;
+    // How far above the reference a score may lie: p dv within float16, and p
+    // so that 2^30 of them have a sum.  From scales that the rows see only:
+    // what lies in other places may be a signalling NaN, which a maximum would
+    // not drop but quiet.
+    auto limit_of = [](const float(&x)[8]) { return fminf(kTopMax - __builtin_amdgcn_logf(largest(x)), kPMax); };
+    float all = kTopMax;  // where every row sees every key
     if constexpr (!F16) {
         float vs[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) vs[e] = kv.vs[e >> 2][e & 3];
-        limit = fminf(kTopMax - __builtin_amdgcn_logf(largest(vs)), kPMax);
+        all = limit_of(vs);
     }
 
     uint32_t ph[R][4], pl[R][4];
@@ -609,6 +612,10 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
                     dv[e] = seen ? dv[e] : 0.0f;
                 }
             }
+        }
+        float limit = all;
+        if constexpr (!F16) {
+            if (edge) limit = limit_of(dv);
         }
         // The reference moves only when a row has outgrown it, or could have by
         // the lane's largest score and value scale.  (NaN is never above: it

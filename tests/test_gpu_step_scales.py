@@ -135,3 +135,51 @@ def test_small_and_large_values_within_the_stated_range(max_pages):
     """Values of 2^-66 that take the attention beside values of 2^95 that do not."""
     Case([300], [1], 2, 1, 64, lambda j, L: 1.0 if j == 120 else 0.0, lambda j, L: 2.0 ** -66 if j == 120 else 2.0 ** 95,
          max_pages=max_pages).check(122.0, "2^-66 beside 2^95")
+
+
+SIGNALLING = np.array([0x7FA00000, 0xFFA00001, 0x7F800001, 0xFFBFFFFF], np.uint32).view(np.float32)
+
+
+def _fill_tails(P, lens):
+    """Scales behind the last positions: signalling NaN of both signs."""
+    for b, L in enumerate(lens):
+        for j in range(L, -(-L // P.page) * P.page):
+            for s in (P.ks, P.vs):
+                s[P.table[b, j // P.page], :, j % P.page] = SIGNALLING[j % 4]
+
+
+@TABLES
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("L", [33, 34, 35, 36, 49, 50, 145, 161, 273, 289, 297])
+def test_a_large_value_beside_places_that_hold_signalling_nan(L, dim, max_pages):
+    """The last position's value is 2^33 times the others', so the weights' reference has to move in the tile whose
+    other places nobody sees, whatever is in them."""
+    c = Case([L, 5], [1, 1], 4, 2, dim, lambda j, n: 0.5, lambda j, n: 1e4 if j == n - 1 else 1e-6, max_pages=max_pages)
+    _fill_tails(c.P, [L, 5])
+    c.check(2.0, f"length {L}, D {dim}")
+
+
+@TABLES
+@pytest.mark.parametrize("heads,group,dim", [(2, 2, 64), (2, 2, 128), (2, 2, 256), (16, 16, 128)])
+def test_a_signalling_nan_that_only_later_rows_see(heads, group, dim, max_pages):
+    """Rows before it are as without it, though their own last value moves the reference; rows from it on are NaN."""
+    L, n = 149, 64 if heads == 16 else 8
+    first = L - n
+    c = Case([L], [n], heads * group, heads, dim, lambda j, m: 0.5, lambda j, m: 1e4 if j in (first, first + 4) else 1e-6,
+             max_pages=max_pages if heads == 2 else None)
+    bad = first + 5
+    c.P.vs[c.P.table[0, bad // 16], :, bad % 16] = SIGNALLING[0]
+    qmv = _qmv()
+    c.q[:, :, 0] = 2.0 * c.sign
+    cache, table = c.P.to_gpu(DEV)
+    batch = qmv.KVBatch(table, _ints([0, n]), _ints([L]), n)
+    width = c.Hq * dim
+    out = torch.empty(n, width, device=DEV)
+    wsb = qmv.attn_paged_ws_bytes(cache, batch, c.Hq)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=DEV)
+    qmv.attn_paged(cache, batch, dev(c.q.reshape(n, width)), width, out, width, c.Hq, 1.0, 0, ws, wsb)
+    got = host(out).reshape(c.q.shape)
+    ref, tol = _tolerance(c.q[:5].astype(np.float64), c.P.rows("k", 0)[:bad], c.P.rows("v", 0)[:bad],
+                          [first + i for i in range(5)], 1.0)
+    assert_within(got[:5], ref, tol, "rows before it")
+    assert np.isnan(got[5:]).all()
