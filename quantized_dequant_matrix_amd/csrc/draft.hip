@@ -111,9 +111,11 @@ struct Weights {
 };
 
 // +infinity counts as the largest float; NaN weighs nothing: v_med3_f32 with
-// a NaN gives the smallest of the other two (the compiler's own median drops
-// the -infinity as an identity).
+// a quiet NaN gives the smallest of the other two (the compiler's own median
+// drops the -infinity as an identity).  A signalling NaN is quieted first:
+// the median would do that itself and then drop the -infinity.
 __device__ __forceinline__ float clean(float y) {
+    y = __builtin_canonicalizef(y);
     float r;
     asm("v_med3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(y), "v"(kNegInf), "v"(3.4028234663852886e38f));
     return r;
