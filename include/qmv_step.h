@@ -126,7 +126,8 @@ int kv_read(const qmv_kv_cache* cache, const qmv_kv_batch* batch, float* k, int6
  * Scores are formed from the codes before they are scaled: 8-bit keys of 2^96
  * and more may overflow there and give NaN, and a row whose scale * max|q| is
  * below 2^-104 loses accuracy (beside keys below 2^72 its scores are 0 to
- * float32 anyway).  8-bit values outside [2^-70, 2^100] lose accuracy.
+ * float32 anyway).  8-bit values outside [2^-70, 2^100] lose accuracy.  A row
+ * with scores beyond float32 is undefined.
  * q_heads: a multiple of kv_heads, at most 64 times as many, and
  * T * q_heads / 16 + B * kv_heads < 2^24.  scale finite; window >= 0 (0: none).
  * ws: attn_paged_ws_bytes(cache, batch, q_heads) bytes, 16-byte aligned,
