@@ -247,16 +247,14 @@ __device__ __forceinline__ float row_sum(float v) {
     return v + __shfl_xor(v, 32, kWave);
 }
 
-// v_max3_f32 as it is: fmaxf of values the compiler cannot trace to an
-// arithmetic result adds an instruction an operand to quiet NaNs.
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-    return r;
-}
-
+// The largest of eight, NaN if one is: gfx950's three-operand maximum, which
+// needs no quieting of its operands first (fmaxf of values that the compiler
+// cannot trace to an arithmetic result does).  No inline assembly: its operands
+// come from matrix instructions, whose results the compiler waits for only
+// where it knows the reader.
 __device__ __forceinline__ float largest(const float (&x)[8]) {
-    return fmaxf(max3(x[0], x[1], max3(x[2], x[3], x[4])), max3(x[5], x[6], x[7]));
+    auto max3 = [](float a, float b, float c) { return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c); };
+    return max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), __builtin_elementwise_maximum(x[6], x[7]));
 }
 
 __device__ __forceinline__ uint32_t pk(float a, float b) {
@@ -581,9 +579,9 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
     }
 
     // How far above the reference a score may lie: p dv within float16, and p
-    // so that 2^30 of them have a sum.  From scales that the rows see only:
-    // what lies in other places may be a signalling NaN, which a maximum would
-    // not drop but quiet.
+    // so that 2^30 of them have a sum.  From scales that the row sees only:
+    // what lies in other places may be anything, and a NaN would lift the limit
+    // for the values beside it.
     auto limit_of = [](const float(&x)[8]) { return fminf(kTopMax - __builtin_amdgcn_logf(largest(x)), kPMax); };
     float all = kTopMax;  // where every row sees every key
     if constexpr (!F16) {
