@@ -35,10 +35,10 @@
 //   p: two float16 terms, the scale of a value row multiplied in before the
 //     split.  float16 has few exponents, so what is split is p dv 2^-c with a
 //     reference c of the row's own, a whole number: where c moves, the
-//     largest p dv comes to lie in [2^10, 2^12), and it may grow to 2^15
-//     before c moves again.  The second term ends at 2^-24, 2^-34 of the
-//     largest product of a weight and a value's scale: a large value that
-//     weighs nothing takes nothing from the others.
+//     largest p dv comes to lie in [2^9, 2^11), and it may grow to 2^15
+//     before c moves again.  The second term is rounded to half a step of
+//     2^-24, 2^-34 of the largest product of a weight and a value's scale: a
+//     large value that weighs nothing takes nothing from the others.
 //     8-bit codes become float16 exactly: a byte u = code + 128 read as a
 //     float16 is u 2^-24, and one fused multiply-add makes it
 //     (u - 128) 2^-9.
@@ -73,7 +73,7 @@ constexpr float kInf = __builtin_inff();
 static_assert(kAttnWaves == kWavesPerBlock && kWaveThreads == kWave && kOwnerBytes == sizeof(int4));
 constexpr float kQParts = 127.0f * 16384.0f;     // largest |q| in parts: 127 2^14 (its digits: 127, 0, 0)
 // Weights are exp2(score - c), c the row's reference (tile_step):
-constexpr float kTop = 10.0f;                    // log2 of the largest p dv where c is set, rounded down
+constexpr float kTop = 9.0f;                     // log2 of the largest p dv where c is set, rounded down
 constexpr float kTopMax = 15.0f;                 // ... and without a move: float16 holds it
 constexpr float kPTop = 80.0f, kPMax = 90.0f;    // the same of p itself (values of zero would ask for any)
 constexpr float kNoRef = -3.4028234663852886e38f;  // c before any key: the first weight is infinite and sets it
@@ -257,8 +257,17 @@ __device__ __forceinline__ float largest(const float (&x)[8]) {
     return max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), __builtin_elementwise_maximum(x[6], x[7]));
 }
 
+// Two float16, rounded to nearest, once: of a conversion that the compiler may
+// repeat, one is fused with the product before it and another is not, and the
+// two differ by a step of float16.  HOLD: nor fused at all (two instructions
+// that each write half a register are slower than the packed conversion); not
+// for results of exponentials, whose readers the compiler has to know.
+template <bool HOLD>
 __device__ __forceinline__ uint32_t pk(float a, float b) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
+    if constexpr (HOLD) asm("" : "+v"(a), "+v"(b));
+    uint32_t r = __builtin_bit_cast(uint32_t, f16x2{static_cast<_Float16>(a), static_cast<_Float16>(b)});
+    asm("" : "+v"(r));
+    return r;
 }
 
 template <int D, bool F16>
@@ -619,7 +628,7 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
         // the lane's largest score and value scale.  (NaN is never above: it
         // stays in the sum or the products.)
         if (__ballot(fmaf(largest(s[r]), W.qs[r], -W.c[r]) > limit) != 0) {
-            // the largest p dv becomes 2^10 .. 2^12 (log2 dv rounded down to the
+            // the largest p dv becomes 2^9 .. 2^11 (log2 dv rounded down to the
             // exponent), unless p itself would pass 2^81
             float cn = W.c[r];
 #pragma unroll
@@ -650,9 +659,9 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            ph[r][e] = pk(p[2 * e], p[2 * e + 1]);
+            ph[r][e] = pk<!F16>(p[2 * e], p[2 * e + 1]);
             const f16x2 h = __builtin_bit_cast(f16x2, ph[r][e]);
-            pl[r][e] = pk(p[2 * e] - static_cast<float>(h[0]), p[2 * e + 1] - static_cast<float>(h[1]));
+            pl[r][e] = pk<true>(p[2 * e] - static_cast<float>(h[0]), p[2 * e + 1] - static_cast<float>(h[1]));
         }
     }
 
