@@ -76,6 +76,12 @@ constexpr float kQParts = 127.0f * 16384.0f;     // largest |q| in parts: 127 2^
 constexpr float kTop = 9.0f;                     // log2 of the largest p dv where c is set, rounded down
 constexpr float kTopMax = 15.0f;                 // ... and without a move: float16 holds it
 constexpr float kPTop = 80.0f, kPMax = 90.0f;    // the same of p itself (values of zero would ask for any)
+// Value scales are taken times 2^16, which brings ordinary ones (2^-7) near
+// kTop.  So the exponent that makes a weight which counts is near 0: at 16 its
+// rounding to float32 alone takes 2^-20 of the weight.  (8 multiplications a
+// tile, for all its rows; no difference in time.)
+constexpr int kScaleShift = 16;
+constexpr float kScaleUp = 65536.0f;
 constexpr float kNoRef = -3.4028234663852886e38f;  // c before any key: the first weight is infinite and sets it
 
 struct AttnArgs {
@@ -593,19 +599,17 @@ __device__ __forceinline__ void tile_step(const AttnArgs& A, KvRegs<D, F16>& kv,
     // for the values beside it.
     auto limit_of = [](const float(&x)[8]) { return fminf(kTopMax - __builtin_amdgcn_logf(largest(x)), kPMax); };
     float all = kTopMax;  // where every row sees every key
-    if constexpr (!F16) {
-        float vs[8];
+    float vs[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) vs[e] = kv.vs[e >> 2][e & 3];
-        all = limit_of(vs);
-    }
+    for (int e = 0; e < 8; ++e) vs[e] = F16 ? 1.0f : kv.vs[e >> 2][e & 3] * kScaleUp;
+    if constexpr (!F16) all = limit_of(vs);
 
     uint32_t ph[R][4], pl[R][4];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         float dv[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dv[e] = F16 ? 1.0f : kv.vs[e >> 2][e & 3];
+        for (int e = 0; e < 8; ++e) dv[e] = vs[e];
         if (edge) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -855,7 +859,7 @@ void attn_kernel(AttnArgs A) {
             float M = kNoRef;
 #pragma unroll
             for (int i = 0; i < WAVES; ++i) M = fmaxf(M, sm[i][16 * r + n]);
-            const int f = rebase(rows.c[r], M) + (F16 ? 0 : 9);
+            const int f = rebase(rows.c[r], M) + (F16 ? 0 : 9 - kScaleShift);  // values enter times 2^-9
             float* dst = so + (wave * 16 + n) * kPad + 4 * g * (D / 16);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
