@@ -116,7 +116,8 @@ int kv_read(const qmv_kv_cache* cache, const qmv_kv_batch* batch, float* k, int6
  * Accuracy: one pass over the keys, with scores, weights p, sums and results
  * in float32, but narrower operands of the products.  A query element is held
  * to 2^-22 of its row's largest magnitude (a score is off by as much of
- * scale * max|q| * sum|k_j|).  A weight is held to 2^-20 of itself, or
+ * scale * max|q| * sum|k_j|).  A weight is held to 2^-20 of itself (8-bit
+ * values beyond [2^-14, 2^16]: 2^-18), or
  *   8-bit values:   2^-34 of the row's largest weight times value scale, so
  *     that a value which weighs nothing takes nothing from the others; weights
  *     below 2^-114 of the largest may count as zero
@@ -126,7 +127,7 @@ int kv_read(const qmv_kv_cache* cache, const qmv_kv_batch* batch, float* k, int6
  * Scores are formed from the codes before they are scaled: 8-bit keys of 2^96
  * and more may overflow there and give NaN, and a row whose scale * max|q| is
  * below 2^-104 loses accuracy (beside keys below 2^72 its scores are 0 to
- * float32 anyway).  8-bit values outside [2^-70, 2^100] lose accuracy.  A row
+ * float32 anyway).  8-bit values outside [2^-80, 2^90] lose accuracy.  A row
  * with scores beyond float32 is undefined.
  * q_heads: a multiple of kv_heads, at most 64 times as many, and
  * T * q_heads / 16 + B * kv_heads < 2^24.  scale finite; window >= 0 (0: none).
