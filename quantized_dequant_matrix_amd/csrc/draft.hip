@@ -88,25 +88,30 @@ struct Weights {
     double cap;    // softcap / temperature in units of log2, 0: none
     double k;      // log2(e) / temperature
     double twice;  // 2 log2(e) / softcap
-    // cap(y) / temperature in units of log2: the exponent of a weight up to
-    // the row's maximum.  Logits are bounded: y k stays finite.
+    // What exponents are differences of: the logit, or its capped value over
+    // the cap.
     template <bool CAP>
     __device__ __forceinline__ double level(float y) const {
-#pragma clang fp contract(off)
-        // (the product is rounded as the row's own level was: the difference
-        // of the largest logit to it is 0, however large both are)
         const double v = static_cast<double>(y);
-        if constexpr (!CAP) return v * k;
+        if constexpr (!CAP) return v;
         // tanh z = 1 - 2 / (1 + e^(2 z)); beyond |z| = 20 it is +-1 in 64 bits
         const double e = exp2_f64(fmin(fmax(v * twice, -64.0), 64.0));
-        return fma(-2.0, rcp_f64(1.0 + e), 1.0) * cap;
+        return fma(-2.0, rcp_f64(1.0 + e), 1.0);
+    }
+    // A weight's exponent below the level `top`, in units of log2.  The
+    // difference first: of two logits it is exact, so the largest has weight 1
+    // and rows that differ by a constant have the same weights, bit for bit.
+    // Logits are bounded: their differences times k stay finite.
+    template <bool CAP>
+    __device__ __forceinline__ double below(double level, double top) const {
+#pragma clang fp contract(off)
+        return (level - top) * (CAP ? cap : k);
     }
     // weight relative to the level `top` of the row's (or chunk's) maximum;
     // no branches, so that a thread's weights overlap
     template <bool CAP>
     __device__ __forceinline__ double weight(float y, double top) const {
-#pragma clang fp contract(off)
-        return exp2_f64(level<CAP>(y) - top, CAP && y == kNegInf);
+        return exp2_f64(below<CAP>(level<CAP>(y), top), CAP && y == kNegInf);
     }
 };
 
@@ -245,9 +250,9 @@ __device__ __forceinline__ void join_row(const DraftView& D, int64_t b, int r, d
     for (int c = lane + kWave; c < D.chunks; c += kWave) top = fmaxf(top, s[c].top);
     top = wave_max(top);
     *level = D.w.template level<CAP>(top);
-    double z = first.top != kNegInf ? first.sum * exp2_f64(D.w.template level<CAP>(first.top) - *level) : 0.0;
+    double z = first.top != kNegInf ? first.sum * exp2_f64(D.w.template below<CAP>(D.w.template level<CAP>(first.top), *level)) : 0.0;
     for (int c = lane + kWave; c < D.chunks; c += kWave)
-        if (s[c].top != kNegInf) z += s[c].sum * exp2_f64(D.w.template level<CAP>(s[c].top) - *level);
+        if (s[c].top != kNegInf) z += s[c].sum * exp2_f64(D.w.template below<CAP>(D.w.template level<CAP>(s[c].top), *level));
     *sum = wave_add(z);
 }
 

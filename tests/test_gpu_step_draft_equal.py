@@ -32,3 +32,23 @@ def test_a_draft_rejected_where_both_rows_are_equal(B, G, V, T, cap, how):
     assert sure.min() > 1e-12  # the draws from p themselves lie off their borders
     got = _run(target, draft, tokens, None, u, T, cap)
     assert np.array_equal(got[0], acc) and np.array_equal(got[1], out)
+
+
+@pytest.mark.parametrize("B,G,V", [(300, 1, 2), (200, 3, 37), (100, 2, 5000), (8, 1, 60000)])
+@pytest.mark.parametrize("T", [0.89, 1.0, 0.3])
+def test_rows_that_differ_by_a_constant_are_equal(B, G, V, T):
+    """p and q of logits that differ by a constant are the same: a draft rejected there (it is outside the vocabulary)
+    is followed by the token that u draws from p, as from a bonus row.  The logits are whole numbers and a constant of
+    up to 1000 leaves them so: their differences are exact."""
+    say(f"rows apart by a constant: B {B} G {G} V {V} T {T}")
+    rng = np.random.default_rng(V)
+    target = np.round(rng.normal(0, 3.0, (B, G + 1, V))).astype(np.float32)
+    draft = target[:, :G] + rng.integers(-1000, 1001, (B, G, 1)).astype(np.float32)
+    tokens = np.full((B, G), V, np.int32)
+    u = rng.random((B, G + 1), dtype=np.float32)
+    # the same draw as that of a sequence without drafts, in the plain form and in the kernel
+    acc, out, margin = R.draft_verify(target, draft, tokens, np.zeros(B, np.int32), u, T, 0.0)
+    assert (acc == 0).all() and margin.min() > 1e-12
+    for n in (None, np.zeros(B, np.int32)):
+        got = _run(target, draft, tokens, n, u, T, 0.0)
+        assert np.array_equal(got[0], acc) and np.array_equal(got[1], out)
