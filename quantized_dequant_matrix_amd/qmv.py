@@ -1,7 +1,7 @@
 """Python binding of libqmv.so (argument marshalling only).
 
 Every function has the name and argument order of the C entry point declared
-in include/qmv.h or include/qmv_step.h.  Buffer arguments are torch tensors on the GPU (or raw
+in include/qmv.h, include/qmv_step.h or include/qmv_serve.h.  Buffer arguments are torch tensors on the GPU (or raw
 device addresses as ints); sizes are ints; ``stream`` is a torch stream (None:
 torch's current stream).  A non-zero status raises QmvError.  All compute
 happens in the HIP kernels of libqmv.so; there is no fallback of any kind.
@@ -75,14 +75,42 @@ _STEP_SIGS = {
     "draft_verify_ws_bytes": ([_I64, _I32, _I64], _SZ),
     "draft_verify": ([_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _I32, _I64, _F, _F, _P, _SZ, _P], ctypes.c_int),
 }
-for _name, (_args, _res) in (_SIGS | _STEP_SIGS).items():
+
+class _KVPool(ctypes.Structure):
+    _fields_ = [("page_table", _P), ("free_pages", _P), ("num_pages", _I64), ("B", _I32), ("max_pages", _I32),
+                ("page_size", _I32)]
+
+
+class _Lora(ctypes.Structure):
+    _fields_ = [("A", _P), ("Bm", _P), ("rank", _P), ("scale", _P), ("K", _I64), ("N", _I64), ("slots", _I32),
+                ("max_rank", _I32), ("format", _I32)]
+
+
+# include/qmv_serve.h
+_EMBED = ([_P, _P, _P, _I64, _I64, _I64, _F, _P], ctypes.c_int)
+_SERVE_SIGS = {
+    "kv_plan_ws_bytes": ([_P], _SZ),
+    "kv_plan": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _SZ, _P], ctypes.c_int),
+    "embed_q8_0": _EMBED,
+    "embed_q4_0": _EMBED,
+    "embed_q4_k": _EMBED,
+    "embed_q6_k": _EMBED,
+    "lora_add_ws_bytes": ([_P, _I64, _I64], _SZ),
+    "lora_add": ([_P, _P, _P, _P, _I64, _P, _I64, _P, _I64, _I64, _I64, _P, _SZ, _P], ctypes.c_int),
+    "logits_draw_ws_bytes": ([_I64, _I64], _SZ),
+    "logits_draw": ([_P, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _F, _P, _SZ, _P], ctypes.c_int),
+}
+for _name, (_args, _res) in (_SIGS | _STEP_SIGS | _SERVE_SIGS).items():
     _fn = getattr(lib, _name)
     _fn.argtypes = _args
     _fn.restype = _res
 
 EXPORTS = tuple(_SIGS)
 STEP_EXPORTS = tuple(_STEP_SIGS)
+SERVE_EXPORTS = tuple(_SERVE_SIGS)
 KV_Q8, KV_F16 = 0, 1
+PLAN_PAGES, PLAN_ROWS, PLAN_LENGTH, PLAN_STACK = 1, 2, 4, 8
+LORA_F16, LORA_BF16 = 0, 1
 
 QMV_OK, QMV_ERR_NULL, QMV_ERR_SHAPE, QMV_ERR_ALIGN, QMV_ERR_WORKSPACE, QMV_ERR_LAUNCH, QMV_ERR_ARG = range(7)
 
@@ -356,3 +384,101 @@ def draft_verify(target, ldt, draft, ldd, draft_tokens, n_draft, u, accepted, to
                                                                          accepted, tokens, ws)
     _step("draft_verify", d, stream, target, ldt, draft, ldd, draft_tokens, n_draft, u, accepted, tokens, B, G, V,
           temperature, softcap, ws, ws_bytes)
+
+
+# ---- include/qmv_serve.h ----
+
+class KVPool:
+    """qmv_kv_pool over torch tensors: page_table int32 [B][max_pages] (the one of KVBatch), free_pages int32
+    [num_pages].  Keeps the tensors alive."""
+
+    def __init__(self, page_table, free_pages, page_size):
+        if page_table.dtype != torch.int32 or free_pages.dtype != torch.int32 or page_table.dim() != 2 or free_pages.dim() != 1:
+            raise ValueError("page_table [B][max_pages] and free_pages [num_pages] are int32")
+        _on_gpu(page_table, free_pages)
+        self.tensors = page_table, free_pages
+        self.struct = _KVPool(_ptr(page_table), _ptr(free_pages), free_pages.shape[0], *page_table.shape, page_size)
+        self.ref = ctypes.addressof(self.struct)
+        self.device = page_table.get_device()
+
+
+class Lora:
+    """qmv_lora over torch tensors: A [slots][max_rank][K] and Bm [slots][N][max_rank], both float16 or both bfloat16,
+    scale float32 [slots], rank int32 [slots] or None.  Keeps the tensors alive."""
+
+    def __init__(self, A, Bm, scale, rank=None):
+        if A.dtype != Bm.dtype or A.dtype not in (torch.float16, torch.bfloat16):
+            raise ValueError("A and Bm are both float16 or both bfloat16")
+        if A.dim() != 3 or Bm.dim() != 3 or A.shape[0] != Bm.shape[0] or A.shape[1] != Bm.shape[2]:
+            raise ValueError("A is [slots][max_rank][K] and Bm [slots][N][max_rank]")
+        if scale.dtype != torch.float32 or scale.shape != A.shape[:1]:
+            raise ValueError("scale is float32 [slots]")
+        if rank is not None and (rank.dtype != torch.int32 or rank.shape != A.shape[:1]):
+            raise ValueError("rank is int32 [slots]")
+        self.tensors = tuple(t for t in (A, Bm, scale, rank) if t is not None)
+        _on_gpu(*self.tensors)
+        self.struct = _Lora(_ptr(A), _ptr(Bm), _ptr(rank), _ptr(scale), A.shape[2], Bm.shape[1], A.shape[0], A.shape[1],
+                            LORA_F16 if A.dtype == torch.float16 else LORA_BF16)
+        self.ref = ctypes.addressof(self.struct)
+        self.device = A.get_device()
+
+
+def _own(descriptor, d):
+    """Address of a descriptor whose tensors are on GPU d (the current one)."""
+    if descriptor.device != d:
+        raise ValueError("the descriptor's tensors are on another GPU than the current one")
+    return descriptor.ref
+
+
+def kv_plan_ws_bytes(pool) -> int:
+    return int(lib.kv_plan_ws_bytes(pool.ref))
+
+
+def kv_plan(pool, kv_len, keep, n_new, free_count, new_len, new_count, row_start, position, slot, status, T, ws, ws_bytes,
+            stream=None):
+    d = _device()
+    p = _own(pool, d)
+    *args, ws = _gpu(d, kv_len, keep, n_new, free_count, new_len, new_count, row_start, position, slot, status, ws)
+    _step("kv_plan", d, stream, p, *args, T, ws, ws_bytes)
+
+
+def embed_q8_0(W, tokens, y, N, K, M, scale, stream=None):
+    d = _device()
+    _step("embed_q8_0", d, stream, *_gpu(d, W, tokens, y), N, K, M, scale)
+
+
+def embed_q4_0(W, tokens, y, N, K, M, scale, stream=None):
+    d = _device()
+    _step("embed_q4_0", d, stream, *_gpu(d, W, tokens, y), N, K, M, scale)
+
+
+def embed_q4_k(W, tokens, y, N, K, M, scale, stream=None):
+    d = _device()
+    _step("embed_q4_k", d, stream, *_gpu(d, W, tokens, y), N, K, M, scale)
+
+
+def embed_q6_k(W, tokens, y, N, K, M, scale, stream=None):
+    d = _device()
+    _step("embed_q6_k", d, stream, *_gpu(d, W, tokens, y), N, K, M, scale)
+
+
+def lora_add_ws_bytes(lora, B, T) -> int:
+    return int(lib.lora_add_ws_bytes(lora.ref, B, T))
+
+
+def lora_add(lora, adapter, row_start, x, ldx, base, ldb, y, ldy, B, T, ws, ws_bytes, stream=None):
+    d = _device()
+    p = _own(lora, d)
+    adapter, row_start, x, base, y, ws = _gpu(d, adapter, row_start, x, base, y, ws)
+    _step("lora_add", d, stream, p, adapter, row_start, x, ldx, base, ldb, y, ldy, B, T, ws, ws_bytes)
+
+
+def logits_draw_ws_bytes(V, M) -> int:
+    return int(lib.logits_draw_ws_bytes(V, M))
+
+
+def logits_draw(logits, ldl, temperature, top_k, top_p, min_p, u, token, kept, V, M, softcap, ws, ws_bytes, stream=None):
+    d = _device()
+    logits, temperature, top_k, top_p, min_p, u, token, kept, ws = _gpu(d, logits, temperature, top_k, top_p, min_p, u,
+                                                                        token, kept, ws)
+    _step("logits_draw", d, stream, logits, ldl, temperature, top_k, top_p, min_p, u, token, kept, V, M, softcap, ws, ws_bytes)
