@@ -13,8 +13,10 @@
 //     to hold all answers;
 //   - their elements are collected (up to 4096), sorted, and give the answers
 //     exactly.
-// Rows with a top-k of up to 2048 need no sums: the bins count, and the first
-// k are collected whole.  Rows of temperature 0 end with the first step.
+// Rows with a small top-k need no sums and are read once: the largest logits of
+// runs of 64 are counted in bins, the bin where k runs are reached says what the
+// first k elements reach at least, and what lies there is collected whole.  Rows
+// of temperature 0 end with the first step.
 //
 // Weights are whole multiples of 2^-q of the row's largest: their sums are
 // exact in 64-bit integers in any order, so bins can be summed by atomics and
@@ -24,6 +26,8 @@
 // logits, or nearly) is resolved digit by digit of a 64-bit key (order code of
 // the logit, then the index from below) instead: slower, whatever the row.
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "qmv_device.h"
 #include "serve_internal.h"
@@ -36,10 +40,14 @@ namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / kWave;
 constexpr int kBins = 4096, kBinsPer = kBins / kThreads;
+constexpr float kEqualBins = 3072.0f;
 constexpr int kMostCands = 4096, kCandsPer = kMostCands / kThreads;
 constexpr int kMostCounted = 2048;  // largest top-k that is collected whole
+constexpr int kRun = 64;            // logits whose largest is kept
 constexpr int kDigitBins = 2048;
 constexpr int kMaxParts = kWave;  // a lane a part when they are joined
+constexpr int kWorkgroups = 512;   // of a call, about
+constexpr int kMostSplit = kWorkgroups / 2;  // rows that are split have two parts at least
 constexpr float kMaxLogit = 3.4028234663852886e38f;
 
 struct Sum {
@@ -81,7 +89,6 @@ struct Head {
     uint32_t above_count;
     uint32_t collected;
     int32_t k_bin, p_lo, p_hi, u_lo, u_hi;
-    uint32_t cands;  // elements of these bins
 };
 
 struct DrawView {
@@ -89,16 +96,25 @@ struct DrawView {
     double twice;  // 2 log2(e) / softcap
     int q;
     int parts;
-    int64_t part_len;  // a multiple of 4
+    int most_parts;    // with work enough for a workgroup each
+    int run_parts;     // of a row by runs where it is collected
+    int64_t part_len;  // of the first kernel, a multiple of 64
     bool vec;          // rows are 16-byte aligned
+    int64_t runs;      // of a row
     Part* part;        // [M][parts]
+    float* run;        // [M][runs]
     Head* head;        // [M]
     uint32_t* count;   // [M][kBins]
     uint64_t* mass;    // [M][kBins]
     uint64_t* cand;    // [M][kMostCands]
 };
 
-enum Mode { kFirst, kCounted, kSummed };
+enum Mode {
+    kFirst,    // the first element
+    kByRuns,   // the first top_k, found by runs
+    kCounted,  // the first top_k, found by counts of all elements
+    kSummed
+};
 
 // A row's parameters, the same in every thread.
 template <bool CAP>
@@ -123,14 +139,17 @@ struct Row {
         const double r = fma(exp2_f64(e), unit, 4503599627370496.0);
         return __builtin_bit_cast(uint64_t, r) & 0xFFFFFFFFFFFFFull;
     }
-    // Bins follow the order.  1 + distance * per_bin has 512 bins an octave, 8
-    // octaves: equal steps near the largest logit, then steps in proportion to
-    // the distance, so that neither the temperature nor the spread of the
-    // logits matters much.
-    __device__ __forceinline__ int bin_of(float v) const {
-        const float t = fminf(top - fminf(v, kMaxLogit), kMaxLogit);
-        const uint32_t b = (__float_as_uint(fmaf(t, per_bin, 1.0f)) - 0x3f800000u) >> 14;
-        return static_cast<int>(b < kBins ? b : kBins - 1);
+    // Bins follow the order: 3072 equal steps of the distance from the largest
+    // logit, then 128 an octave.  *part: where in the bin, of 4096 parts.
+    __device__ __forceinline__ int bin_of(float v, int* part = nullptr) const {
+        const float x = fminf(fminf(top - fminf(v, kMaxLogit), kMaxLogit) * per_bin, 1e6f);
+        const uint32_t past = __float_as_uint(x) - __float_as_uint(kEqualBins);
+        const int b = static_cast<int>(past >> 16) + static_cast<int>(kEqualBins);
+        const int e = static_cast<int>(x);
+        const bool equal = x < kEqualBins;
+        // 12 bits of a float below 3072 lie behind its point
+        if (part) *part = equal ? static_cast<int>((x - static_cast<float>(e)) * 4096.0f) : static_cast<int>((past & 0xffffu) >> 4);
+        return equal ? e : (b < kBins ? b : kBins - 1);
     }
     // Sums that the answers have to reach.
     __device__ __forceinline__ uint64_t need_p(uint64_t mass) const {
@@ -147,18 +166,43 @@ struct Row {
 
 __device__ __forceinline__ uint64_t at_least_1(uint64_t v) { return v < 1 ? 1 : v; }
 
+// A row's arguments.  They are asked for at once, before anything depends on
+// one of them: a load takes most of a microsecond, and a kernel here a few.
+struct Args {
+    float temperature, top_p, min_p, u;
+    int32_t top_k;
+};
+
+__device__ __forceinline__ Args args_of(const DrawView& D, int64_t m) {
+    const float* t = D.a.temperature + m;
+    Args A;
+    A.temperature = *t;
+    A.top_p = *(D.a.top_p ? D.a.top_p + m : t);
+    A.min_p = *(D.a.min_p ? D.a.min_p + m : t);
+    A.top_k = *(D.a.top_k ? D.a.top_k + m : reinterpret_cast<const int32_t*>(t));
+    A.u = D.a.u[m];
+    if (!D.a.top_p) A.top_p = 1.0f;
+    if (!D.a.min_p) A.min_p = 0.0f;
+    if (!D.a.top_k) A.top_k = 0;
+    return A;
+}
+
+__device__ __forceinline__ bool by_runs(const DrawView& D, const Args& A) {
+    return A.temperature > 0.0f && A.top_k > 0 && A.top_k <= kMostCounted && 4 * static_cast<int64_t>(A.top_k) <= D.runs;
+}
+
 template <bool CAP>
-__device__ __forceinline__ Row<CAP> row_of(const DrawView& D, int64_t m, uint64_t best, float sum, uint32_t count) {
+__device__ __forceinline__ Row<CAP> row_of(const DrawView& D, int64_t m, const Args& A, uint64_t best, float sum,
+                                           uint32_t count) {
     Row<CAP> R;
     R.y = D.a.logits + m * D.a.ldl;
     R.best = best;
-    const float T = D.a.temperature[m];
+    const float T = A.temperature, min_p = A.min_p;
     R.mode = kFirst;
     if (best == 0 || !(T > 0.0f)) return R;
-    R.top_k = D.a.top_k ? D.a.top_k[m] : 0;
-    R.top_p = D.a.top_p ? D.a.top_p[m] : 1.0f;
-    R.u = D.a.u[m];
-    const float min_p = D.a.min_p ? D.a.min_p[m] : 0.0f;
+    R.top_k = A.top_k;
+    R.top_p = A.top_p;
+    R.u = A.u;
     R.has_min = min_p > 0.0f;
     R.min_exponent = R.has_min ? log2(static_cast<double>(min_p)) : 0.0;
     R.w.k = kLog2e / static_cast<double>(T);
@@ -166,42 +210,105 @@ __device__ __forceinline__ Row<CAP> row_of(const DrawView& D, int64_t m, uint64_
     R.w.twice = D.twice;
     R.unit = static_cast<double>(uint64_t{1} << D.q);
     R.top = logit_of(static_cast<uint32_t>(best >> 32));
-    // the first octave ends at the nearer of eight powers of two of weight and
-    // an eighth of the mean distance
+    // the equal steps reach to the nearer of twice the mean distance and a
+    // weight of 2^-64: neither the spread of the logits nor the temperature
+    // then matters much
     const float mean = count ? fmaxf(R.top - sum / static_cast<float>(count), 0.0f) : 0.0f;
-    R.per_bin = fminf(fmaxf(mean > 0.0f ? 8.0f / mean : 0.0f, static_cast<float>(fmin(R.w.k, 1e30)) * 0.125f), 1e30f);
-    R.mode = R.top_k > 0 && R.top_k <= kMostCounted ? kCounted : kSummed;
+    R.per_bin = fminf(fmaxf(mean > 0.0f ? 0.5f * kEqualBins / mean : 0.0f,
+                            static_cast<float>(fmin(R.w.k, 1e28)) * (kEqualBins / 64.0f)), 1e30f);
+    // With k runs of the 4096 of 262,144 logits, hardly more than k elements
+    // reach the k-th run's largest; where a run in four is asked for, about 1.15 k
+    // do, and where more are, the elements are counted themselves.
+    R.mode = R.top_k <= 0 || R.top_k > kMostCounted ? kSummed : (by_runs(D, A) ? kByRuns : kCounted);
     return R;
 }
 
-// f(logit, index) for the logits of [lo, hi), 16 a thread and step; -infinity
-// past the end.  lo is a multiple of 4.
-template <class F>
-__device__ __forceinline__ void for_logits(const float* y, int64_t lo, int64_t hi, bool vec, F&& f) {
-    constexpr int kU = 4;
-    for (int64_t base = lo + 4 * threadIdx.x; base < hi; base += kU * 4 * kThreads) {
-        float v[kU][4];
+// 16 logits of a thread, 4 by 4; -infinity past the end.  `from` is a multiple
+// of 4.  WIDE: a wave's batch is 4 KB in a row (128 rows of 262,144 read for
+// their first elements in 33 us, 38 with the four quads a workgroup's width
+// apart); else every wave gets its share of a part that is less than a batch
+// (10.8 against 9.7 us for the bins of one row in parts of 4096).
+constexpr int kU = 4;
+constexpr int64_t kStep = kU * 4 * kThreads;  // logits of a workgroup's batch
+
+struct Batch {
+    float v[kU][4];
+};
+
+template <bool WIDE>
+__device__ __forceinline__ int place_of(int j) {  // of a thread's quad j in a batch
+    const int t = static_cast<int>(threadIdx.x);
+    if constexpr (WIDE) return (t / kWave) * (kU * 4 * kWave) + j * (4 * kWave) + (t & (kWave - 1)) * 4;
+    return (j * kThreads + t) * 4;
+}
+
+template <bool WIDE = false>
+__device__ __forceinline__ Batch load_batch(const float* y, int64_t from, int64_t hi, bool vec) {
+    Batch B;
 #pragma unroll
-        for (int j = 0; j < kU; ++j) {
-            const int64_t at = base + j * 4 * kThreads;
-            if (vec && at + 4 <= hi) {
-                const float4 x = *reinterpret_cast<const float4*>(y + at);
-                v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
-            } else {
+    for (int j = 0; j < kU; ++j) {
+        const int64_t at = from + place_of<WIDE>(j);
+        if (vec && at + 4 <= hi) {
+            const float4 x = *reinterpret_cast<const float4*>(y + at);
+            B.v[j][0] = x.x; B.v[j][1] = x.y; B.v[j][2] = x.z; B.v[j][3] = x.w;
+        } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[j][e] = at + e < hi ? y[at + e] : kNegInf;
-            }
+            for (int e = 0; e < 4; ++e) B.v[j][e] = at + e < hi ? y[at + e] : kNegInf;
         }
+    }
+    return B;
+}
+
+// f(four logits, index of their first) for the logits of [lo, hi); `B` is the
+// first batch, and the next one is asked for before a batch is used.
+template <bool WIDE, class F>
+__device__ __forceinline__ void for_quads(Batch B, const float* y, int64_t lo, int64_t hi, bool vec, F&& f) {
+    for (int64_t from = lo; from < hi; from += kStep) {
+        Batch next;
+        if (from + kStep < hi) next = load_batch<WIDE>(y, from + kStep, hi, vec);
 #pragma unroll
-        for (int j = 0; j < kU; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f(v[j][e], base + j * 4 * kThreads + e);
+        for (int j = 0; j < kU; ++j) f(B.v[j], from + place_of<WIDE>(j));
+        B = next;
     }
 }
 
-__device__ __forceinline__ uint64_t shfl_up64(uint64_t v, int d) {
-    const uint32_t lo = __shfl_up(static_cast<uint32_t>(v), d, kWave), hi = __shfl_up(static_cast<uint32_t>(v >> 32), d, kWave);
-    return (static_cast<uint64_t>(hi) << 32) | lo;
+template <class F>
+__device__ __forceinline__ void for_logits(const Batch& B, const float* y, int64_t lo, int64_t hi, bool vec, F&& f) {
+    for_quads<false>(B, y, lo, hi, vec, [&](const float (&v)[4], int64_t at) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f(v[e], at + e);
+    });
+}
+
+// Inclusive sums over the wave (ROWS: over each 16 lanes), in lane order, by
+// row shifts and broadcasts.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ void add_lanes(Sum& v) {
+    const uint32_t lo = static_cast<uint32_t>(v.mass), hi = static_cast<uint32_t>(v.mass >> 32);
+    const uint32_t l = __builtin_amdgcn_update_dpp(0, static_cast<int>(lo), CTRL, ROW_MASK, 0xF, false);
+    const uint32_t h = __builtin_amdgcn_update_dpp(0, static_cast<int>(hi), CTRL, ROW_MASK, 0xF, false);
+    v.mass += (static_cast<uint64_t>(h) << 32) | l;
+    v.count += static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v.count), CTRL, ROW_MASK, 0xF, false));
+}
+
+template <bool ROWS>
+__device__ __forceinline__ Sum wave_upto(Sum v) {
+    add_lanes<0x111, 0xF>(v);
+    add_lanes<0x112, 0xF>(v);
+    add_lanes<0x114, 0xF>(v);
+    add_lanes<0x118, 0xF>(v);
+    if constexpr (!ROWS) {
+        add_lanes<0x142, 0xA>(v);
+        add_lanes<0x143, 0xC>(v);
+    }
+    return v;
+}
+
+__device__ __forceinline__ Sum of_lane(const Sum& v, int lane) {
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(v.mass)), lane);
+    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(v.mass >> 32)), lane);
+    return {(static_cast<uint64_t>(hi) << 32) | lo,
+            static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v.count), lane))};
 }
 
 __device__ __forceinline__ Part join(Part p) {  // over the wave, in every lane
@@ -215,40 +322,31 @@ __device__ __forceinline__ Part join(Part p) {  // over the wave, in every lane
     return p;
 }
 
+// Sums of the waves.  Two of them take turns, so that one barrier a scan is
+// enough: who writes one of them again has passed the barrier behind its reads.
 struct Scan {
-    uint64_t mass[kWaves];
-    uint32_t count[kWaves];
+    uint64_t mass[2][kWaves];
+    uint32_t count[2][kWaves];
 };
 
 // Sums before this thread in thread order, and the total.
-__device__ __forceinline__ Sum block_before(Scan& S, Sum mine, Sum* total) {
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
-    Sum upto = mine;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const uint64_t m = shfl_up64(upto.mass, d);
-        const uint32_t c = __shfl_up(upto.count, d, kWave);
-        if (lane >= d) {
-            upto.mass += m;
-            upto.count += c;
-        }
-    }
-    __syncthreads();
+__device__ __forceinline__ Sum block_before(Scan& S, int& turn, Sum mine, Sum* total) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
+    const Sum upto = wave_upto<false>(mine);
+    turn ^= 1;
     if (lane == kWave - 1) {
-        S.mass[wave] = upto.mass;
-        S.count[wave] = upto.count;
+        S.mass[turn][wave] = upto.mass;
+        S.count[turn][wave] = upto.count;
     }
     __syncthreads();
+    const int w = lane & (kWaves - 1);
+    const Sum waves = wave_upto<true>({S.mass[turn][w], S.count[turn][w]});
+    *total = of_lane(waves, kWaves - 1);
     Sum before = {upto.mass - mine.mass, upto.count - mine.count};
-    *total = {0, 0};
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
-        if (i < wave) {
-            before.mass += S.mass[i];
-            before.count += S.count[i];
-        }
-        total->mass += S.mass[i];
-        total->count += S.count[i];
+    if (wave > 0) {
+        const Sum w0 = of_lane(waves, wave - 1);
+        before.mass += w0.mass;
+        before.count += w0.count;
     }
     return before;
 }
@@ -281,7 +379,7 @@ struct Found {
 // The first element of the order whose running count (mass: running sum)
 // reaches `need`, 1 <= need <= the row's.
 template <bool CAP>
-__device__ Found find(Digits& S, const DrawView& D, const Row<CAP>& R, bool mass, uint64_t need) {
+__device__ __noinline__ Found find(Digits& S, int& turn, const DrawView& D, const Row<CAP>& R, bool mass, uint64_t need) {
     uint64_t prefix = 0;
     Sum before = {0, 0}, upto = {0, 0};
     const int t = threadIdx.x;
@@ -295,7 +393,7 @@ __device__ Found find(Digits& S, const DrawView& D, const Row<CAP>& R, bool mass
             S.count[i] = 0;
         }
         __syncthreads();
-        for_logits(R.y, 0, D.a.V, D.vec, [&](float v, int64_t i) {
+        for_logits(load_batch(R.y, 0, D.a.V, D.vec), R.y, 0, D.a.V, D.vec, [&](float v, int64_t i) {
             if (!weighs(v)) return;
             const uint64_t key = key_of(v, i);
             if (d > 0 && (key >> high) != (prefix >> high)) return;
@@ -307,7 +405,7 @@ __device__ Found find(Digits& S, const DrawView& D, const Row<CAP>& R, bool mass
         __syncthreads();
         const Sum two[2] = {{S.mass[2 * t], S.count[2 * t]}, {S.mass[2 * t + 1], S.count[2 * t + 1]}};
         Sum total;
-        Sum run = block_before(S.scan, {two[0].mass + two[1].mass, two[0].count + two[1].count}, &total);
+        Sum run = block_before(S.scan, turn, {two[0].mass + two[1].mass, two[0].count + two[1].count}, &total);
         run.mass += before.mass;
         run.count += before.count;
         for (int j = 0; j < 2; ++j) {
@@ -325,9 +423,10 @@ __device__ Found find(Digits& S, const DrawView& D, const Row<CAP>& R, bool mass
 
 // token and count of a row of any kind
 template <bool CAP>
-__device__ void draw_by_digits(Digits& S, const DrawView& D, const Row<CAP>& R, int32_t* token, int32_t* n) {
+__device__ __noinline__ void draw_by_digits(Digits& S, const DrawView& D, const Row<CAP>& R, int32_t* token, int32_t* n) {
     Sum mine = {0, 0}, above = {0, 0}, total, kept;
-    for_logits(R.y, 0, D.a.V, D.vec, [&](float v, int64_t) {
+    int turn = 0;
+    for_logits(load_batch(R.y, 0, D.a.V, D.vec), R.y, 0, D.a.V, D.vec, [&](float v, int64_t) {
         if (!weighs(v)) return;
         const double e = R.exponent(v);
         const uint64_t w = R.mass_of(e);
@@ -338,20 +437,32 @@ __device__ void draw_by_digits(Digits& S, const DrawView& D, const Row<CAP>& R, 
             above.count += 1;
         }
     });
-    block_before(S.scan, above, &kept);
-    block_before(S.scan, mine, &total);
+    __syncthreads();
+    block_before(S.scan, turn, above, &kept);
+    block_before(S.scan, turn, mine, &total);
     if (!R.has_min) kept = total;
     if (kept.count == 0) kept = {static_cast<uint64_t>(R.unit), 1};
     Sum of_k = total;
     if (R.top_k > 0 && static_cast<uint32_t>(R.top_k) < total.count)
-        of_k = find(S, D, R, false, static_cast<uint64_t>(R.top_k)).upto;
+        of_k = find(S, turn, D, R, false, static_cast<uint64_t>(R.top_k)).upto;
     if (of_k.count < kept.count) kept = of_k;
     if (R.top_p < 1.0f) {
-        const Sum of_p = find(S, D, R, true, at_least_1(R.need_p(of_k.mass))).upto;
+        const Sum of_p = find(S, turn, D, R, true, at_least_1(R.need_p(of_k.mass))).upto;
         if (of_p.count < kept.count) kept = of_p;
     }
     *n = static_cast<int32_t>(kept.count);
-    *token = index_of(find(S, D, R, true, at_least_1(R.need_u(kept.mass))).key);
+    *token = index_of(find(S, turn, D, R, true, at_least_1(R.need_u(kept.mass))).key);
+}
+
+// The same on copies: what the caller holds stays in registers.
+template <bool CAP>
+__device__ __forceinline__ void by_digits(Digits& S, const DrawView& D, const Row<CAP>& R, int32_t* token, int32_t* n) {
+    const DrawView view = D;
+    const Row<CAP> row = R;
+    int32_t a, b;
+    draw_by_digits(S, view, row, &a, &b);
+    *token = a;
+    *n = b;
 }
 
 // ------------------------------------------------------------ by bins
@@ -365,21 +476,27 @@ struct Bins {
 struct Ask {
     Scan scan;
     Hit hit[5];
-    uint32_t cands;
 };
 
-__device__ __forceinline__ Bins load_bins(Ask& S, const uint32_t* count, const uint64_t* mass, bool summed) {
+// The bins as they lie in memory.
+__device__ __forceinline__ Bins load_bins(const uint32_t* count, const uint64_t* mass) {
     Bins B;
-    Sum mine = {0, 0};
 #pragma unroll
     for (int j = 0; j < kBinsPer; ++j) {
         B.bin[j].count = count[kBinsPer * threadIdx.x + j];
-        B.bin[j].mass = summed ? mass[kBinsPer * threadIdx.x + j] : 0;
+        B.bin[j].mass = mass[kBinsPer * threadIdx.x + j];
+    }
+    return B;
+}
+
+__device__ __forceinline__ void sum_bins(Ask& S, int& turn, Bins& B) {
+    Sum mine = {0, 0};
+#pragma unroll
+    for (int j = 0; j < kBinsPer; ++j) {
         mine.mass += B.bin[j].mass;
         mine.count += B.bin[j].count;
     }
-    B.before = block_before(S.scan, mine, &B.total);
-    return B;
+    B.before = block_before(S.scan, turn, mine, &B.total);
 }
 
 // The thread whose bin reaches `need` says so in hit[slot].
@@ -396,14 +513,12 @@ __device__ __forceinline__ void ask_bins(Ask& S, const Bins& B, int slot, bool m
 // Bins that hold the answers, in every thread.
 template <bool CAP>
 __device__ __forceinline__ Head choose_bins(Ask& S, const Row<CAP>& R, const Bins& B, Sum above) {
-    Head H = {above.mass, above.count, 0, -1, 0, -1, 0, -1, 0};
+    Head H = {above.mass, above.count, 0, -1, 0, -1, 0, -1};
     const uint32_t kk = R.top_k > 0 && static_cast<uint32_t>(R.top_k) < B.total.count ? R.top_k : B.total.count;
-    if (threadIdx.x == 0) S.cands = 0;
-    if (R.mode == kCounted) {
+    if (R.mode != kSummed) {  // the first kk whole (of runs: fewer than k may be there, then all)
         ask_bins(S, B, 0, false, kk);
         __syncthreads();
-        H.u_hi = S.hit[0].at;  // the first kk whole
-        H.cands = S.hit[0].upto.count;
+        H.u_hi = R.mode == kByRuns && B.total.count < static_cast<uint32_t>(R.top_k) ? kBins - 1 : S.hit[0].at;
         return H;
     }
     uint64_t k_lo = B.total.mass, k_hi = B.total.mass;
@@ -437,15 +552,6 @@ __device__ __forceinline__ Head choose_bins(Ask& S, const Row<CAP>& R, const Bin
     __syncthreads();
     H.u_lo = S.hit[3].at;
     H.u_hi = S.hit[4].at;
-    uint32_t mine = 0;
-#pragma unroll
-    for (int j = 0; j < kBinsPer; ++j) {
-        const int b = kBinsPer * static_cast<int>(threadIdx.x) + j;
-        if (b == H.k_bin || (b >= H.p_lo && b <= H.p_hi) || (b >= H.u_lo && b <= H.u_hi)) mine += B.bin[j].count;
-    }
-    if (mine) atomicAdd(&S.cands, mine);
-    __syncthreads();
-    H.cands = S.cands;
     return H;
 }
 
@@ -453,84 +559,162 @@ __device__ __forceinline__ bool chosen(const Head& H, int b) {
     return b == H.k_bin || (b >= H.p_lo && b <= H.p_hi) || (b >= H.u_lo && b <= H.u_hi);
 }
 
-struct Sorter {
-    uint64_t key[2 * kMostCands];
-    Ask ask;
-    Hit hit[3];
+// The chosen bins numbered through: the three ranges follow each other, since
+// what is drawn is kept, and what is kept is among the first k.
+struct Chosen {
+    int u_lo, u_hi, p_lo, p_hi, count, per;  // per: buckets a bin
+    __device__ __forceinline__ explicit Chosen(const Head& H) {
+        u_lo = H.u_lo;
+        u_hi = H.u_hi;
+        p_lo = max(H.p_lo, u_hi + 1);
+        p_hi = max(H.p_hi, p_lo - 1);
+        count = (u_hi - u_lo + 1) + (p_hi - p_lo + 1) + 1;
+        per = max(kMostCands / count, 1);
+    }
+    __device__ __forceinline__ int bucket(int bin, int part) const {
+        const int i = bin <= u_hi ? bin - u_lo : (u_hi - u_lo + 1) + (bin <= p_hi ? bin - p_lo : p_hi - p_lo + 1);
+        return min(i * per + ((part * per) >> 12), kMostCands - 1);
+    }
 };
 
-// Sorts the n <= kMostCands keys in S.key, first of the order first; thread t
-// gets keys 4 t .. 4 t + 3 (0 past the end).
-__device__ __forceinline__ void sort_cands(Sorter& S, uint32_t n, uint64_t (&mine)[kCandsPer]) {
-    const int t = threadIdx.x, lane = t & (kWave - 1);
-    __syncthreads();
+struct Sorter {
+    uint64_t key[kMostCands], sorted[kMostCands];
+    uint32_t start[kMostCands + 1];
+    Ask ask;
+    Hit hit[3];
+    uint32_t above;
+};
+
+// Sorts n <= kMostCands keys, first of the order first: thread t has keys t,
+// t + 1024, .. (anything past the n-th) and gets keys 4 t .. 4 t + 3 (0 past
+// the end).  Up to 64 by exchanges in a wave; more go to 4096 buckets, equal
+// parts of the chosen bins, of which most hold one or none, and are ranked in
+// theirs.  (Exchanges among 1024 threads take 36 to 78 steps.)
+template <bool CAP>
+__device__ __forceinline__ void sort_cands(Sorter& S, int& turn, const Row<CAP>& R, const Head& H, uint32_t n,
+                                           uint64_t (&mine)[kCandsPer]) {
+    const int t = threadIdx.x;
     if (n <= kWave) {
         if (t < kWave) {
-            uint64_t key[1] = {lane < n ? S.key[lane] : 0};
+            uint64_t key[1] = {t < n ? mine[0] : 0};
             wave_sort_desc(key);
-            S.key[lane] = key[0];
+            S.sorted[t] = key[0];
         }
-    } else if (n <= 4 * kWave) {
-        if (t < kWave) {
-            uint64_t key[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) key[j] = j * kWave + lane < n ? S.key[j * kWave + lane] : 0;
-            wave_sort_desc(key);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) S.key[j * kWave + lane] = key[j];
-        }
-    } else if (n <= kThreads) {
-        uint64_t key[1] = {t < n ? S.key[t] : 0};
-        __syncthreads();
-        block_sort_desc(key, S.key);
-        __syncthreads();
-        S.key[t] = key[0];
     } else {
-        uint64_t key[kCandsPer];
+        const Chosen C(H);
+        int bucket[kCandsPer];
+        uint32_t slot[kCandsPer];
 #pragma unroll
-        for (int j = 0; j < kCandsPer; ++j) key[j] = j * kThreads + t < n ? S.key[j * kThreads + t] : 0;
-        __syncthreads();
-        block_sort_desc(key, S.key);
+        for (int j = 0; j < kCandsPer; ++j) S.start[j * kThreads + t] = 0;
+        if (t == 0) S.start[kMostCands] = n;
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kCandsPer; ++j) S.key[j * kThreads + t] = key[j];
+        for (int j = 0; j < kCandsPer; ++j) {
+            if (j * kThreads + t >= n) continue;
+            int part;
+            const int bin = R.bin_of(logit_of(static_cast<uint32_t>(mine[j] >> 32)), &part);
+            bucket[j] = C.bucket(bin, part);
+            slot[j] = atomicAdd(&S.start[bucket[j]], 1u);
+        }
+        __syncthreads();
+        uint32_t in[kCandsPer];
+        Sum own = {0, 0}, total;
+#pragma unroll
+        for (int j = 0; j < kCandsPer; ++j) {
+            in[j] = S.start[kCandsPer * t + j];
+            own.count += in[j];
+        }
+        uint32_t before = block_before(S.ask.scan, turn, own, &total).count;
+#pragma unroll
+        for (int j = 0; j < kCandsPer; ++j) {
+            S.start[kCandsPer * t + j] = before;
+            before += in[j];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kCandsPer; ++j)
+            if (j * kThreads + t < n) S.key[S.start[bucket[j]] + slot[j]] = mine[j];
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kCandsPer; ++j) {
+            if (j * kThreads + t >= n) continue;
+            const uint32_t lo = S.start[bucket[j]], hi = S.start[bucket[j] + 1];
+            uint32_t rank = lo;
+            for (uint32_t i = lo; i < hi; ++i) rank += S.key[i] > mine[j] ? 1u : 0u;
+            S.sorted[rank] = mine[j];
+        }
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kCandsPer; ++j) mine[j] = kCandsPer * t + j < n ? S.key[kCandsPer * t + j] : 0;
+    for (int j = 0; j < kCandsPer; ++j) mine[j] = kCandsPer * t + j < n ? S.sorted[kCandsPer * t + j] : 0;
 }
 
-// The collected elements of a row, sorted, and the answers among them.
+// The answers among the n collected elements of a row (sort_cands says how a
+// thread holds them).
 template <bool CAP>
-__device__ __forceinline__ void draw_from_cands(Sorter& S, const Row<CAP>& R, const Bins& B, const Head& H, int32_t* token,
-                                                int32_t* n) {
-    uint64_t key[kCandsPer];
-    sort_cands(S, H.cands, key);
+__device__ __forceinline__ void draw_from_cands(Sorter& S, int& turn, const Row<CAP>& R, const Bins& B, const Head& H,
+                                                uint32_t n_cands, uint64_t (&key)[kCandsPer], int32_t* token, int32_t* n) {
     const int t = threadIdx.x;
-    double e[kCandsPer];
-    Sum w[kCandsPer];
+    const bool whole = R.mode != kSummed;  // the first k are here
+    if (t == 0) S.above = 0;
+    sort_cands(S, turn, R, H, n_cands, key);
+    Sum w[kCandsPer], kept, of_k;
+    if (whole) {
+        uint32_t above = 0;
+        Sum own = {0, 0};
+#pragma unroll
+        for (int j = 0; j < kCandsPer; ++j) {
+            w[j] = {0, 0};
+            if (key[j] && kCandsPer * t + j < R.top_k) {
+                const double e = R.exponent(logit_of(static_cast<uint32_t>(key[j] >> 32)));
+                w[j] = {R.mass_of(e), 1u};
+                above += e >= R.min_exponent ? 1u : 0u;
+            }
+            own.mass += w[j].mass;
+            own.count += w[j].count;
+        }
+        if (R.has_min && above) atomicAdd(&S.above, above);
+        const Sum before = block_before(S.ask.scan, turn, own, &of_k);
+        auto ask = [&](int slot, bool mass, uint64_t need) {
+            Sum run = before;
+#pragma unroll
+            for (int j = 0; j < kCandsPer; ++j) {
+                const Sum next = {run.mass + w[j].mass, run.count + w[j].count};
+                if (reaches(run, next, mass, need)) S.hit[slot] = {run, next, kCandsPer * t + j};
+                run = next;
+            }
+            __syncthreads();
+            return S.hit[slot];
+        };
+        kept = of_k;
+        if (R.top_p < 1.0f) kept = ask(0, true, at_least_1(R.need_p(of_k.mass))).upto;
+        if (R.has_min && S.above < kept.count) kept = ask(1, false, max(S.above, 1u)).upto;
+        *n = static_cast<int32_t>(kept.count);
+        *token = index_of(S.sorted[ask(2, true, at_least_1(R.need_u(kept.mass))).at]);
+        return;
+    }
     int bin[kCandsPer];
 #pragma unroll
     for (int j = 0; j < kCandsPer; ++j) {
         const float v = logit_of(static_cast<uint32_t>(key[j] >> 32));
         bin[j] = key[j] ? R.bin_of(v) : -1;
-        e[j] = key[j] ? R.exponent(v) : 0.0;
-        w[j] = {key[j] ? R.mass_of(e[j]) : 0, key[j] ? 1u : 0u};
+        w[j] = {key[j] ? R.mass_of(R.exponent(v)) : 0, key[j] ? 1u : 0u};
     }
-    const uint32_t kk = R.top_k > 0 && static_cast<uint32_t>(R.top_k) < B.total.count ? R.top_k : B.total.count;
-    // the element of bin `of` (of any, with -1: then from the first on) that
-    // reaches `need`
-    auto ask = [&](int slot, int of, Sum before, bool mass, uint64_t need) -> Hit {
+    // the element that reaches `need`, in the bin that does
+    auto ask = [&](int slot, bool mass, uint64_t need) -> Hit {
+        ask_bins(S.ask, B, slot, mass, need);
+        __syncthreads();
+        const Hit of = S.ask.hit[slot];
         Sum own = {0, 0}, in[kCandsPer], total;
 #pragma unroll
         for (int j = 0; j < kCandsPer; ++j) {
-            in[j] = of < 0 || bin[j] == of ? w[j] : Sum{0, 0};
+            in[j] = bin[j] == of.at ? w[j] : Sum{0, 0};
             own.mass += in[j].mass;
             own.count += in[j].count;
         }
-        Sum run = block_before(S.ask.scan, own, &total);
-        run.mass += before.mass;
-        run.count += before.count;
+        Sum run = block_before(S.ask.scan, turn, own, &total);
+        run.mass += of.before.mass;
+        run.count += of.before.count;
 #pragma unroll
         for (int j = 0; j < kCandsPer; ++j) {
             const Sum next = {run.mass + in[j].mass, run.count + in[j].count};
@@ -540,53 +724,26 @@ __device__ __forceinline__ void draw_from_cands(Sorter& S, const Row<CAP>& R, co
         __syncthreads();
         return S.hit[slot];
     };
-    auto ask_in_bin = [&](int slot, bool mass, uint64_t need) -> Hit {
-        ask_bins(S.ask, B, slot, mass, need);
+    const uint32_t kk = R.top_k > 0 && static_cast<uint32_t>(R.top_k) < B.total.count ? R.top_k : B.total.count;
+    of_k = B.total;
+    if (H.k_bin >= 0) {
+        of_k = ask(0, false, kk).upto;
+    } else if (kk < B.total.count) {  // the end of a bin
+        ask_bins(S.ask, B, 0, false, kk);
         __syncthreads();
-        const Hit h = S.ask.hit[slot];
-        return ask(slot, h.at, h.before, mass, need);
-    };
-    Sum kept, of_k;
-    if (R.mode == kCounted) {
-        Sum mine = {0, 0}, first = {0, 0};
-#pragma unroll
-        for (int j = 0; j < kCandsPer; ++j) {
-            if (static_cast<uint32_t>(kCandsPer * t + j) >= kk) w[j] = {0, 0};
-            first.mass += w[j].mass;
-            first.count += w[j].count;
-            if (w[j].count && e[j] >= R.min_exponent) {
-                mine.mass += w[j].mass;
-                mine.count += 1;
-            }
-        }
-        block_before(S.ask.scan, first, &of_k);
-        kept = of_k;
-        if (R.has_min) block_before(S.ask.scan, mine, &kept);
-    } else {
-        of_k = B.total;
-        if (H.k_bin >= 0) {
-            of_k = ask_in_bin(0, false, kk).upto;
-        } else if (kk < B.total.count) {  // the end of a bin
-            ask_bins(S.ask, B, 0, false, kk);
-            __syncthreads();
-            of_k = S.ask.hit[0].upto;
-        }
-        kept = of_k;
-        if (R.has_min && H.above_count < kept.count) kept = {H.above_mass, H.above_count};
+        of_k = S.ask.hit[0].upto;
     }
+    kept = of_k;
+    if (R.has_min && H.above_count < kept.count) kept = {H.above_mass, H.above_count};
     if (kept.count == 0) kept = {static_cast<uint64_t>(R.unit), 1};
     if (R.top_p < 1.0f) {
-        const uint64_t need = at_least_1(R.need_p(of_k.mass));
-        const Sum of_p = (R.mode == kCounted ? ask(1, -1, {0, 0}, true, need) : ask_in_bin(1, true, need)).upto;
+        const Sum of_p = ask(1, true, at_least_1(R.need_p(of_k.mass))).upto;
         if (of_p.count < kept.count) kept = of_p;
     }
-    const uint64_t need = at_least_1(R.need_u(kept.mass));
-    const Hit h = R.mode == kCounted ? ask(2, -1, {0, 0}, true, need) : ask_in_bin(2, true, need);
     *n = static_cast<int32_t>(kept.count);
-    *token = index_of(S.key[h.at]);
+    *token = index_of(S.sorted[ask(2, true, at_least_1(R.need_u(kept.mass))).at]);
 }
 
-template <bool CAP>
 __device__ __forceinline__ void store(const DrawView& D, int64_t m, int32_t token, int32_t n) {
     if (threadIdx.x == 0) {
         D.a.token[m] = token;
@@ -596,15 +753,46 @@ __device__ __forceinline__ void store(const DrawView& D, int64_t m, int32_t toke
 
 // ------------------------------------------------------------ steps of a part
 
-__device__ __forceinline__ Part first_of(const float* y, int64_t lo, int64_t hi, bool vec, Part* lds) {
-    Part p = {0, 0.0f, 0};
-    for_logits(y, lo, hi, vec, [&](float v, int64_t i) {
-        const uint64_t key = weighs(v) ? key_of(v, i) : 0;
-        p.best = key > p.best ? key : p.best;
-        const bool ordinary = fabsf(v) < 1e6f;  // false for NaN
-        p.sum += ordinary ? v : 0.0f;
-        p.count += ordinary ? 1 : 0;
+__device__ __forceinline__ float max16(float v) {  // over 16 lanes, in the last one
+    auto step = [](float x, auto ctrl) {
+        const int b = __builtin_bit_cast(int, x);
+        return fmaxf(x, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(b, b, decltype(ctrl)::value, 0xF, 0xF, false)));
+    };
+    v = step(v, std::integral_constant<int, 0x111>{});
+    v = step(v, std::integral_constant<int, 0x112>{});
+    v = step(v, std::integral_constant<int, 0x114>{});
+    return step(v, std::integral_constant<int, 0x118>{});
+}
+
+// The first element of [lo, hi), and the largest logits of its runs to `run`
+// (null: not wanted).  A run is what 16 lanes hold of a batch.  One logit in
+// four is enough for their mean.
+template <bool WIDE>
+__device__ __forceinline__ Part first_of(const float* y, int64_t lo, int64_t hi, bool vec, Part* lds, float* run) {
+    float best = kNegInf, sum = 0.0f;
+    int32_t at_best = 0;
+    uint32_t count = 0;
+    for_quads<WIDE>(load_batch<WIDE>(y, lo, hi, vec), y, lo, hi, vec, [&](const float (&v)[4], int64_t at) {
+        // NaN is dropped; a NaN that is left is not larger than anything
+        float top = fminf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), kMaxLogit);
+        top = v[0] != v[0] && v[1] != v[1] && v[2] != v[2] && v[3] != v[3] ? kNegInf : top;
+        at_best = top > best ? static_cast<int32_t>(at) : at_best;  // a thread goes through rising indexes
+        best = fmaxf(best, top);
+        const bool ordinary = fabsf(v[0]) < 1e6f;  // false for NaN
+        sum += ordinary ? v[0] : 0.0f;
+        count += ordinary ? 1 : 0;
+        if (run) {
+            top = max16(top);
+            if ((threadIdx.x & 15) == 15 && at - 60 < hi) run[static_cast<uint32_t>(at) / kRun] = top;
+        }
     });
+    Part p = {0, sum, count};
+    if (best > kNegInf) {
+        int place = 3;
+#pragma unroll
+        for (int e = 2; e >= 0; --e) place = at_best + e < hi && fminf(y[at_best + e], kMaxLogit) == best ? e : place;
+        p.best = key_of(best, at_best + place);
+    }
     p = join(p);
     const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
     if (lane == 0) lds[wave] = p;
@@ -616,16 +804,16 @@ __device__ __forceinline__ Part first_of(const float* y, int64_t lo, int64_t hi,
 // Counts (and sums) of the logits of [lo, hi) into bins in LDS, zero before.
 // Returns this thread's share of those that pass min_p.
 template <bool CAP>
-__device__ __forceinline__ Sum fill_bins(const DrawView& D, const Row<CAP>& R, int64_t lo, int64_t hi, uint32_t* count,
-                                         uint64_t* mass) {
+__device__ __forceinline__ Sum fill_bins(const Batch& first, const DrawView& D, const Row<CAP>& R, int64_t lo, int64_t hi,
+                                         uint32_t* count, uint64_t* mass) {
     Sum above = {0, 0};
     if (R.mode == kCounted) {
-        for_logits(R.y, lo, hi, D.vec, [&](float v, int64_t) {
+        for_logits(first, R.y, lo, hi, D.vec, [&](float v, int64_t) {
             if (weighs(v)) atomicAdd(&count[R.bin_of(v)], 1u);
         });
         return above;
     }
-    for_logits(R.y, lo, hi, D.vec, [&](float v, int64_t) {
+    for_logits(first, R.y, lo, hi, D.vec, [&](float v, int64_t) {
         if (!weighs(v)) return;
         const double e = R.exponent(v);
         const uint64_t w = R.mass_of(e);
@@ -640,13 +828,15 @@ __device__ __forceinline__ Sum fill_bins(const DrawView& D, const Row<CAP>& R, i
     return above;
 }
 
-// Keys of the logits of [lo, hi) in chosen bins, behind *n keys in LDS: at
-// most as many as the bins count, which is at most kMostCands.
+// Keys of the logits of [lo, hi) in chosen bins, to LDS; *n counts them, also
+// those for which there is no room.
 template <bool CAP>
-__device__ __forceinline__ void collect(const DrawView& D, const Row<CAP>& R, const Head& H, int64_t lo, int64_t hi,
-                                        uint64_t* keys, uint32_t* n) {
-    for_logits(R.y, lo, hi, D.vec, [&](float v, int64_t i) {
-        if (weighs(v) && chosen(H, R.bin_of(v))) keys[atomicAdd(n, 1u)] = key_of(v, i);
+__device__ __forceinline__ void collect(const Batch& first, const DrawView& D, const Row<CAP>& R, const Head& H, int64_t lo,
+                                        int64_t hi, uint64_t* keys, uint32_t* n) {
+    for_logits(first, R.y, lo, hi, D.vec, [&](float v, int64_t i) {
+        if (!weighs(v) || !chosen(H, R.bin_of(v))) return;
+        const uint32_t at = atomicAdd(n, 1u);
+        if (at < kMostCands) keys[at] = key_of(v, i);
     });
 }
 
@@ -667,86 +857,197 @@ void draw_row_kernel(DrawView D) {
     __shared__ Ask ask;
     __shared__ Part parts[kWaves];
     __shared__ uint32_t collected;
-    const int64_t m = blockIdx.x;
+    const int64_t m = blockIdx.x, V = D.a.V;
     const int t = threadIdx.x;
+    const Args A = args_of(D, m);
     fill_exp_table();
-    const Part p = first_of(D.a.logits + m * D.a.ldl, 0, D.a.V, D.vec, parts);
-    Row<CAP> R = row_of<CAP>(D, m, p.best, p.sum, p.count);
+    const float* y = D.a.logits + m * D.a.ldl;
+    const Part p = first_of<true>(y, 0, V, D.vec, parts, nullptr);
+    Row<CAP> R = row_of<CAP>(D, m, A, p.best, p.sum, p.count);
     int32_t token = p.best ? index_of(p.best) : -1, n = p.best ? 1 : 0;
     if (R.mode != kFirst) {
+        int turn = 0;
         R.level_of_top();
         for (int i = t; i < kBins; i += kThreads) {
             S.bins.count[i] = 0;
             S.bins.mass[i] = 0;
         }
         if (t == 0) collected = 0;
+        const Batch again = load_batch(y, 0, V, D.vec);
         __syncthreads();
-        const Sum mine = fill_bins(D, R, 0, D.a.V, S.bins.count, S.bins.mass);
+        const Sum mine = fill_bins(again, D, R, 0, V, S.bins.count, S.bins.mass);
         Sum above;
-        block_before(ask.scan, mine, &above);  // and a barrier behind the atomics
-        const Bins B = load_bins(ask, S.bins.count, S.bins.mass, R.mode == kSummed);
+        block_before(ask.scan, turn, mine, &above);  // and a barrier behind the atomics
+        Bins B = load_bins(S.bins.count, S.bins.mass);
+        sum_bins(ask, turn, B);  // and one behind the loads
         const Head H = choose_bins(ask, R, B, above);
+        collect(load_batch(y, 0, V, D.vec), D, R, H, 0, V, S.sorter.key, &collected);
         __syncthreads();
-        if (H.cands > kMostCands) {
-            draw_by_digits(S.digits, D, R, &token, &n);
+        const uint32_t found = collected;
+        if (found > kMostCands) {
+            by_digits(S.digits, D, R, &token, &n);
         } else {
-            collect(D, R, H, 0, D.a.V, S.sorter.key, &collected);
-            draw_from_cands(S.sorter, R, B, H, &token, &n);
+            uint64_t key[kCandsPer];
+#pragma unroll
+            for (int j = 0; j < kCandsPer; ++j) key[j] = S.sorter.key[j * kThreads + t];
+            __syncthreads();
+            draw_from_cands(S.sorter, turn, R, B, H, found, key, &token, &n);
         }
     }
-    store<CAP>(D, m, token, n);
+    store(D, m, token, n);
 }
 
 // ------------------------------------------------------------ a row by several
 
+template <bool WIDE>
 __global__ __launch_bounds__(kThreads)
 void draw_first_kernel(DrawView D) {
     __shared__ Part parts[kWaves];
     const int64_t m = blockIdx.y, lo = blockIdx.x * D.part_len;
     const int t = threadIdx.x;
+    const Args A = args_of(D, m);
     // this part's share of the row's bins
     for (int i = blockIdx.x * kThreads + t; i < kBins; i += D.parts * kThreads) {
         D.count[m * kBins + i] = 0;
         D.mass[m * kBins + i] = 0;
     }
-    const Part p = first_of(D.a.logits + m * D.a.ldl, lo, min(lo + D.part_len, D.a.V), D.vec, parts);
+    const Part p = first_of<WIDE>(D.a.logits + m * D.a.ldl, lo, min(lo + D.part_len, D.a.V), D.vec, parts,
+                            by_runs(D, A) ? D.run + m * D.runs : nullptr);
     if (t == 0) {
         D.part[m * D.parts + blockIdx.x] = p;
         if (blockIdx.x == 0) D.head[m] = Head{};
     }
 }
 
-// The row as its parts say, in every thread of the workgroup.
-template <bool CAP>
-__device__ __forceinline__ Row<CAP> row_of_parts(const DrawView& D, int64_t m) {
+// What the parts say about a row, in every thread.
+__device__ __forceinline__ Part part_of(const DrawView& D, int64_t m) {
     const int lane = threadIdx.x & (kWave - 1);
-    Part p = lane < D.parts ? D.part[m * D.parts + lane] : Part{0, 0.0f, 0};
-    p = join(p);
-    return row_of<CAP>(D, m, p.best, p.sum, p.count);
+    return lane < D.parts ? D.part[m * D.parts + lane] : Part{0, 0.0f, 0};
 }
 
+// A share of the work of the bins or collect kernel: a part of a row.
+struct Unit {
+    int64_t m, lo, hi;
+    bool some;
+};
+
+struct Shares {
+    uint64_t by_runs[kMostSplit / kWave], others[kMostSplit / kWave];
+    int32_t row;
+};
+
+// Which rows there are is known on the device only: rows by runs need hardly
+// any work in these two kernels, and rows of temperature 0 none.  The
+// workgroups share out the others: every row by runs is `run_parts` units, and
+// the other rows have what is left in equal parts.
+__device__ __forceinline__ Unit unit_of(Shares& S, const DrawView& D, int run_parts) {
+    const int t = threadIdx.x, M = static_cast<int>(D.a.M);
+    Unit U = {0, 0, D.a.V, false};
+    int part = blockIdx.x, parts = D.parts;
+    if (M > 1) {
+        if (t < kMostSplit) {  // whole waves
+            bool runs = false, other = false;
+            if (t < M) {
+                const Args A = args_of(D, t);
+                runs = by_runs(D, A);
+                other = A.temperature > 0.0f && !runs;
+            }
+            const uint64_t r = __ballot(runs), o = __ballot(other);
+            if ((t & (kWave - 1)) == 0) {
+                S.by_runs[t / kWave] = r;
+                S.others[t / kWave] = o;
+            }
+        }
+        __syncthreads();
+        int n_runs = 0, n_others = 0;
+#pragma unroll
+        for (int i = 0; i < kMostSplit / kWave; ++i) {
+            n_runs += __popcll(S.by_runs[i]);
+            n_others += __popcll(S.others[i]);
+        }
+        int unit = blockIdx.x, nth;
+        const bool runs = unit < n_runs * run_parts;
+        if (runs) {
+            parts = run_parts;
+        } else {
+            unit -= n_runs * run_parts;
+            if (n_others == 0) return U;
+            // the rows are at most half the workgroups, so that this is at least 1
+            parts = min((static_cast<int>(gridDim.x) - n_runs * run_parts) / n_others, D.most_parts);
+        }
+        nth = unit / parts;
+        part = unit - nth * parts;
+        if (nth >= (runs ? n_runs : n_others)) return U;
+        // the thread of that row finds itself
+        if (t < kMostSplit) {
+            const uint64_t* mask = runs ? S.by_runs : S.others;
+            int before = 0;
+            for (int i = 0; i < t / kWave; ++i) before += __popcll(mask[i]);
+            const uint64_t own = mask[t / kWave], bit = uint64_t{1} << (t & (kWave - 1));
+            if ((own & bit) != 0 && before + __popcll(own & (bit - 1)) == nth) S.row = t;
+        }
+        __syncthreads();
+        U.m = S.row;
+    }
+    const int64_t len = ((D.a.V + parts - 1) / parts + kRun - 1) / kRun * kRun;  // whole runs
+    U.lo = part * len;
+    U.hi = min(U.lo + len, D.a.V);
+    U.some = U.lo < U.hi;
+    return U;
+}
+
+// Bins of a part of a row.  Rows by runs: one workgroup counts their runs, and
+// says which bins to collect.
 template <bool CAP>
 __global__ __launch_bounds__(kThreads)
 void draw_bins_kernel(DrawView D) {
     __shared__ uint64_t mass[kBins];
     __shared__ uint32_t count[kBins];
-    __shared__ Scan scan;
-    const int64_t m = blockIdx.y, lo = blockIdx.x * D.part_len;
+    __shared__ Ask ask;
+    __shared__ Shares shares;
     const int t = threadIdx.x;
-    Row<CAP> R = row_of_parts<CAP>(D, m);
-    if (R.mode == kFirst) return;
+    const Unit U = unit_of(shares, D, 1);
+    if (!U.some) return;
+    const int64_t m = U.m;
+    const Args A = args_of(D, m);
+    const bool runs = by_runs(D, A);
+    if (!(A.temperature > 0.0f) || (runs && U.lo > 0)) return;
+    Part p = part_of(D, m);
+    Batch first;
+    if (!runs) first = load_batch(D.a.logits + m * D.a.ldl, U.lo, U.hi, D.vec);
     fill_exp_table();
     for (int i = t; i < kBins; i += kThreads) {
         count[i] = 0;
         mass[i] = 0;
     }
+    p = join(p);
+    Row<CAP> R = row_of<CAP>(D, m, A, p.best, p.sum, p.count);
+    if (R.mode == kFirst) return;
     __syncthreads();
+    int turn = 0;
+    if (R.mode == kByRuns) {
+        const float* run = D.run + m * D.runs;
+        for (int64_t i = t; i < D.runs; i += 4 * kThreads) {
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = i + j * kThreads < D.runs ? run[i + j * kThreads] : kNegInf;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (weighs(v[j])) atomicAdd(&count[R.bin_of(v[j])], 1u);
+        }
+        __syncthreads();
+        Bins B = load_bins(count, mass);
+        sum_bins(ask, turn, B);
+        const Head H = choose_bins(ask, R, B, {0, 0});
+        if (t == 0) D.head[m].u_hi = H.u_hi;
+        return;
+    }
     R.level_of_top();
-    const Sum mine = fill_bins(D, R, lo, min(lo + D.part_len, D.a.V), count, mass);
+    const Sum mine = fill_bins(first, D, R, U.lo, U.hi, count, mass);
     __syncthreads();
     if (R.has_min && R.mode == kSummed) {
         Sum above;
-        block_before(scan, mine, &above);
+        block_before(ask.scan, turn, mine, &above);
         if (t == 0 && above.count) {
             atomicAdd(&D.head[m].above_count, above.count);
             atomicAdd(reinterpret_cast<unsigned long long*>(&D.head[m].above_mass),
@@ -767,30 +1068,72 @@ __global__ __launch_bounds__(kThreads)
 void draw_collect_kernel(DrawView D) {
     __shared__ uint64_t keys[kMostCands];
     __shared__ Ask ask;
-    __shared__ uint32_t n, base;
-    const int64_t m = blockIdx.y, lo = blockIdx.x * D.part_len;
+    __shared__ uint32_t n, base, listed;
+    __shared__ int32_t list[kThreads];
+    __shared__ Shares shares;
     const int t = threadIdx.x;
-    const Row<CAP> R = row_of_parts<CAP>(D, m);
-    if (R.mode == kFirst) return;
-    if (t == 0) n = 0;
-    const Bins B = load_bins(ask, D.count + m * kBins, D.mass + m * kBins, R.mode == kSummed);
+    const Unit U = unit_of(shares, D, D.run_parts);
+    if (!U.some) return;
+    const int64_t m = U.m, lo = U.lo, hi = U.hi;
+    const Args A = args_of(D, m);
+    Part p = part_of(D, m);
     Head* head = D.head + m;
-    const Head H = choose_bins(ask, R, B, {head->above_mass, head->above_count});
-    if (blockIdx.x == 0 && t == 0) {
-        head->k_bin = H.k_bin;
-        head->p_lo = H.p_lo;
-        head->p_hi = H.p_hi;
-        head->u_lo = H.u_lo;
-        head->u_hi = H.u_hi;
-        head->cands = H.cands;
+    Head H = *head;
+    if (!(A.temperature > 0.0f)) return;
+    Bins B = {};
+    Batch first;
+    if (!by_runs(D, A)) {
+        B = load_bins(D.count + m * kBins, D.mass + m * kBins);
+        first = load_batch(D.a.logits + m * D.a.ldl, lo, hi, D.vec);
     }
-    if (H.cands > kMostCands) return;
-    collect(D, R, H, lo, min(lo + D.part_len, D.a.V), keys, &n);
+    if (t == 0) n = listed = 0;
+    p = join(p);
+    const Row<CAP> R = row_of<CAP>(D, m, A, p.best, p.sum, p.count);
+    if (R.mode == kFirst) return;
+    if (R.mode == kByRuns) {
+        __syncthreads();
+        // only runs that reach the bins are read, by 16 threads each
+        const float* run = D.run + m * D.runs;
+        const int64_t r0 = lo / kRun, r1 = (hi + kRun - 1) / kRun;
+        for (int64_t r = r0; r < r1; r += kThreads) {
+            const float top = r + t < r1 ? run[r + t] : kNegInf;
+            if (weighs(top) && R.bin_of(top) <= H.u_hi) list[atomicAdd(&listed, 1u)] = static_cast<int32_t>(r + t - r0);
+            __syncthreads();
+            const uint32_t have = listed;
+            for (uint32_t i = t / 16; i < have; i += kThreads / 16) {
+                const int64_t at = (r0 + list[i]) * kRun + (t & 15) * 4;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v = at + e < hi ? R.y[at + e] : kNegInf;
+                    if (!weighs(v) || R.bin_of(v) > H.u_hi) continue;
+                    const uint32_t to = atomicAdd(&n, 1u);
+                    if (to < kMostCands) keys[to] = key_of(v, at + e);
+                }
+            }
+            __syncthreads();
+            if (t == 0) listed = 0;
+            __syncthreads();
+        }
+    } else {
+        int turn = 0;
+        sum_bins(ask, turn, B);
+        H = choose_bins(ask, R, B, {H.above_mass, H.above_count});
+        if (lo == 0 && t == 0) {
+            head->k_bin = H.k_bin;
+            head->p_lo = H.p_lo;
+            head->p_hi = H.p_hi;
+            head->u_lo = H.u_lo;
+            head->u_hi = H.u_hi;
+        }
+        collect(first, D, R, H, lo, hi, keys, &n);
+    }
     __syncthreads();
-    if (n == 0) return;
-    if (t == 0) base = atomicAdd(&head->collected, n);
+    const uint32_t found = n;
+    if (found == 0) return;
+    if (t == 0) base = atomicAdd(&head->collected, found);
     __syncthreads();
-    for (uint32_t i = t; i < n; i += kThreads) D.cand[m * kMostCands + base + i] = keys[i];
+    for (uint32_t i = t; i < found && i < kMostCands; i += kThreads)
+        if (base + i < kMostCands) D.cand[m * kMostCands + base + i] = keys[i];
 }
 
 template <bool CAP>
@@ -802,22 +1145,36 @@ void draw_token_kernel(DrawView D) {
     };
     __shared__ Lds S;
     const int64_t m = blockIdx.x;
-    Row<CAP> R = row_of_parts<CAP>(D, m);
+    Part p = part_of(D, m);
+    const Args A = args_of(D, m);
+    Head H = D.head[m];
+    uint64_t key[kCandsPer];
+    const uint64_t* cand = D.cand + m * kMostCands;
+    key[0] = cand[threadIdx.x];
+    fill_exp_table();
+    Bins B = {};
+    if (A.temperature > 0.0f && !by_runs(D, A)) B = load_bins(D.count + m * kBins, D.mass + m * kBins);
+#pragma unroll
+    for (int j = 1; j < kCandsPer; ++j) {
+        key[j] = 0;
+        if (j * kThreads < H.collected) key[j] = cand[j * kThreads + threadIdx.x];
+    }
+    p = join(p);
+    Row<CAP> R = row_of<CAP>(D, m, A, p.best, p.sum, p.count);
     int32_t token = R.best ? index_of(R.best) : -1, n = R.best ? 1 : 0;
     if (R.mode != kFirst) {
-        fill_exp_table();
         __syncthreads();
         R.level_of_top();
-        const Head H = D.head[m];
-        if (H.cands > kMostCands) {
-            draw_by_digits(S.digits, D, R, &token, &n);
+        if (R.mode == kByRuns) H.k_bin = H.p_hi = -1, H.p_lo = H.u_lo = 0;
+        if (H.collected > kMostCands) {
+            by_digits(S.digits, D, R, &token, &n);
         } else {
-            const Bins B = load_bins(S.sorter.ask, D.count + m * kBins, D.mass + m * kBins, R.mode == kSummed);
-            for (uint32_t i = threadIdx.x; i < H.cands; i += kThreads) S.sorter.key[i] = D.cand[m * kMostCands + i];
-            draw_from_cands(S.sorter, R, B, H, &token, &n);
+            int turn = 0;
+            if (R.mode == kSummed) sum_bins(S.sorter.ask, turn, B);
+            draw_from_cands(S.sorter, turn, R, B, H, H.collected, key, &token, &n);
         }
     }
-    store<CAP>(D, m, token, n);
+    store(D, m, token, n);
 }
 
 template <bool CAP>
@@ -828,25 +1185,32 @@ hipError_t launch(const DrawView& D, hipStream_t stream) {
         return hipGetLastError();
     }
     const dim3 grid(static_cast<unsigned>(D.parts), static_cast<unsigned>(D.a.M));
-    hipLaunchKernelGGL(draw_first_kernel, grid, block, 0, stream, D);
+    if (D.part_len >= kStep)
+        hipLaunchKernelGGL(draw_first_kernel<true>, grid, block, 0, stream, D);
+    else
+        hipLaunchKernelGGL(draw_first_kernel<false>, grid, block, 0, stream, D);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(draw_bins_kernel<CAP>, grid, block, 0, stream, D);
+    const dim3 shares(static_cast<unsigned>(D.parts * D.a.M));
+    hipLaunchKernelGGL(draw_bins_kernel<CAP>, shares, block, 0, stream, D);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(draw_collect_kernel<CAP>, grid, block, 0, stream, D);
+    hipLaunchKernelGGL(draw_collect_kernel<CAP>, shares, block, 0, stream, D);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(draw_token_kernel<CAP>, rows, block, 0, stream, D);
     return hipGetLastError();
 }
 
-// Workgroups of a row: about 512 in all, 4096 logits each at least.
+// Workgroups of a row: about 512 in all (two a CU), 4096 logits each at least.
+constexpr int64_t kPartLeast = 4096;
 int parts_of(int64_t V, int64_t M) {
-    const int64_t most = (V + 4095) / 4096, want = 512 / M;
+    const int64_t most = (V + kPartLeast - 1) / kPartLeast, want = kWorkgroups / M;
     const int64_t parts = want < most ? want : most;
     return static_cast<int>(parts < 1 ? 1 : (parts > kMaxParts ? kMaxParts : parts));
 }
+
+int64_t runs_of(int64_t V) { return (V + kRun - 1) / kRun; }
 
 size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
@@ -857,7 +1221,8 @@ size_t draw_ws_bytes(int64_t V, int64_t M) {
     if (parts == 1) return 256;
     const size_t m = static_cast<size_t>(M);
     return align256(m * static_cast<size_t>(parts) * sizeof(Part)) + align256(m * sizeof(Head)) +
-           m * (kBins * (sizeof(uint32_t) + sizeof(uint64_t)) + kMostCands * sizeof(uint64_t));
+           m * (kBins * (sizeof(uint32_t) + sizeof(uint64_t)) + kMostCands * sizeof(uint64_t)) +
+           align256(m * static_cast<size_t>(runs_of(V)) * sizeof(float));
 }
 
 hipError_t launch_logits_draw(const DrawArgs& a, void* ws, hipStream_t stream) {
@@ -868,8 +1233,14 @@ hipError_t launch_logits_draw(const DrawArgs& a, void* ws, hipStream_t stream) {
     while ((int64_t{1} << bits) < a.V) ++bits;
     D.q = 62 - bits < 51 ? 62 - bits : 51;
     D.parts = parts_of(a.V, a.M);
-    D.part_len = ((a.V + D.parts - 1) / D.parts + 3) / 4 * 4;
+    const int64_t most = (a.V + kPartLeast - 1) / kPartLeast;
+    D.most_parts = static_cast<int>(most < kMaxParts ? most : kMaxParts);
+    // half the workgroups, were all rows by runs
+    D.run_parts = D.parts / 2 < 16 ? (D.parts > 1 ? D.parts / 2 : 1) : 16;
+    // whole runs, which are whole quads
+    D.part_len = ((a.V + D.parts - 1) / D.parts + kRun - 1) / kRun * kRun;
     D.vec = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && a.ldl % 4 == 0;
+    D.runs = D.parts > 1 ? runs_of(a.V) : 0;
     const size_t m = static_cast<size_t>(a.M);
     char* p = static_cast<char*>(ws);
     D.part = reinterpret_cast<Part*>(p);
@@ -881,6 +1252,8 @@ hipError_t launch_logits_draw(const DrawArgs& a, void* ws, hipStream_t stream) {
     D.cand = reinterpret_cast<uint64_t*>(p);
     p += m * kMostCands * sizeof(uint64_t);
     D.count = reinterpret_cast<uint32_t*>(p);
+    p += m * kBins * sizeof(uint32_t);
+    D.run = reinterpret_cast<float*>(p);
     return a.softcap > 0.0f ? launch<true>(D, stream) : launch<false>(D, stream);
 }
 
