@@ -15,10 +15,12 @@
 // the weights, has a lane an output instead.
 //
 // The operands' k index is a dummy: lane (i, g) = (l % 16, l / 16) holds
-// eight (four in expand) neighbouring elements of its row, and instruction e
-// takes element e of each, so that loads are 16 (8) bytes.  Results: lane (i,
-// g) has rows 4 g .. 4 g + 3 of column i: four neighbouring ranks, or outputs,
-// of row i.
+// eight neighbouring elements of its row (four of ranks up to 16), and
+// instruction e takes element e of each, so that loads are 16 (8) bytes.
+// Results: lane (i, g) has rows 4 g .. 4 g + 3 of column i.  In shrink these
+// are four neighbouring ranks of x's row i; in expand rows of y, whose column i
+// is output n0 + 4 i + u in the u-th of four products, so that the four are
+// neighbours and a load or store of y is 256 bytes in a row of four rows.
 #include <stdint.h>
 
 #include <type_traits>
@@ -48,9 +50,8 @@ struct LoraView {
 
 // A tile's rows and its adapter.
 struct Tile {
-    int row, rows;  // rows <= 0: nothing to do
-    int slot;       // -1: no adapter
-    int rank;
+    int row, rows;  // rows 0: nothing to do
+    int slot;       // as the caller gave it
 };
 
 // Sequence b's tiles have the numbers from row_start[b] / 16 + b on: enough for
@@ -70,19 +71,22 @@ __device__ __forceinline__ Tile tile_of(const LoraView& D, int tile) {
         lo += c * step;
         span = left < step - 1 ? left : step - 1;
     }
-    Tile t = {0, 0, -1, 0};
+    Tile t = {0, 0, -1};
     if (lo >= D.a.B) return t;
     const int64_t first = start[lo], end = min(static_cast<int64_t>(start[lo + 1]), D.a.T);
     const int64_t row = first + kTile * (tile - (first >> 4) - lo);
     if (row < 0 || row >= end) return t;
     t.row = static_cast<int>(row);
     t.rows = static_cast<int>(min(end - row, static_cast<int64_t>(kTile)));
-    const int s = D.a.adapter[lo];
-    if (s < 0 || s >= D.l.slots) return t;
-    t.slot = s;
-    const int r = D.l.rank ? D.l.rank[s] : D.l.max_rank;
-    t.rank = r < 0 ? 0 : (r > D.l.max_rank ? D.l.max_rank : r);
+    t.slot = D.a.adapter[lo];
     return t;
+}
+
+// The tile's rank, 0 without an adapter.
+__device__ __forceinline__ int rank_of(const LoraView& D, const Tile& t) {
+    if (t.slot < 0 || t.slot >= D.l.slots) return 0;
+    const int r = D.l.rank ? D.l.rank[t.slot] : D.l.max_rank;
+    return r < 0 ? 0 : (r > D.l.max_rank ? D.l.max_rank : r);
 }
 
 // Elements I of a vector of 16-bit weights, as float32.
@@ -104,61 +108,71 @@ template <bool BF16, int RT>
 __global__ __launch_bounds__(kBlockThreads)
 void lora_shrink_kernel(LoraView D) {
     __shared__ f32x4 lds[kWaves][RT][kWave];
+    // steps of 32 k that are loaded at once: their latency is the time of this
+    // kernel, and 128 k are a wave's share where there are many
+    constexpr int kSteps = RT <= 4 ? 4 : (RT <= 8 ? 2 : 1);
     const Tile t = tile_of(D, blockIdx.x);
-    if (t.rows <= 0 || t.slot < 0 || t.rank == 0) return;
+    if (t.rows == 0) return;
     const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1), i = lane & 15, g = lane >> 4;
-    const int tiles = (t.rank + 15) / 16;
     const float* x = D.a.x + (t.row + min(i, t.rows - 1)) * D.a.ldx;
-    const uint16_t* A = static_cast<const uint16_t*>(D.l.A) + static_cast<int64_t>(t.slot) * D.l.max_rank * D.l.K;
     const int64_t lo = (static_cast<int64_t>(blockIdx.y) * kWaves + wave) * D.k_wave, hi = min(lo + D.k_wave, D.l.K);
-    f32x4 acc[RT] = {};
-    struct Loads {
-        f32x4 x[2];
-        uint32_t a[RT][4];
-    };
-    auto load = [&](int64_t k0) {
-        Loads L;
-        const int64_t k = k0 + 8 * g;
-        const bool in = k < hi;
-        const int64_t kc = in ? k : 0;
-        if (D.x_vec) {
-            L.x[0] = *reinterpret_cast<const f32x4*>(x + kc);
-            L.x[1] = *reinterpret_cast<const f32x4*>(x + kc + 4);
-        } else {
+    f32x4 xs[kSteps][2];
+    auto load_x = [&](int64_t k0) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                L.x[0][e] = x[kc + e];
-                L.x[1][e] = x[kc + 4 + e];
+        for (int s = 0; s < kSteps; ++s) {
+            const int64_t k = k0 + 32 * s + 8 * g;
+            const bool in = k < hi;
+            const float* p = x + (in ? k : 0);
+            if (D.x_vec) {
+                xs[s][0] = *reinterpret_cast<const f32x4*>(p);
+                xs[s][1] = *reinterpret_cast<const f32x4*>(p + 4);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    xs[s][0][e] = p[e];
+                    xs[s][1][e] = p[4 + e];
+                }
+            }
+            if (!in) xs[s][0] = xs[s][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+    };
+    load_x(lo);  // while the adapter is looked up
+    const int rank = rank_of(D, t);
+    if (rank == 0) return;
+    const int tiles = (rank + 15) / 16;
+    const uint16_t* A = static_cast<const uint16_t*>(D.l.A) + static_cast<int64_t>(t.slot) * D.l.max_rank * D.l.K;
+    f32x4 acc[RT] = {};
+    for (int64_t k0 = lo; k0 < hi; k0 += 32 * kSteps) {
+        if (k0 > lo) load_x(k0);
+        uint32_t a[kSteps][RT][4];
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int64_t k = k0 + 32 * s + 8 * g;
+            const bool in = k < hi;
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                if (r >= tiles) continue;
+                const int j = 16 * r + i;
+                const bool real = in && j < rank;  // what lies behind the rank or K may be anything
+                const uint4 w = *reinterpret_cast<const uint4*>(A + (j < rank ? j : 0) * D.l.K + (in ? k : 0));
+                a[s][r][0] = real ? w.x : 0u;
+                a[s][r][1] = real ? w.y : 0u;
+                a[s][r][2] = real ? w.z : 0u;
+                a[s][r][3] = real ? w.w : 0u;
             }
         }
-        if (!in) L.x[0] = L.x[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            if (r >= tiles) continue;
-            const int j = 16 * r + i;
-            const bool real = in && j < t.rank;  // what lies behind the rank or K may be anything
-            const uint4 w = *reinterpret_cast<const uint4*>(A + (j < t.rank ? j : 0) * D.l.K + kc);
-            L.a[r][0] = real ? w.x : 0u;
-            L.a[r][1] = real ? w.y : 0u;
-            L.a[r][2] = real ? w.z : 0u;
-            L.a[r][3] = real ? w.w : 0u;
-        }
-        return L;
-    };
-    if (lo < hi) {
-        Loads now = load(lo);
-        for (int64_t k0 = lo; k0 < hi; k0 += 32) {
-            Loads next;
-            if (k0 + 32 < hi) next = load(k0 + 32);
+        for (int s = 0; s < kSteps; ++s) {
+            if (k0 + 32 * s >= hi) continue;
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 if (r >= tiles) continue;
                 static_for<8>([&](auto e) {
-                    acc[r] = __builtin_amdgcn_mfma_f32_16x16x4f32(element<BF16, e>(now.a[r]), now.x[decltype(e)::value / 4][decltype(e)::value % 4], acc[r], 0,
+                    constexpr int kE = decltype(e)::value;
+                    acc[r] = __builtin_amdgcn_mfma_f32_16x16x4f32(element<BF16, kE>(a[s][r]), xs[s][kE / 4][kE % 4], acc[r], 0,
                                                                   0, 0);
                 });
             }
-            now = next;
         }
     }
 #pragma unroll
@@ -175,17 +189,27 @@ void lora_shrink_kernel(LoraView D) {
     }
 }
 
-// base + add to y, four outputs from n on (fewer at the end of the row).
-__device__ __forceinline__ void update4(const LoraView& D, int64_t row, int64_t n, const f32x4& add) {
-    const float* b = D.a.base ? D.a.base + row * D.a.ldb + n : nullptr;
-    float* y = D.a.y + row * D.a.ldy + n;
-    if (D.y_vec && n + 4 <= D.l.N) {
-        f32x4 v = b ? *reinterpret_cast<const f32x4*>(b) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        *reinterpret_cast<f32x4*>(y) = v + add;
+// Four elements of a row from n on, whose last one is n_end - 1 (zeros behind it).
+__device__ __forceinline__ f32x4 load4_of(const float* p, int64_t n, int64_t n_end, bool vec) {
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (vec && n + 4 <= n_end) {
+        v = *reinterpret_cast<const f32x4*>(p + n);
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (n + e < D.l.N) y[e] = (b ? b[e] : 0.0f) + add[e];
+            if (n + e < n_end) v[e] = p[n + e];
+    }
+    return v;
+}
+
+// Results are not read again here and go past the L2.
+__device__ __forceinline__ void store4_of(float* p, int64_t n, int64_t n_end, bool vec, const f32x4& v) {
+    if (vec && n + 4 <= n_end) {
+        __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(p + n));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n + e < n_end) p[n + e] = v[e];
     }
 }
 
@@ -194,14 +218,19 @@ __global__ __launch_bounds__(kBlockThreads)
 void lora_expand_kernel(LoraView D) {
     __shared__ float v_row[256];
     const Tile t = tile_of(D, blockIdx.x);
-    if (t.rows <= 0) return;
+    if (t.rows == 0) return;
     const int64_t lo = static_cast<int64_t>(blockIdx.y) * D.n_share, hi = min(lo + D.n_share, D.l.N);
     const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1), i = lane & 15, g = lane >> 4;
-    if (t.slot < 0 || t.rank == 0) {
+    const int rank = rank_of(D, t);
+    if (rank == 0) {
         if (D.a.base == D.a.y) return;
-        for (int r = 0; r < t.rows; ++r)
-            for (int64_t n = lo + 4 * threadIdx.x; n < hi; n += 4 * kBlockThreads)
-                update4(D, t.row + r, n, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+        for (int64_t n = lo + 4 * threadIdx.x; n < hi; n += 4 * kBlockThreads) {
+#pragma unroll 4
+            for (int r = 0; r < t.rows; ++r) {
+                const f32x4 b = D.a.base ? load4_of(D.a.base + (t.row + r) * D.a.ldb, n, hi, D.y_vec) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                store4_of(D.a.y + (t.row + r) * D.a.ldy, n, hi, D.y_vec, b);
+            }
+        }
         return;
     }
     const float scale = D.l.scale[t.slot];
@@ -209,80 +238,114 @@ void lora_expand_kernel(LoraView D) {
     const int64_t share = D.a.T * D.l.max_rank;  // of K, in part
     const float* part = D.part + static_cast<int64_t>(t.row) * D.l.max_rank;
     if (t.rows == 1) {
-        if (threadIdx.x < t.rank) {
+        const int64_t n = lo + threadIdx.x;  // the share is a thread's output each, or a few
+        constexpr int kVec = RT * 2;         // 16-byte pieces of a row of Bm
+        uint4 w[kVec];
+        float b = 0.0f;
+        auto load = [&](int64_t n) {
+            b = D.a.base ? D.a.base[t.row * D.a.ldb + n] : 0.0f;
+#pragma unroll
+            for (int c = 0; c < kVec; ++c)
+                if (8 * c < rank) w[c] = *reinterpret_cast<const uint4*>(Bm + n * D.l.max_rank + 8 * c);
+        };
+        if (n < hi) load(n);  // while v is summed
+        if (threadIdx.x < RT * 16) {
             float sum = 0.0f;
-            for (int s = 0; s < D.k_shares; ++s) sum += part[s * share + threadIdx.x];
+            if (threadIdx.x < rank)
+                for (int s = 0; s < D.k_shares; ++s) sum += part[s * share + threadIdx.x];
             v_row[threadIdx.x] = sum;
         }
         __syncthreads();
-        for (int64_t n = lo + threadIdx.x; n < hi; n += kBlockThreads) {
-            const uint16_t* w = Bm + n * D.l.max_rank;
+        for (int64_t m = n; m < hi; m += kBlockThreads) {
+            if (m > n) load(m);
             float sum = 0.0f;
-            for (int j = 0; j + 8 <= t.rank; j += 8) {
-                const uint4 q = *reinterpret_cast<const uint4*>(w + j);
-                const uint32_t d[4] = {q.x, q.y, q.z, q.w};
-                static_for<8>([&](auto e) { sum = fmaf(element<BF16, e>(d), v_row[j + e], sum); });
-            }
-            if (t.rank & 7) {
-                const int j = t.rank & ~7;
-                const uint4 q = *reinterpret_cast<const uint4*>(w + j);
-                const uint32_t d[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) {
+                if (8 * c >= rank) continue;
+                const uint32_t d[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
                 static_for<8>([&](auto e) {
-                    if (j + e < t.rank) sum = fmaf(element<BF16, e>(d), v_row[j + e], sum);
+                    constexpr int kE = decltype(e)::value;
+                    const float a = element<BF16, kE>(d);
+                    // what lies behind the rank may be anything
+                    sum = fmaf(8 * c + kE < rank ? a : 0.0f, v_row[8 * c + kE], sum);
                 });
             }
-            const float b = D.a.base ? D.a.base[t.row * D.a.ldb + n] : 0.0f;
-            D.a.y[t.row * D.a.ldy + n] = fmaf(scale, sum, b);
+            D.a.y[t.row * D.a.ldy + m] = fmaf(scale, sum, b);
         }
         return;
     }
-    // v of row i, ranks 16 r + 4 g ..
-    const int tiles = (t.rank + 15) / 16;
-    f32x4 v[RT];
+    constexpr int kE = RT == 1 ? 4 : 8;        // neighbouring ranks of a lane
+    constexpr int kR = RT * 16 / (4 * kE);     // steps of 4 kE ranks
+    constexpr int kAtOnce = kR < 4 ? kR : 4;   // steps whose weights are in registers
+    const int steps = (rank + 4 * kE - 1) / (4 * kE);
+    float v[kR][kE];  // of row i
+    {
+        f32x4 sum[kR][kE / 4] = {};
+        const float* p = part + static_cast<int64_t>(min(i, t.rows - 1)) * D.l.max_rank + kE * g;
+        for (int s = 0; s < D.k_shares; ++s, p += share) {
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        v[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const int j = 16 * r + 4 * g;
-        if (r >= tiles || j >= D.l.max_rank) continue;
-        for (int s = 0; s < D.k_shares; ++s)
-            v[r] += *reinterpret_cast<const f32x4*>(part + s * share + static_cast<int64_t>(min(i, t.rows - 1)) * D.l.max_rank + j);
-    }
-    constexpr int kU = RT <= 2 ? 4 : 2;  // tiles of outputs at a time
-    for (int64_t n0 = lo + wave * (kU * 16); n0 < hi; n0 += kWaves * kU * 16) {
-        f32x4 acc[kU] = {};
-        uint2 w[kU][RT];
+            for (int r = 0; r < kR; ++r)
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int64_t n = min(n0 + 16 * u + i, D.l.N - 1);
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const int j = 16 * r + 4 * g;
-                w[u][r] = make_uint2(0u, 0u);
-                if (r < tiles && j < t.rank) w[u][r] = *reinterpret_cast<const uint2*>(Bm + n * D.l.max_rank + j);
-            }
+                for (int h = 0; h < kE / 4; ++h)
+                    if (4 * kE * r + kE * g + 4 * h < rank) sum[r][h] += *reinterpret_cast<const f32x4*>(p + 4 * kE * r + 4 * h);
         }
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            if (r >= tiles) continue;
-            const int left = t.rank - (16 * r + 4 * g);  // ranks of this lane that count
+        for (int r = 0; r < kR; ++r)
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                uint32_t d[2] = {w[u][r].x, w[u][r].y};
-                if (left < 4) {  // what lies behind the rank may be anything
-                    d[1] = left < 3 ? 0u : d[1] & 0xffffu;
-                    d[0] = left < 1 ? 0u : (left < 2 ? d[0] & 0xffffu : d[0]);
+            for (int e = 0; e < kE; ++e) v[r][e] = 4 * kE * r + kE * g + e < rank ? sum[r][e / 4][e % 4] : 0.0f;
+    }
+    for (int64_t n0 = lo + wave * 64; n0 < hi; n0 += kWaves * 64) {
+        const int64_t n = n0 + 4 * i;
+        f32x4 b[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {  // row 4 g + q
+            b[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (D.a.base && 4 * g + q < t.rows) b[q] = load4_of(D.a.base + (t.row + 4 * g + q) * D.a.ldb, n, hi, D.y_vec);
+        }
+        f32x4 acc[4] = {};
+#pragma unroll
+        for (int r0 = 0; r0 < kR; r0 += kAtOnce) {
+            if (r0 >= steps) continue;
+            uint32_t w[kAtOnce][4][kE / 2];
+#pragma unroll
+            for (int r = 0; r < kAtOnce; ++r) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int j = 4 * kE * (r0 + r) + kE * g;
+                    const uint16_t* p = Bm + min(n + u, D.l.N - 1) * D.l.max_rank + j;
+#pragma unroll
+                    for (int d = 0; d < kE / 2; ++d) w[r][u][d] = 0u;
+                    if (j >= rank) continue;
+                    if constexpr (kE == 8) {
+                        const uint4 q = *reinterpret_cast<const uint4*>(p);
+                        w[r][u][0] = q.x; w[r][u][1] = q.y; w[r][u][2] = q.z; w[r][u][3] = q.w;
+                    } else {
+                        const uint2 q = *reinterpret_cast<const uint2*>(p);
+                        w[r][u][0] = q.x; w[r][u][1] = q.y;
+                    }
                 }
-                static_for<4>([&](auto e) {
-                    acc[u] = __builtin_amdgcn_mfma_f32_16x16x4f32(element<BF16, e>(d), v[r][decltype(e)::value], acc[u], 0, 0, 0);
+            }
+#pragma unroll
+            for (int r = 0; r < kAtOnce; ++r) {
+                if (r0 + r >= steps) continue;
+                const int left = rank - (4 * kE * (r0 + r) + kE * g);  // ranks of this lane that count
+                static_for<kE>([&](auto e) {
+                    constexpr int kI = decltype(e)::value;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const float a = element<BF16, kI>(w[r][u]);
+                        acc[u] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[r0 + r][kI], kI < left ? a : 0.0f, acc[u], 0, 0, 0);
+                    }
                 });
             }
         }
-        if (i < t.rows) {
 #pragma unroll
-            for (int u = 0; u < kU; ++u) {
-                const int64_t n = n0 + 16 * u + 4 * g;
-                if (n < D.l.N) update4(D, t.row + i, n, acc[u] * scale);
-            }
+        for (int q = 0; q < 4; ++q) {
+            if (4 * g + q >= t.rows) continue;
+            f32x4 o;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) o[u] = fmaf(scale, acc[u][q], b[q][u]);
+            store4_of(D.a.y + (t.row + 4 * g + q) * D.a.ldy, n, hi, D.y_vec, o);
         }
     }
 }
