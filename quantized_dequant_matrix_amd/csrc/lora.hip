@@ -7,12 +7,18 @@
 //           their order, so that no atomics are needed
 //   expand  y = base + scale_s Bm_s v, a workgroup a (tile, N share)
 //
-// Both products are float32 matrix instructions (16 x 16 x 4) on weights that
-// become float32 exactly: x and v are not rounded, and the 134 TFLOP/s that
-// they reach are more than the memory asks for up to ranks around 64 (a 16 x
-// 16 tile of y moves 2 KB, which takes as long as 64 ranks' products).  A
-// single row would waste 15 of 16 columns: its expansion, which reads most of
-// the weights, has a lane an output instead.
+// Both products are float32 matrix instructions (16 x 16 x 4, 36 cycles) on
+// weights that become float32 exactly: x and v are not rounded, and the 140
+// TFLOP/s that they reach are more than the memory asks for up to ranks around
+// 64 (a 16 x 16 tile of y moves 2 KB, which takes as long as 64 ranks'
+// products).  A single row would waste 15 of 16 columns: it has the same loads
+// and ordinary multiplications (32 rows of rank 64: 12.4 -> 8.5 us for shrink).
+//
+// Bounds, and what was measured: chunks are bound by HBM (1540 rows, 5376 ->
+// 21504, rank 16: 308 MB in 67 us, 4.6 TB/s); single rows with many adapters by
+// the lines of Bm (a row of Bm of max_rank 64 is a 128-byte line, read whole
+// whatever the adapter's own rank: 32 rows over 24 adapters 24 us, 4.9 TB/s
+// of lines in expand); one row by its two launches (7.9 us).
 //
 // The operands' k index is a dummy: lane (i, g) = (l % 16, l / 16) holds
 // eight neighbouring elements of its row (four of ranks up to 16), and
@@ -28,6 +34,7 @@
 
 #include "qmv_device.h"
 #include "serve_internal.h"
+#include "sort_device.h"
 #include "step_device.h"
 
 namespace qmv {
@@ -60,25 +67,39 @@ struct Tile {
 // wave) without sums over the batch.
 __device__ __forceinline__ Tile tile_of(const LoraView& D, int tile) {
     const int32_t* start = D.a.row_start;
-    const int lane = threadIdx.x & (kWave - 1);
-    int lo = 0, span = static_cast<int>(D.a.B);
-    while (span > 0) {
-        const int step = (span + kWave - 1) / kWave;
-        const int off = (lane + 1) * step;
-        const bool below = off <= span && (start[lo + off] >> 4) + static_cast<int64_t>(lo + off) <= tile;
-        const int c = __popcll(__ballot(below));
-        const int left = span - c * step;
-        lo += c * step;
-        span = left < step - 1 ? left : step - 1;
-    }
+    const int lane = threadIdx.x & (kWave - 1), B = static_cast<int>(D.a.B);
     Tile t = {0, 0, -1};
-    if (lo >= D.a.B) return t;
-    const int64_t first = start[lo], end = min(static_cast<int64_t>(start[lo + 1]), D.a.T);
+    int lo = 0;
+    int64_t first, end;
+    if (B <= kWave) {  // all entries at once
+        const int b = min(lane, B - 1);
+        const int32_t s0 = start[b], s1 = start[b + 1], slot = D.a.adapter[b];
+        lo = __popcll(__ballot(lane < B && (s1 >> 4) + static_cast<int64_t>(lane + 1) <= tile));
+        if (lo >= B) return t;
+        first = __builtin_amdgcn_readlane(s0, lo);
+        end = __builtin_amdgcn_readlane(s1, lo);
+        t.slot = __builtin_amdgcn_readlane(slot, lo);
+    } else {
+        int span = B;
+        while (span > 0) {
+            const int step = (span + kWave - 1) / kWave;
+            const int off = (lane + 1) * step;
+            const bool below = off <= span && (start[lo + off] >> 4) + static_cast<int64_t>(lo + off) <= tile;
+            const int c = __popcll(__ballot(below));
+            const int left = span - c * step;
+            lo += c * step;
+            span = left < step - 1 ? left : step - 1;
+        }
+        if (lo >= B) return t;
+        first = start[lo];
+        end = start[lo + 1];
+        t.slot = D.a.adapter[lo];
+    }
+    end = min(end, D.a.T);
     const int64_t row = first + kTile * (tile - (first >> 4) - lo);
     if (row < 0 || row >= end) return t;
     t.row = static_cast<int>(row);
     t.rows = static_cast<int>(min(end - row, static_cast<int64_t>(kTile)));
-    t.slot = D.a.adapter[lo];
     return t;
 }
 
@@ -97,96 +118,155 @@ __device__ __forceinline__ float element(const uint32_t* w) {
     return half_bits_to_float(I % 2 ? d >> 16 : d & 0xffffu);
 }
 
+// v of lane ^ d.
+__device__ __forceinline__ float xor_lane(float v, int d) {
+    return __uint_as_float(xor_lanes(__float_as_uint(v), d));
+}
+
 template <int N, class F>
 __device__ __forceinline__ void static_for(F&& f) {
     [&]<int... I>(std::integer_sequence<int, I...>) { (f(std::integral_constant<int, I>{}), ...); }
     (std::make_integer_sequence<int, N>{});
 }
 
-// RT: 16 ranks each, at most.
-template <bool BF16, int RT>
-__global__ __launch_bounds__(kBlockThreads)
-void lora_shrink_kernel(LoraView D) {
-    __shared__ f32x4 lds[kWaves][RT][kWave];
+// A wave's share of v = A x: lo .. hi of K, NT times 16 ranks.  Nothing here
+// branches between a load and the next: addresses are held inside the buffers,
+// and what does not count is taken out where it is used.  (Loads behind
+// branches were waited for one by one.)
+template <bool BF16, int NT, bool VEC, bool ONE>
+__device__ __forceinline__ void shrink_wave(const LoraView& D, const float* x, const uint16_t* A, int rank, int64_t lo,
+                                            int64_t hi, f32x4 (&acc)[NT]) {
     // steps of 32 k that are loaded at once: their latency is the time of this
     // kernel, and 128 k are a wave's share where there are many
-    constexpr int kSteps = RT <= 4 ? 4 : (RT <= 8 ? 2 : 1);
-    const Tile t = tile_of(D, blockIdx.x);
-    if (t.rows == 0) return;
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1), i = lane & 15, g = lane >> 4;
-    const float* x = D.a.x + (t.row + min(i, t.rows - 1)) * D.a.ldx;
-    const int64_t lo = (static_cast<int64_t>(blockIdx.y) * kWaves + wave) * D.k_wave, hi = min(lo + D.k_wave, D.l.K);
-    f32x4 xs[kSteps][2];
-    auto load_x = [&](int64_t k0) {
+    constexpr int kSteps = NT <= 4 ? 4 : (NT <= 8 ? 2 : 1);
+    const int lane = threadIdx.x & (kWave - 1), i = lane & 15, g = lane >> 4;
+    const uint16_t* row[NT];
+#pragma unroll
+    for (int r = 0; r < NT; ++r) row[r] = A + min(16 * r + i, rank - 1) * D.l.K;
+    for (int64_t k0 = lo; k0 < hi; k0 += 32 * kSteps) {
+        f32x4 xs[kSteps][2];
+        uint4 a[kSteps][NT];
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-            const int64_t k = k0 + 32 * s + 8 * g;
-            const bool in = k < hi;
-            const float* p = x + (in ? k : 0);
-            if (D.x_vec) {
-                xs[s][0] = *reinterpret_cast<const f32x4*>(p);
-                xs[s][1] = *reinterpret_cast<const f32x4*>(p + 4);
+            const int64_t k = min(k0 + 32 * s + 8 * g, hi - 8);
+            if constexpr (VEC) {
+                xs[s][0] = *reinterpret_cast<const f32x4*>(x + k);
+                xs[s][1] = *reinterpret_cast<const f32x4*>(x + k + 4);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    xs[s][0][e] = p[e];
-                    xs[s][1][e] = p[4 + e];
+                    xs[s][0][e] = x[k + e];
+                    xs[s][1][e] = x[k + 4 + e];
                 }
             }
-            if (!in) xs[s][0] = xs[s][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int r = 0; r < NT; ++r) a[s][r] = *reinterpret_cast<const uint4*>(row[r] + k);
         }
-    };
-    load_x(lo);  // while the adapter is looked up
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const bool in = k0 + 32 * s + 8 * g < hi;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                xs[s][0][e] = in ? xs[s][0][e] : 0.0f;
+                xs[s][1][e] = in ? xs[s][1][e] : 0.0f;
+            }
+            uint32_t w[NT][4];
+#pragma unroll
+            for (int r = 0; r < NT; ++r) {
+                // what lies behind the rank may be anything, and so may x beside it
+                const bool real = in && 16 * r + i < rank;
+                w[r][0] = real ? a[s][r].x : 0u;
+                w[r][1] = real ? a[s][r].y : 0u;
+                w[r][2] = real ? a[s][r].z : 0u;
+                w[r][3] = real ? a[s][r].w : 0u;
+            }
+            static_for<8>([&](auto e) {
+                constexpr int kE = decltype(e)::value;
+#pragma unroll
+                for (int r = 0; r < NT; ++r)
+                    if constexpr (ONE)
+                        acc[r][kE % 4] = fmaf(element<BF16, kE>(w[r]), xs[s][kE / 4][kE % 4], acc[r][kE % 4]);
+                    else
+                        acc[r] = __builtin_amdgcn_mfma_f32_16x16x4f32(element<BF16, kE>(w[r]), xs[s][kE / 4][kE % 4], acc[r], 0, 0,
+                                                                  0);
+            });
+        }
+    }
+}
+
+// The workgroup's: the waves' sums through LDS, in their order.
+template <bool BF16, int NT>
+__device__ __forceinline__ void shrink_tile(const LoraView& D, const Tile& t, int rank, f32x4* lds) {
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1), i = lane & 15;
+    const float* x = D.a.x + (t.row + min(i, t.rows - 1)) * D.a.ldx;
+    const uint16_t* A = static_cast<const uint16_t*>(D.l.A) + static_cast<int64_t>(t.slot) * D.l.max_rank * D.l.K;
+    const int64_t lo = (static_cast<int64_t>(blockIdx.y) * kWaves + wave) * D.k_wave, hi = min(lo + D.k_wave, D.l.K);
+    f32x4 acc[NT] = {};
+    float* part = D.part + (static_cast<int64_t>(blockIdx.y) * D.a.T + t.row) * D.l.max_rank;
+    if (t.rows == 1) {
+        // lane (i, g) has the sum over its k for rank 16 r + i
+        if (D.x_vec)
+            shrink_wave<BF16, NT, true, true>(D, x, A, rank, lo, hi, acc);
+        else
+            shrink_wave<BF16, NT, false, true>(D, x, A, rank, lo, hi, acc);
+        float* sums = reinterpret_cast<float*>(lds);
+#pragma unroll
+        for (int r = 0; r < NT; ++r) {
+            float v = (acc[r][0] + acc[r][1]) + (acc[r][2] + acc[r][3]);
+            v += xor_lane(v, 16);
+            v += xor_lane(v, 32);
+            if (lane < 16) sums[wave * (NT * 16) + 16 * r + lane] = v;
+        }
+        __syncthreads();
+        const int j = threadIdx.x;
+        if (j < NT * 16 && j < D.l.max_rank) {
+            float v = sums[j];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) v += sums[w * (NT * 16) + j];
+            part[j] = v;
+        }
+        return;
+    }
+    if (D.x_vec)
+        shrink_wave<BF16, NT, true, false>(D, x, A, rank, lo, hi, acc);
+    else
+        shrink_wave<BF16, NT, false, false>(D, x, A, rank, lo, hi, acc);
+#pragma unroll
+    for (int r = 0; r < NT; ++r) lds[(wave * NT + r) * kWave + lane] = acc[r];
+    __syncthreads();
+#pragma unroll
+    for (int r0 = 0; r0 < NT; r0 += kWaves) {
+        const int r = r0 + wave, j = 16 * r + 4 * (lane >> 4);
+        if (r >= NT || i >= t.rows || j >= D.l.max_rank) continue;
+        f32x4 sum = lds[r * kWave + lane];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) sum += lds[(w * NT + r) * kWave + lane];
+        *reinterpret_cast<f32x4*>(part + static_cast<int64_t>(i) * D.l.max_rank + j) = sum;
+    }
+}
+
+// RT: 16 ranks each, at most; a tile takes the next power of two of its own.
+template <bool BF16, int RT>
+__global__ __launch_bounds__(kBlockThreads)
+void lora_shrink_kernel(LoraView D) {
+    __shared__ f32x4 lds[kWaves * RT * kWave];
+    const Tile t = tile_of(D, blockIdx.x);
+    if (t.rows == 0) return;
     const int rank = rank_of(D, t);
     if (rank == 0) return;
-    const int tiles = (rank + 15) / 16;
-    const uint16_t* A = static_cast<const uint16_t*>(D.l.A) + static_cast<int64_t>(t.slot) * D.l.max_rank * D.l.K;
-    f32x4 acc[RT] = {};
-    for (int64_t k0 = lo; k0 < hi; k0 += 32 * kSteps) {
-        if (k0 > lo) load_x(k0);
-        uint32_t a[kSteps][RT][4];
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const int64_t k = k0 + 32 * s + 8 * g;
-            const bool in = k < hi;
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                if (r >= tiles) continue;
-                const int j = 16 * r + i;
-                const bool real = in && j < rank;  // what lies behind the rank or K may be anything
-                const uint4 w = *reinterpret_cast<const uint4*>(A + (j < rank ? j : 0) * D.l.K + (in ? k : 0));
-                a[s][r][0] = real ? w.x : 0u;
-                a[s][r][1] = real ? w.y : 0u;
-                a[s][r][2] = real ? w.z : 0u;
-                a[s][r][3] = real ? w.w : 0u;
-            }
-        }
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            if (k0 + 32 * s >= hi) continue;
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                if (r >= tiles) continue;
-                static_for<8>([&](auto e) {
-                    constexpr int kE = decltype(e)::value;
-                    acc[r] = __builtin_amdgcn_mfma_f32_16x16x4f32(element<BF16, kE>(a[s][r]), xs[s][kE / 4][kE % 4], acc[r], 0,
-                                                                  0, 0);
-                });
-            }
-        }
+    if constexpr (RT > 8) {
+        if (rank > 128) return shrink_tile<BF16, 16>(D, t, rank, lds);
     }
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-        if (r < tiles) lds[wave][r][lane] = acc[r];
-    __syncthreads();
-    float* part = D.part + (static_cast<int64_t>(blockIdx.y) * D.a.T + t.row) * D.l.max_rank;
-    for (int o = threadIdx.x; o < tiles * kWave; o += kBlockThreads) {
-        const int r = o / kWave, l = o & (kWave - 1), row = l & 15, j = 16 * r + 4 * (l >> 4);
-        f32x4 sum = lds[0][r][l];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) sum += lds[w][r][l];
-        if (row < t.rows && j < D.l.max_rank) *reinterpret_cast<f32x4*>(part + static_cast<int64_t>(row) * D.l.max_rank + j) = sum;
+    if constexpr (RT > 4) {
+        if (rank > 64) return shrink_tile<BF16, 8>(D, t, rank, lds);
     }
+    if constexpr (RT > 2) {
+        if (rank > 32) return shrink_tile<BF16, 4>(D, t, rank, lds);
+    }
+    if constexpr (RT > 1) {
+        if (rank > 16) return shrink_tile<BF16, 2>(D, t, rank, lds);
+    }
+    shrink_tile<BF16, 1>(D, t, rank, lds);
 }
 
 // Four elements of a row from n on, whose last one is n_end - 1 (zeros behind it).
@@ -213,10 +293,126 @@ __device__ __forceinline__ void store4_of(float* p, int64_t n, int64_t n_end, bo
     }
 }
 
+// v of the tile's rows, summed over the K shares in their order, into LDS (16
+// rows, kStride apart).  Eight shares are asked for at once.
+template <int RT, int kStride>
+__device__ __forceinline__ void sum_shares(const LoraView& D, const Tile& t, int rank, float* lds) {
+    constexpr int kQuads = RT * 4;  // of a row
+    const int64_t share = D.a.T * D.l.max_rank;
+    for (int o = threadIdx.x; o < t.rows * kQuads; o += kBlockThreads) {
+        const int row = o / kQuads, j = 4 * (o & (kQuads - 1));
+        f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (j < rank) {
+            const float* p = D.part + static_cast<int64_t>(t.row + row) * D.l.max_rank + j;
+            for (int s0 = 0; s0 < D.k_shares; s0 += 8) {
+                f32x4 v[8];
+#pragma unroll
+                for (int s = 0; s < 8; ++s) v[s] = *reinterpret_cast<const f32x4*>(p + min(s0 + s, D.k_shares - 1) * share);
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    if (s0 + s < D.k_shares) sum += v[s];
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] = j + e < rank ? sum[e] : 0.0f;
+        }
+        *reinterpret_cast<f32x4*>(lds + row * kStride + j) = sum;
+    }
+    __syncthreads();
+}
+
+// Several rows: 64 outputs a wave and turn.  No branch between loads (see
+// shrink_wave) where the 64 are all there and aligned.
+template <bool BF16, int NT, int kStride>
+__device__ __forceinline__ void expand_rows(const LoraView& D, const Tile& t, int rank, float scale, const uint16_t* Bm,
+                                            int64_t lo, int64_t hi, float* v_lds) {
+    constexpr int kE = NT == 1 ? 4 : 8;       // neighbouring ranks of a lane
+    constexpr int kR = NT * 16 / (4 * kE);    // steps of 4 kE ranks
+    constexpr int kAtOnce = kR < 2 ? kR : 2;  // steps whose weights are in registers
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1), i = lane & 15, g = lane >> 4;
+    const int rows_here = t.rows - 4 * g;  // of this lane's four
+    int64_t at[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) at[q] = t.row + min(4 * g + q, t.rows - 1);
+    f32x4 b[4];
+    uint32_t w[kAtOnce][4][kE / 2];
+    auto load_base = [&](int64_t n0) {
+        const int64_t n = n0 + 4 * i;
+        if (!D.a.base) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) b[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        } else if (D.y_vec && n0 + 64 <= hi) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                b[q] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(D.a.base + at[q] * D.a.ldb + n));
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) b[q] = load4_of(D.a.base + at[q] * D.a.ldb, n, hi, false);
+        }
+    };
+    auto load_weights = [&](int64_t n0, int r0) {
+#pragma unroll
+        for (int r = 0; r < kAtOnce; ++r) {
+            const int j = 4 * kE * (r0 + r) + kE * g;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint16_t* p = Bm + min(n0 + 4 * i + u, D.l.N - 1) * D.l.max_rank + (j < rank ? j : 0);
+                if constexpr (kE == 8) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(p);
+                    w[r][u][0] = q.x; w[r][u][1] = q.y; w[r][u][2] = q.z; w[r][u][3] = q.w;
+                } else {
+                    const uint2 q = *reinterpret_cast<const uint2*>(p);
+                    w[r][u][0] = q.x; w[r][u][1] = q.y;
+                }
+            }
+        }
+    };
+    // the first turn's loads while v is summed
+    const int64_t first = lo + wave * 64;
+    if (first < hi) {
+        load_base(first);
+        load_weights(first, 0);
+    }
+    sum_shares<NT, kStride>(D, t, rank, v_lds);
+    float v[kR][kE];  // of row i
+#pragma unroll
+    for (int r = 0; r < kR; ++r)
+#pragma unroll
+        for (int e = 0; e < kE; ++e) v[r][e] = v_lds[min(i, t.rows - 1) * kStride + 4 * kE * r + kE * g + e];
+    for (int64_t n0 = first; n0 < hi; n0 += kWaves * 64) {
+        const int64_t n = n0 + 4 * i;
+        if (n0 > first) load_base(n0);
+        f32x4 acc[4] = {};
+#pragma unroll
+        for (int r0 = 0; r0 < kR; r0 += kAtOnce) {
+            if (n0 > first || r0 > 0) load_weights(n0, r0);
+#pragma unroll
+            for (int r = 0; r < kAtOnce; ++r) {
+                const int left = rank - (4 * kE * (r0 + r) + kE * g);  // ranks of this lane that count
+                static_for<kE>([&](auto e) {
+                    constexpr int kI = decltype(e)::value;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const float a = element<BF16, kI>(w[r][u]);
+                        acc[u] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[r0 + r][kI], kI < left ? a : 0.0f, acc[u], 0, 0, 0);
+                    }
+                });
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            f32x4 o;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) o[u] = fmaf(scale, acc[u][q], b[q][u]);
+            if (q < rows_here) store4_of(D.a.y + at[q] * D.a.ldy, n, hi, D.y_vec && n0 + 64 <= hi, o);
+        }
+    }
+}
+
 template <bool BF16, int RT>
 __global__ __launch_bounds__(kBlockThreads)
 void lora_expand_kernel(LoraView D) {
-    __shared__ float v_row[256];
+    constexpr int kStride = RT * 16 + 4;
+    __shared__ __align__(16) float v_lds[kTile * kStride];
     const Tile t = tile_of(D, blockIdx.x);
     if (t.rows == 0) return;
     const int64_t lo = static_cast<int64_t>(blockIdx.y) * D.n_share, hi = min(lo + D.n_share, D.l.N);
@@ -235,131 +431,87 @@ void lora_expand_kernel(LoraView D) {
     }
     const float scale = D.l.scale[t.slot];
     const uint16_t* Bm = static_cast<const uint16_t*>(D.l.Bm) + static_cast<int64_t>(t.slot) * D.l.N * D.l.max_rank;
-    const int64_t share = D.a.T * D.l.max_rank;  // of K, in part
-    const float* part = D.part + static_cast<int64_t>(t.row) * D.l.max_rank;
     if (t.rows == 1) {
-        const int64_t n = lo + threadIdx.x;  // the share is a thread's output each, or a few
-        constexpr int kVec = RT * 2;         // 16-byte pieces of a row of Bm
-        uint4 w[kVec];
-        float b = 0.0f;
-        auto load = [&](int64_t n) {
-            b = D.a.base ? D.a.base[t.row * D.a.ldb + n] : 0.0f;
+        sum_shares<RT, kStride>(D, t, rank, v_lds);
+        // kL lanes hold a row of Bm, eight ranks each, so that a wave reads
+        // whole rows one after the other; of kL loads every lane keeps one sum
+        constexpr int kL = RT * 2, kRows = kWave / kL;
+        const int piece = lane & (kL - 1), sub = lane / kL;
+        const bool in = 8 * piece < rank;
+        float v[8];
 #pragma unroll
-            for (int c = 0; c < kVec; ++c)
-                if (8 * c < rank) w[c] = *reinterpret_cast<const uint4*>(Bm + n * D.l.max_rank + 8 * c);
-        };
-        if (n < hi) load(n);  // while v is summed
-        if (threadIdx.x < RT * 16) {
-            float sum = 0.0f;
-            if (threadIdx.x < rank)
-                for (int s = 0; s < D.k_shares; ++s) sum += part[s * share + threadIdx.x];
-            v_row[threadIdx.x] = sum;
-        }
-        __syncthreads();
-        for (int64_t m = n; m < hi; m += kBlockThreads) {
-            if (m > n) load(m);
-            float sum = 0.0f;
+        for (int e = 0; e < 8; ++e) v[e] = v_lds[8 * piece + e];
+        for (int64_t n0 = lo + wave * kWave; n0 < hi; n0 += kWaves * kWave) {
+            uint4 w[kL];
 #pragma unroll
-            for (int c = 0; c < kVec; ++c) {
-                if (8 * c >= rank) continue;
-                const uint32_t d[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+            for (int u = 0; u < kL; ++u) {
+                const int64_t n = min(n0 + u * kRows + sub, D.l.N - 1);
+                w[u] = *reinterpret_cast<const uint4*>(Bm + n * D.l.max_rank + (in ? 8 * piece : 0));
+            }
+            const int64_t n = n0 + piece * kRows + sub;
+            const float b = D.a.base && n < hi ? D.a.base[t.row * D.a.ldb + n] : 0.0f;
+            float out = 0.0f;
+#pragma unroll
+            for (int u = 0; u < kL; ++u) {
+                const uint32_t d[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+                float sum = 0.0f;
                 static_for<8>([&](auto e) {
                     constexpr int kE = decltype(e)::value;
                     const float a = element<BF16, kE>(d);
                     // what lies behind the rank may be anything
-                    sum = fmaf(8 * c + kE < rank ? a : 0.0f, v_row[8 * c + kE], sum);
+                    sum = fmaf(8 * piece + kE < rank ? a : 0.0f, v[kE], sum);
                 });
+#pragma unroll
+                for (int d = 1; d < kL; d <<= 1) sum += xor_lane(sum, d);
+                out = piece == u ? sum : out;
             }
-            D.a.y[t.row * D.a.ldy + m] = fmaf(scale, sum, b);
+            if (n < hi) D.a.y[t.row * D.a.ldy + n] = fmaf(scale, out, b);
         }
         return;
     }
-    constexpr int kE = RT == 1 ? 4 : 8;        // neighbouring ranks of a lane
-    constexpr int kR = RT * 16 / (4 * kE);     // steps of 4 kE ranks
-    constexpr int kAtOnce = kR < 4 ? kR : 4;   // steps whose weights are in registers
-    const int steps = (rank + 4 * kE - 1) / (4 * kE);
-    float v[kR][kE];  // of row i
-    {
-        f32x4 sum[kR][kE / 4] = {};
-        const float* p = part + static_cast<int64_t>(min(i, t.rows - 1)) * D.l.max_rank + kE * g;
-        for (int s = 0; s < D.k_shares; ++s, p += share) {
-#pragma unroll
-            for (int r = 0; r < kR; ++r)
-#pragma unroll
-                for (int h = 0; h < kE / 4; ++h)
-                    if (4 * kE * r + kE * g + 4 * h < rank) sum[r][h] += *reinterpret_cast<const f32x4*>(p + 4 * kE * r + 4 * h);
-        }
-#pragma unroll
-        for (int r = 0; r < kR; ++r)
-#pragma unroll
-            for (int e = 0; e < kE; ++e) v[r][e] = 4 * kE * r + kE * g + e < rank ? sum[r][e / 4][e % 4] : 0.0f;
+    if constexpr (RT > 8) {
+        if (rank > 128) return expand_rows<BF16, 16, kStride>(D, t, rank, scale, Bm, lo, hi, v_lds);
     }
-    for (int64_t n0 = lo + wave * 64; n0 < hi; n0 += kWaves * 64) {
-        const int64_t n = n0 + 4 * i;
-        f32x4 b[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {  // row 4 g + q
-            b[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (D.a.base && 4 * g + q < t.rows) b[q] = load4_of(D.a.base + (t.row + 4 * g + q) * D.a.ldb, n, hi, D.y_vec);
-        }
-        f32x4 acc[4] = {};
-#pragma unroll
-        for (int r0 = 0; r0 < kR; r0 += kAtOnce) {
-            if (r0 >= steps) continue;
-            uint32_t w[kAtOnce][4][kE / 2];
-#pragma unroll
-            for (int r = 0; r < kAtOnce; ++r) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int j = 4 * kE * (r0 + r) + kE * g;
-                    const uint16_t* p = Bm + min(n + u, D.l.N - 1) * D.l.max_rank + j;
-#pragma unroll
-                    for (int d = 0; d < kE / 2; ++d) w[r][u][d] = 0u;
-                    if (j >= rank) continue;
-                    if constexpr (kE == 8) {
-                        const uint4 q = *reinterpret_cast<const uint4*>(p);
-                        w[r][u][0] = q.x; w[r][u][1] = q.y; w[r][u][2] = q.z; w[r][u][3] = q.w;
-                    } else {
-                        const uint2 q = *reinterpret_cast<const uint2*>(p);
-                        w[r][u][0] = q.x; w[r][u][1] = q.y;
-                    }
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < kAtOnce; ++r) {
-                if (r0 + r >= steps) continue;
-                const int left = rank - (4 * kE * (r0 + r) + kE * g);  // ranks of this lane that count
-                static_for<kE>([&](auto e) {
-                    constexpr int kI = decltype(e)::value;
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const float a = element<BF16, kI>(w[r][u]);
-                        acc[u] = __builtin_amdgcn_mfma_f32_16x16x4f32(v[r0 + r][kI], kI < left ? a : 0.0f, acc[u], 0, 0, 0);
-                    }
-                });
-            }
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (4 * g + q >= t.rows) continue;
-            f32x4 o;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) o[u] = fmaf(scale, acc[u][q], b[q][u]);
-            store4_of(D.a.y + (t.row + 4 * g + q) * D.a.ldy, n, hi, D.y_vec, o);
-        }
+    if constexpr (RT > 4) {
+        if (rank > 64) return expand_rows<BF16, 8, kStride>(D, t, rank, scale, Bm, lo, hi, v_lds);
     }
+    if constexpr (RT > 2) {
+        if (rank > 32) return expand_rows<BF16, 4, kStride>(D, t, rank, scale, Bm, lo, hi, v_lds);
+    }
+    if constexpr (RT > 1) {
+        if (rank > 16) return expand_rows<BF16, 2, kStride>(D, t, rank, scale, Bm, lo, hi, v_lds);
+    }
+    expand_rows<BF16, 1, kStride>(D, t, rank, scale, Bm, lo, hi, v_lds);
 }
 
 // Tiles of the numbering above.
 int64_t tiles_of(int64_t B, int64_t T) { return T / kTile + B; }
 
-// K shares: enough that some 4096 waves are at work, of 128 k a wave at least.
+int64_t tiles_with_rows(int64_t B, int64_t T) { return tiles_of(B, T) < T ? tiles_of(B, T) : T; }  // at most
+
+// K shares: enough that some 4096 waves are at work, each with 128 k (what it
+// loads at once) or a multiple.  More shares of fewer k gain nothing here and
+// cost the expansion their sums (32 rows of rank up to 64: 128 k a wave 24 us,
+// 64 k 25, 32 k 33 when the rest was 4 us slower).
 void split_k(const qmv_lora& l, int64_t B, int64_t T, int* shares, int64_t* per_wave) {
-    const int64_t real = tiles_of(B, T) < T ? tiles_of(B, T) : T;  // tiles that can have rows
-    int64_t want = 1024 / real, most = (l.K + 4 * 128 - 1) / (4 * 128);
+    const int64_t most = (l.K + kWaves * 128 - 1) / (kWaves * 128);
+    int64_t want = 1024 / tiles_with_rows(B, T);
     want = want < 1 ? 1 : (want > most ? most : want);
-    *per_wave = ((l.K + want * kWaves - 1) / (want * kWaves) + 31) / 32 * 32;
+    *per_wave = ((l.K + want * kWaves - 1) / (want * kWaves) + 127) / 128 * 128;
     *shares = static_cast<int>((l.K + *per_wave * kWaves - 1) / (*per_wave * kWaves));
+}
+
+// Outputs of a workgroup of the expand kernel, a multiple of 256: some 4096
+// workgroups for ranks up to 32, where HBM is the limit and an even end counts
+// (1540 rows of 21504, rank 16: 67 us, with 1024 of them 76), some 1024 above,
+// where the start of one, v and its own registers cost more (1460 rows of 5376,
+// rank up to 128: 49 us, with 4096 of them 53).
+int64_t share_n(const qmv_lora& l, int64_t B, int64_t T) {
+    const int64_t workgroups = l.max_rank <= 32 ? 4096 : 1024;
+    int64_t share = (l.N * tiles_with_rows(B, T) / workgroups + 255) / 256 * 256;
+    share = share < 256 ? 256 : (share > 2048 ? 2048 : share);
+    const int64_t least = (l.N / 65535 + 256) / 256 * 256;  // a grid has at most 65535 of them
+    return share < least ? least : share;
 }
 
 template <bool BF16, int RT>
@@ -401,11 +553,7 @@ hipError_t launch_lora(const qmv_lora& l, const LoraArgs& a, void* ws, hipStream
     D.a = a;
     D.part = static_cast<float*>(ws);
     split_k(l, a.B, a.T, &D.k_shares, &D.k_wave);
-    const int64_t real = tiles_of(a.B, a.T) < a.T ? tiles_of(a.B, a.T) : a.T;
-    int64_t share = (l.N * real / 2048 + 255) / 256 * 256;
-    share = share < 256 ? 256 : (share > 2048 ? 2048 : share);
-    const int64_t least = (l.N / 65535 + 256) / 256 * 256;  // a grid has at most 65535 of them
-    D.n_share = share < least ? least : share;
+    D.n_share = share_n(l, a.B, a.T);
     D.x_vec = rows_aligned(a.x, a.ldx);
     D.y_vec = rows_aligned(a.y, a.ldy) && (!a.base || rows_aligned(a.base, a.ldb));
     return l.format == QMV_LORA_BF16 ? launch_rank<true>(D, stream) : launch_rank<false>(D, stream);
