@@ -43,6 +43,7 @@ constexpr int kBins = 4096, kBinsPer = kBins / kThreads;
 constexpr float kEqualBins = 3072.0f;
 constexpr int kMostCands = 4096, kCandsPer = kMostCands / kThreads;
 constexpr int kMostCounted = 2048;  // largest top-k that is collected whole
+constexpr int kSparse = 256;        // logits of a wave's 1024 that are brought together
 constexpr int kRun = 64;            // logits whose largest is kept
 constexpr int kDigitBins = 2048;
 constexpr int kMaxParts = kWave;  // a lane a part when they are joined
@@ -55,7 +56,13 @@ struct Sum {
     uint32_t count;
 };
 
-__device__ __forceinline__ bool weighs(float y) { return y > kNegInf; }  // false for NaN
+// Neither NaN nor -infinity, by the number's bits.  (y > -infinity says the
+// same, but where lanes are counted by it the compiler makes "not equal" of it,
+// which NaN is.)
+__device__ __forceinline__ bool weighs(float y) {
+    const uint32_t b = __float_as_uint(y), from_low = b - 0xff800000u;  // -infinity, then NaN, then 0 ..
+    return (from_low & 0x7fffffffu) >= 0x00800000u || b == 0x7f800000u;
+}
 
 // Larger logits have larger codes; -0 ranks with +0.
 __device__ __forceinline__ uint32_t code_of(float y) {
@@ -150,6 +157,17 @@ struct Row {
         // 12 bits of a float below 3072 lie behind its point
         if (part) *part = equal ? static_cast<int>((x - static_cast<float>(e)) * 4096.0f) : static_cast<int>((past & 0xffffu) >> 4);
         return equal ? e : (b < kBins ? b : kBins - 1);
+    }
+    // A logit below this one lies behind bin `b`: what that bin can reach, and
+    // more than the roundings of bin_of below it.
+    __device__ __forceinline__ float floor_of(int b) const {
+        const float e = static_cast<float>(b + 1);
+        const float x = e <= kEqualBins ? e
+                                        : __uint_as_float(__float_as_uint(kEqualBins) +
+                                                          (static_cast<uint32_t>(b + 1 - static_cast<int>(kEqualBins)) << 16));
+        const float t = x / per_bin * 1.00001f;
+        const float v = top - t - (fabsf(top) + t) * 1e-6f;
+        return b < kBins - 1 ? v : -kMaxLogit;
     }
     // Sums that the answers have to reach.
     __device__ __forceinline__ uint64_t need_p(uint64_t mass) const {
@@ -801,11 +819,12 @@ __device__ __forceinline__ Part first_of(const float* y, int64_t lo, int64_t hi,
     return join(p);
 }
 
-// Counts (and sums) of the logits of [lo, hi) into bins in LDS, zero before.
+// Counts (and sums) of the logits of [lo, hi) into bins in LDS, zero before;
+// sparse: kSparse floats a wave, of its own.
 // Returns this thread's share of those that pass min_p.
 template <bool CAP>
 __device__ __forceinline__ Sum fill_bins(const Batch& first, const DrawView& D, const Row<CAP>& R, int64_t lo, int64_t hi,
-                                         uint32_t* count, uint64_t* mass) {
+                                         uint32_t* count, uint64_t* mass, float* sparse) {
     Sum above = {0, 0};
     if (R.mode == kCounted) {
         for_logits(first, R.y, lo, hi, D.vec, [&](float v, int64_t) {
@@ -813,8 +832,7 @@ __device__ __forceinline__ Sum fill_bins(const Batch& first, const DrawView& D, 
         });
         return above;
     }
-    for_logits(first, R.y, lo, hi, D.vec, [&](float v, int64_t) {
-        if (!weighs(v)) return;
+    auto add = [&](float v) {
         const double e = R.exponent(v);
         const uint64_t w = R.mass_of(e);
         const int b = R.bin_of(v);
@@ -824,7 +842,42 @@ __device__ __forceinline__ Sum fill_bins(const Batch& first, const DrawView& D, 
             above.mass += w;
             above.count += 1;
         }
-    });
+    };
+    const int lane = threadIdx.x & (kWave - 1);
+    float* mine = sparse + (threadIdx.x / kWave) * kSparse;
+    Batch B = first;
+    for (int64_t from = lo; from < hi; from += kStep) {
+        Batch next;
+        if (from + kStep < hi) next = load_batch(R.y, from + kStep, hi, D.vec);
+        uint32_t n = 0;
+#pragma unroll
+        for (int j = 0; j < kU; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) n += static_cast<uint32_t>(__popcll(__ballot(weighs(B.v[j][e]))));
+        if (n <= kSparse) {
+            // mostly forbidden tokens: the others side by side, so that a
+            // weight is not formed for 64 lanes where two have one
+            uint32_t at = 0;
+#pragma unroll
+            for (int j = 0; j < kU; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint64_t some = __ballot(weighs(B.v[j][e]));
+                    if (weighs(B.v[j][e])) mine[at + __popcll(some & ((uint64_t{1} << lane) - 1))] = B.v[j][e];
+                    at += static_cast<uint32_t>(__popcll(some));
+                }
+            __builtin_amdgcn_wave_barrier();
+            for (uint32_t i = lane; i < n; i += kWave) add(mine[i]);
+            __builtin_amdgcn_wave_barrier();
+        } else {
+#pragma unroll
+            for (int j = 0; j < kU; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (weighs(B.v[j][e])) add(B.v[j][e]);
+        }
+        B = next;
+    }
     return above;
 }
 
@@ -833,10 +886,16 @@ __device__ __forceinline__ Sum fill_bins(const Batch& first, const DrawView& D, 
 template <bool CAP>
 __device__ __forceinline__ void collect(const Batch& first, const DrawView& D, const Row<CAP>& R, const Head& H, int64_t lo,
                                         int64_t hi, uint64_t* keys, uint32_t* n) {
-    for_logits(first, R.y, lo, hi, D.vec, [&](float v, int64_t i) {
-        if (!weighs(v) || !chosen(H, R.bin_of(v))) return;
-        const uint32_t at = atomicAdd(n, 1u);
-        if (at < kMostCands) keys[at] = key_of(v, i);
+    // four at a time are dropped, most of them (NaN is not above anything)
+    const float least = R.floor_of(max(H.u_hi, max(H.p_hi, H.k_bin)));
+    for_quads<false>(first, R.y, lo, hi, D.vec, [&](const float (&v)[4], int64_t i) {
+        if (!(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) >= least)) return;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (!(v[e] >= least) || !chosen(H, R.bin_of(v[e]))) continue;
+            const uint32_t at = atomicAdd(n, 1u);
+            if (at < kMostCands) keys[at] = key_of(v[e], i + e);
+        }
     });
 }
 
@@ -849,6 +908,7 @@ void draw_row_kernel(DrawView D) {
         struct {
             uint64_t mass[kBins];
             uint32_t count[kBins];
+            float sparse[kWaves * kSparse];
         } bins;
         Sorter sorter;
         Digits digits;
@@ -875,7 +935,7 @@ void draw_row_kernel(DrawView D) {
         if (t == 0) collected = 0;
         const Batch again = load_batch(y, 0, V, D.vec);
         __syncthreads();
-        const Sum mine = fill_bins(again, D, R, 0, V, S.bins.count, S.bins.mass);
+        const Sum mine = fill_bins(again, D, R, 0, V, S.bins.count, S.bins.mass, S.bins.sparse);
         Sum above;
         block_before(ask.scan, turn, mine, &above);  // and a barrier behind the atomics
         Bins B = load_bins(S.bins.count, S.bins.mass);
@@ -928,7 +988,7 @@ __device__ __forceinline__ Part part_of(const DrawView& D, int64_t m) {
 // A share of the work of the bins or collect kernel: a part of a row.
 struct Unit {
     int64_t m, lo, hi;
-    bool some;
+    bool some, runs;
 };
 
 struct Shares {
@@ -942,7 +1002,7 @@ struct Shares {
 // the other rows have what is left in equal parts.
 __device__ __forceinline__ Unit unit_of(Shares& S, const DrawView& D, int run_parts) {
     const int t = threadIdx.x, M = static_cast<int>(D.a.M);
-    Unit U = {0, 0, D.a.V, false};
+    Unit U = {0, 0, D.a.V, false, false};
     int part = blockIdx.x, parts = D.parts;
     if (M > 1) {
         if (t < kMostSplit) {  // whole waves
@@ -988,6 +1048,9 @@ __device__ __forceinline__ Unit unit_of(Shares& S, const DrawView& D, int run_pa
         }
         __syncthreads();
         U.m = S.row;
+        U.runs = runs;
+    } else {
+        U.runs = by_runs(D, args_of(D, 0));
     }
     const int64_t len = ((D.a.V + parts - 1) / parts + kRun - 1) / kRun * kRun;  // whole runs
     U.lo = part * len;
@@ -1003,18 +1066,18 @@ __global__ __launch_bounds__(kThreads)
 void draw_bins_kernel(DrawView D) {
     __shared__ uint64_t mass[kBins];
     __shared__ uint32_t count[kBins];
+    __shared__ float sparse[kWaves * kSparse];
     __shared__ Ask ask;
     __shared__ Shares shares;
     const int t = threadIdx.x;
     const Unit U = unit_of(shares, D, 1);
     if (!U.some) return;
     const int64_t m = U.m;
-    const Args A = args_of(D, m);
-    const bool runs = by_runs(D, A);
-    if (!(A.temperature > 0.0f) || (runs && U.lo > 0)) return;
-    Part p = part_of(D, m);
     Batch first;
-    if (!runs) first = load_batch(D.a.logits + m * D.a.ldl, U.lo, U.hi, D.vec);
+    if (!U.runs) first = load_batch(D.a.logits + m * D.a.ldl, U.lo, U.hi, D.vec);
+    Part p = part_of(D, m);
+    const Args A = args_of(D, m);
+    if (!(A.temperature > 0.0f) || (U.runs && U.lo > 0)) return;
     fill_exp_table();
     for (int i = t; i < kBins; i += kThreads) {
         count[i] = 0;
@@ -1043,7 +1106,7 @@ void draw_bins_kernel(DrawView D) {
         return;
     }
     R.level_of_top();
-    const Sum mine = fill_bins(first, D, R, U.lo, U.hi, count, mass);
+    const Sum mine = fill_bins(first, D, R, U.lo, U.hi, count, mass, sparse);
     __syncthreads();
     if (R.has_min && R.mode == kSummed) {
         Sum above;
@@ -1075,17 +1138,17 @@ void draw_collect_kernel(DrawView D) {
     const Unit U = unit_of(shares, D, D.run_parts);
     if (!U.some) return;
     const int64_t m = U.m, lo = U.lo, hi = U.hi;
-    const Args A = args_of(D, m);
-    Part p = part_of(D, m);
-    Head* head = D.head + m;
-    Head H = *head;
-    if (!(A.temperature > 0.0f)) return;
     Bins B = {};
     Batch first;
-    if (!by_runs(D, A)) {
+    if (!U.runs) {
         B = load_bins(D.count + m * kBins, D.mass + m * kBins);
         first = load_batch(D.a.logits + m * D.a.ldl, lo, hi, D.vec);
     }
+    Head* head = D.head + m;
+    Head H = *head;
+    Part p = part_of(D, m);
+    const Args A = args_of(D, m);
+    if (!(A.temperature > 0.0f)) return;
     if (t == 0) n = listed = 0;
     p = join(p);
     const Row<CAP> R = row_of<CAP>(D, m, A, p.best, p.sum, p.count);
@@ -1100,15 +1163,29 @@ void draw_collect_kernel(DrawView D) {
             if (weighs(top) && R.bin_of(top) <= H.u_hi) list[atomicAdd(&listed, 1u)] = static_cast<int32_t>(r + t - r0);
             __syncthreads();
             const uint32_t have = listed;
-            for (uint32_t i = t / 16; i < have; i += kThreads / 16) {
-                const int64_t at = (r0 + list[i]) * kRun + (t & 15) * 4;
+            for (uint32_t i = t / 16; i < have; i += 4 * (kThreads / 16)) {  // four at a time
+                float v[4][4];
+                int64_t at[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float v = at + e < hi ? R.y[at + e] : kNegInf;
-                    if (!weighs(v) || R.bin_of(v) > H.u_hi) continue;
-                    const uint32_t to = atomicAdd(&n, 1u);
-                    if (to < kMostCands) keys[to] = key_of(v, at + e);
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t k = i + j * (kThreads / 16);
+                    at[j] = k < have ? (r0 + list[k]) * kRun + (t & 15) * 4 : hi;
+                    if (D.vec && at[j] + 4 <= hi) {
+                        const float4 x = *reinterpret_cast<const float4*>(R.y + at[j]);
+                        v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[j][e] = at[j] + e < hi ? R.y[at[j] + e] : kNegInf;
+                    }
                 }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (!weighs(v[j][e]) || R.bin_of(v[j][e]) > H.u_hi) continue;
+                        const uint32_t to = atomicAdd(&n, 1u);
+                        if (to < kMostCands) keys[to] = key_of(v[j][e], at[j] + e);
+                    }
             }
             __syncthreads();
             if (t == 0) listed = 0;
