@@ -38,8 +38,16 @@
 namespace qmv {
 namespace {
 
-constexpr int kThreads = 1024, kWaves = kThreads / kWave;
-constexpr int kBins = 4096, kBinsPer = kBins / kThreads;
+// Threads of a workgroup, T below.  Besides passing over logits the kernels for
+// the bins do what is the same in every thread (a row's parameters, sums to be
+// reached): fewer waves of more logits each spend less on it (32 rows, top-p:
+// 46 us for the two with 512 threads, 57 with 256, 62 with 1024).  The last
+// kernel has a row a workgroup and few elements, and takes what it can (8-11 us;
+// 10-14 with 512).
+constexpr int kThreads = 1024;
+constexpr int kBinThreads = 512;
+constexpr int kMostWaves = kThreads / kWave;
+constexpr int kBins = 4096;
 constexpr float kEqualBins = 3072.0f;
 constexpr int kMostCands = 4096, kCandsPer = kMostCands / kThreads;
 constexpr int kMostCounted = 2048;  // largest top-k that is collected whole
@@ -241,31 +249,31 @@ __device__ __forceinline__ Row<CAP> row_of(const DrawView& D, int64_t m, const A
     return R;
 }
 
-// 16 logits of a thread, 4 by 4; -infinity past the end.  `from` is a multiple
-// of 4.  WIDE: a wave's batch is 4 KB in a row (128 rows of 262,144 read for
-// their first elements in 33 us, 38 with the four quads a workgroup's width
-// apart); else every wave gets its share of a part that is less than a batch
-// (10.8 against 9.7 us for the bins of one row in parts of 4096).
+// 16 logits of a thread of a workgroup of T, 4 by 4; -infinity past the end.
+// `from` is a multiple of 4.  WIDE: a wave's batch is 4 KB in a row (128 rows of
+// 262,144 read for their first elements in 33 us, 38 with the four quads a
+// workgroup's width apart); else every wave gets its share of a part that is
+// less than a batch.
 constexpr int kU = 4;
-constexpr int64_t kStep = kU * 4 * kThreads;  // logits of a workgroup's batch
+template <int T> constexpr int64_t kStep = kU * 4 * T;  // logits of a workgroup's batch
 
 struct Batch {
     float v[kU][4];
 };
 
-template <bool WIDE>
+template <int T, bool WIDE>
 __device__ __forceinline__ int place_of(int j) {  // of a thread's quad j in a batch
     const int t = static_cast<int>(threadIdx.x);
     if constexpr (WIDE) return (t / kWave) * (kU * 4 * kWave) + j * (4 * kWave) + (t & (kWave - 1)) * 4;
-    return (j * kThreads + t) * 4;
+    return (j * T + t) * 4;
 }
 
-template <bool WIDE = false>
+template <int T, bool WIDE = false>
 __device__ __forceinline__ Batch load_batch(const float* y, int64_t from, int64_t hi, bool vec) {
     Batch B;
 #pragma unroll
     for (int j = 0; j < kU; ++j) {
-        const int64_t at = from + place_of<WIDE>(j);
+        const int64_t at = from + place_of<T, WIDE>(j);
         if (vec && at + 4 <= hi) {
             const float4 x = *reinterpret_cast<const float4*>(y + at);
             B.v[j][0] = x.x; B.v[j][1] = x.y; B.v[j][2] = x.z; B.v[j][3] = x.w;
@@ -279,20 +287,20 @@ __device__ __forceinline__ Batch load_batch(const float* y, int64_t from, int64_
 
 // f(four logits, index of their first) for the logits of [lo, hi); `B` is the
 // first batch, and the next one is asked for before a batch is used.
-template <bool WIDE, class F>
+template <int T, bool WIDE, class F>
 __device__ __forceinline__ void for_quads(Batch B, const float* y, int64_t lo, int64_t hi, bool vec, F&& f) {
-    for (int64_t from = lo; from < hi; from += kStep) {
+    for (int64_t from = lo; from < hi; from += kStep<T>) {
         Batch next;
-        if (from + kStep < hi) next = load_batch<WIDE>(y, from + kStep, hi, vec);
+        if (from + kStep<T> < hi) next = load_batch<T, WIDE>(y, from + kStep<T>, hi, vec);
 #pragma unroll
-        for (int j = 0; j < kU; ++j) f(B.v[j], from + place_of<WIDE>(j));
+        for (int j = 0; j < kU; ++j) f(B.v[j], from + place_of<T, WIDE>(j));
         B = next;
     }
 }
 
-template <class F>
+template <int T, class F>
 __device__ __forceinline__ void for_logits(const Batch& B, const float* y, int64_t lo, int64_t hi, bool vec, F&& f) {
-    for_quads<false>(B, y, lo, hi, vec, [&](const float (&v)[4], int64_t at) {
+    for_quads<T, false>(B, y, lo, hi, vec, [&](const float (&v)[4], int64_t at) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) f(v[e], at + e);
     });
@@ -343,11 +351,12 @@ __device__ __forceinline__ Part join(Part p) {  // over the wave, in every lane
 // Sums of the waves.  Two of them take turns, so that one barrier a scan is
 // enough: who writes one of them again has passed the barrier behind its reads.
 struct Scan {
-    uint64_t mass[2][kWaves];
-    uint32_t count[2][kWaves];
+    uint64_t mass[2][kMostWaves];
+    uint32_t count[2][kMostWaves];
 };
 
 // Sums before this thread in thread order, and the total.
+template <int T>
 __device__ __forceinline__ Sum block_before(Scan& S, int& turn, Sum mine, Sum* total) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x & (kWave - 1);
     const Sum upto = wave_upto<false>(mine);
@@ -357,9 +366,9 @@ __device__ __forceinline__ Sum block_before(Scan& S, int& turn, Sum mine, Sum* t
         S.count[turn][wave] = upto.count;
     }
     __syncthreads();
-    const int w = lane & (kWaves - 1);
-    const Sum waves = wave_upto<true>({S.mass[turn][w], S.count[turn][w]});
-    *total = of_lane(waves, kWaves - 1);
+    const Sum mine_of = lane < (T / kWave) ? Sum{S.mass[turn][lane], S.count[turn][lane]} : Sum{0, 0};
+    const Sum waves = wave_upto<true>(mine_of);
+    *total = of_lane(waves, (T / kWave) - 1);
     Sum before = {upto.mass - mine.mass, upto.count - mine.count};
     if (wave > 0) {
         const Sum w0 = of_lane(waves, wave - 1);
@@ -411,7 +420,7 @@ __device__ __noinline__ Found find(Digits& S, int& turn, const DrawView& D, cons
             S.count[i] = 0;
         }
         __syncthreads();
-        for_logits(load_batch(R.y, 0, D.a.V, D.vec), R.y, 0, D.a.V, D.vec, [&](float v, int64_t i) {
+        for_logits<kThreads>(load_batch<kThreads>(R.y, 0, D.a.V, D.vec), R.y, 0, D.a.V, D.vec, [&](float v, int64_t i) {
             if (!weighs(v)) return;
             const uint64_t key = key_of(v, i);
             if (d > 0 && (key >> high) != (prefix >> high)) return;
@@ -421,14 +430,18 @@ __device__ __noinline__ Found find(Digits& S, int& turn, const DrawView& D, cons
                       static_cast<unsigned long long>(R.mass_of(R.exponent(v))));
         });
         __syncthreads();
-        const Sum two[2] = {{S.mass[2 * t], S.count[2 * t]}, {S.mass[2 * t + 1], S.count[2 * t + 1]}};
-        Sum total;
-        Sum run = block_before(S.scan, turn, {two[0].mass + two[1].mass, two[0].count + two[1].count}, &total);
+        constexpr int kPer = kDigitBins / kThreads;
+        Sum mine = {0, 0}, total;
+        for (int j = 0; j < kPer; ++j) {
+            mine.mass += S.mass[kPer * t + j];
+            mine.count += S.count[kPer * t + j];
+        }
+        Sum run = block_before<kThreads>(S.scan, turn, mine, &total);
         run.mass += before.mass;
         run.count += before.count;
-        for (int j = 0; j < 2; ++j) {
-            const Sum next = {run.mass + two[j].mass, run.count + two[j].count};
-            if (reaches(run, next, mass, need)) S.hit = {run, next, 2 * t + j};
+        for (int j = 0; j < kPer; ++j) {
+            const Sum next = {run.mass + S.mass[kPer * t + j], run.count + S.count[kPer * t + j]};
+            if (reaches(run, next, mass, need)) S.hit = {run, next, kPer * t + j};
             run = next;
         }
         __syncthreads();
@@ -444,7 +457,7 @@ template <bool CAP>
 __device__ __noinline__ void draw_by_digits(Digits& S, const DrawView& D, const Row<CAP>& R, int32_t* token, int32_t* n) {
     Sum mine = {0, 0}, above = {0, 0}, total, kept;
     int turn = 0;
-    for_logits(load_batch(R.y, 0, D.a.V, D.vec), R.y, 0, D.a.V, D.vec, [&](float v, int64_t) {
+    for_logits<kThreads>(load_batch<kThreads>(R.y, 0, D.a.V, D.vec), R.y, 0, D.a.V, D.vec, [&](float v, int64_t) {
         if (!weighs(v)) return;
         const double e = R.exponent(v);
         const uint64_t w = R.mass_of(e);
@@ -456,8 +469,8 @@ __device__ __noinline__ void draw_by_digits(Digits& S, const DrawView& D, const 
         }
     });
     __syncthreads();
-    block_before(S.scan, turn, above, &kept);
-    block_before(S.scan, turn, mine, &total);
+    block_before<kThreads>(S.scan, turn, above, &kept);
+    block_before<kThreads>(S.scan, turn, mine, &total);
     if (!R.has_min) kept = total;
     if (kept.count == 0) kept = {static_cast<uint64_t>(R.unit), 1};
     Sum of_k = total;
@@ -485,10 +498,12 @@ __device__ __forceinline__ void by_digits(Digits& S, const DrawView& D, const Ro
 
 // ------------------------------------------------------------ by bins
 
-// The bins of a row with their running sums: thread t holds bins 4 t .. 4 t + 3.
+// The bins of a row with their running sums: a thread holds kPer neighbours.
+template <int T>
 struct Bins {
-    Sum bin[kBinsPer];
-    Sum before, total;
+    static constexpr int kPer = kBins / T;
+    Sum bin[kPer];
+    Sum own, before, total;
 };
 
 struct Ask {
@@ -497,40 +512,46 @@ struct Ask {
 };
 
 // The bins as they lie in memory.
-__device__ __forceinline__ Bins load_bins(const uint32_t* count, const uint64_t* mass) {
-    Bins B;
+template <int T>
+__device__ __forceinline__ Bins<T> load_bins(const uint32_t* count, const uint64_t* mass) {
+    Bins<T> B;
+    constexpr int kPer = Bins<T>::kPer;
 #pragma unroll
-    for (int j = 0; j < kBinsPer; ++j) {
-        B.bin[j].count = count[kBinsPer * threadIdx.x + j];
-        B.bin[j].mass = mass[kBinsPer * threadIdx.x + j];
+    for (int j = 0; j < Bins<T>::kPer; ++j) {
+        B.bin[j].count = count[kPer * threadIdx.x + j];
+        B.bin[j].mass = mass[kPer * threadIdx.x + j];
     }
     return B;
 }
 
-__device__ __forceinline__ void sum_bins(Ask& S, int& turn, Bins& B) {
+template <int T>
+__device__ __forceinline__ void sum_bins(Ask& S, int& turn, Bins<T>& B) {
     Sum mine = {0, 0};
 #pragma unroll
-    for (int j = 0; j < kBinsPer; ++j) {
+    for (int j = 0; j < Bins<T>::kPer; ++j) {
         mine.mass += B.bin[j].mass;
         mine.count += B.bin[j].count;
     }
-    B.before = block_before(S.scan, turn, mine, &B.total);
+    B.own = mine;
+    B.before = block_before<T>(S.scan, turn, mine, &B.total);
 }
 
 // The thread whose bin reaches `need` says so in hit[slot].
-__device__ __forceinline__ void ask_bins(Ask& S, const Bins& B, int slot, bool mass, uint64_t need) {
+template <int T>
+__device__ __forceinline__ void ask_bins(Ask& S, const Bins<T>& B, int slot, bool mass, uint64_t need) {
     Sum run = B.before;
+    if (!reaches(run, {run.mass + B.own.mass, run.count + B.own.count}, mass, need)) return;
 #pragma unroll
-    for (int j = 0; j < kBinsPer; ++j) {
+    for (int j = 0; j < Bins<T>::kPer; ++j) {
         const Sum next = {run.mass + B.bin[j].mass, run.count + B.bin[j].count};
-        if (reaches(run, next, mass, need)) S.hit[slot] = {run, next, kBinsPer * static_cast<int>(threadIdx.x) + j};
+        if (reaches(run, next, mass, need)) S.hit[slot] = {run, next, Bins<T>::kPer * static_cast<int>(threadIdx.x) + j};
         run = next;
     }
 }
 
 // Bins that hold the answers, in every thread.
-template <bool CAP>
-__device__ __forceinline__ Head choose_bins(Ask& S, const Row<CAP>& R, const Bins& B, Sum above) {
+template <bool CAP, int T>
+__device__ __forceinline__ Head choose_bins(Ask& S, const Row<CAP>& R, const Bins<T>& B, Sum above) {
     Head H = {above.mass, above.count, 0, -1, 0, -1, 0, -1};
     const uint32_t kk = R.top_k > 0 && static_cast<uint32_t>(R.top_k) < B.total.count ? R.top_k : B.total.count;
     if (R.mode != kSummed) {  // the first kk whole (of runs: fewer than k may be there, then all)
@@ -642,7 +663,7 @@ __device__ __forceinline__ void sort_cands(Sorter& S, int& turn, const Row<CAP>&
             in[j] = S.start[kCandsPer * t + j];
             own.count += in[j];
         }
-        uint32_t before = block_before(S.ask.scan, turn, own, &total).count;
+        uint32_t before = block_before<kThreads>(S.ask.scan, turn, own, &total).count;
 #pragma unroll
         for (int j = 0; j < kCandsPer; ++j) {
             S.start[kCandsPer * t + j] = before;
@@ -670,7 +691,7 @@ __device__ __forceinline__ void sort_cands(Sorter& S, int& turn, const Row<CAP>&
 // The answers among the n collected elements of a row (sort_cands says how a
 // thread holds them).
 template <bool CAP>
-__device__ __forceinline__ void draw_from_cands(Sorter& S, int& turn, const Row<CAP>& R, const Bins& B, const Head& H,
+__device__ __forceinline__ void draw_from_cands(Sorter& S, int& turn, const Row<CAP>& R, const Bins<kThreads>& B, const Head& H,
                                                 uint32_t n_cands, uint64_t (&key)[kCandsPer], int32_t* token, int32_t* n) {
     const int t = threadIdx.x;
     const bool whole = R.mode != kSummed;  // the first k are here
@@ -692,7 +713,7 @@ __device__ __forceinline__ void draw_from_cands(Sorter& S, int& turn, const Row<
             own.count += w[j].count;
         }
         if (R.has_min && above) atomicAdd(&S.above, above);
-        const Sum before = block_before(S.ask.scan, turn, own, &of_k);
+        const Sum before = block_before<kThreads>(S.ask.scan, turn, own, &of_k);
         auto ask = [&](int slot, bool mass, uint64_t need) {
             Sum run = before;
 #pragma unroll
@@ -714,9 +735,13 @@ __device__ __forceinline__ void draw_from_cands(Sorter& S, int& turn, const Row<
     int bin[kCandsPer];
 #pragma unroll
     for (int j = 0; j < kCandsPer; ++j) {
-        const float v = logit_of(static_cast<uint32_t>(key[j] >> 32));
-        bin[j] = key[j] ? R.bin_of(v) : -1;
-        w[j] = {key[j] ? R.mass_of(R.exponent(v)) : 0, key[j] ? 1u : 0u};
+        bin[j] = -1;
+        w[j] = {0, 0};
+        if (key[j]) {
+            const float v = logit_of(static_cast<uint32_t>(key[j] >> 32));
+            bin[j] = R.bin_of(v);
+            w[j] = {R.mass_of(R.exponent(v)), 1u};
+        }
     }
     // the element that reaches `need`, in the bin that does
     auto ask = [&](int slot, bool mass, uint64_t need) -> Hit {
@@ -730,7 +755,7 @@ __device__ __forceinline__ void draw_from_cands(Sorter& S, int& turn, const Row<
             own.mass += in[j].mass;
             own.count += in[j].count;
         }
-        Sum run = block_before(S.ask.scan, turn, own, &total);
+        Sum run = block_before<kThreads>(S.ask.scan, turn, own, &total);
         run.mass += of.before.mass;
         run.count += of.before.count;
 #pragma unroll
@@ -785,12 +810,12 @@ __device__ __forceinline__ float max16(float v) {  // over 16 lanes, in the last
 // The first element of [lo, hi), and the largest logits of its runs to `run`
 // (null: not wanted).  A run is what 16 lanes hold of a batch.  One logit in
 // four is enough for their mean.
-template <bool WIDE>
+template <int T, bool WIDE>
 __device__ __forceinline__ Part first_of(const float* y, int64_t lo, int64_t hi, bool vec, Part* lds, float* run) {
     float best = kNegInf, sum = 0.0f;
     int32_t at_best = 0;
     uint32_t count = 0;
-    for_quads<WIDE>(load_batch<WIDE>(y, lo, hi, vec), y, lo, hi, vec, [&](const float (&v)[4], int64_t at) {
+    for_quads<T, WIDE>(load_batch<T, WIDE>(y, lo, hi, vec), y, lo, hi, vec, [&](const float (&v)[4], int64_t at) {
         // NaN is dropped; a NaN that is left is not larger than anything
         float top = fminf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), kMaxLogit);
         top = v[0] != v[0] && v[1] != v[1] && v[2] != v[2] && v[3] != v[3] ? kNegInf : top;
@@ -815,19 +840,19 @@ __device__ __forceinline__ Part first_of(const float* y, int64_t lo, int64_t hi,
     const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
     if (lane == 0) lds[wave] = p;
     __syncthreads();
-    p = lane < kWaves ? lds[lane] : Part{0, 0.0f, 0};
+    p = lane < T / kWave ? lds[lane] : Part{0, 0.0f, 0};
     return join(p);
 }
 
 // Counts (and sums) of the logits of [lo, hi) into bins in LDS, zero before;
 // sparse: kSparse floats a wave, of its own.
 // Returns this thread's share of those that pass min_p.
-template <bool CAP>
+template <int T, bool CAP>
 __device__ __forceinline__ Sum fill_bins(const Batch& first, const DrawView& D, const Row<CAP>& R, int64_t lo, int64_t hi,
                                          uint32_t* count, uint64_t* mass, float* sparse) {
     Sum above = {0, 0};
     if (R.mode == kCounted) {
-        for_logits(first, R.y, lo, hi, D.vec, [&](float v, int64_t) {
+        for_logits<T>(first, R.y, lo, hi, D.vec, [&](float v, int64_t) {
             if (weighs(v)) atomicAdd(&count[R.bin_of(v)], 1u);
         });
         return above;
@@ -846,9 +871,9 @@ __device__ __forceinline__ Sum fill_bins(const Batch& first, const DrawView& D, 
     const int lane = threadIdx.x & (kWave - 1);
     float* mine = sparse + (threadIdx.x / kWave) * kSparse;
     Batch B = first;
-    for (int64_t from = lo; from < hi; from += kStep) {
+    for (int64_t from = lo; from < hi; from += kStep<T>) {
         Batch next;
-        if (from + kStep < hi) next = load_batch(R.y, from + kStep, hi, D.vec);
+        if (from + kStep<T> < hi) next = load_batch<T>(R.y, from + kStep<T>, hi, D.vec);
         uint32_t n = 0;
 #pragma unroll
         for (int j = 0; j < kU; ++j)
@@ -883,12 +908,12 @@ __device__ __forceinline__ Sum fill_bins(const Batch& first, const DrawView& D, 
 
 // Keys of the logits of [lo, hi) in chosen bins, to LDS; *n counts them, also
 // those for which there is no room.
-template <bool CAP>
+template <int T, bool CAP>
 __device__ __forceinline__ void collect(const Batch& first, const DrawView& D, const Row<CAP>& R, const Head& H, int64_t lo,
                                         int64_t hi, uint64_t* keys, uint32_t* n) {
     // four at a time are dropped, most of them (NaN is not above anything)
     const float least = R.floor_of(max(H.u_hi, max(H.p_hi, H.k_bin)));
-    for_quads<false>(first, R.y, lo, hi, D.vec, [&](const float (&v)[4], int64_t i) {
+    for_quads<T, false>(first, R.y, lo, hi, D.vec, [&](const float (&v)[4], int64_t i) {
         if (!(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) >= least)) return;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -908,21 +933,21 @@ void draw_row_kernel(DrawView D) {
         struct {
             uint64_t mass[kBins];
             uint32_t count[kBins];
-            float sparse[kWaves * kSparse];
+            float sparse[kMostWaves * kSparse];
         } bins;
         Sorter sorter;
         Digits digits;
     };
     __shared__ Lds S;
     __shared__ Ask ask;
-    __shared__ Part parts[kWaves];
+    __shared__ Part parts[kMostWaves];
     __shared__ uint32_t collected;
     const int64_t m = blockIdx.x, V = D.a.V;
     const int t = threadIdx.x;
     const Args A = args_of(D, m);
     fill_exp_table();
     const float* y = D.a.logits + m * D.a.ldl;
-    const Part p = first_of<true>(y, 0, V, D.vec, parts, nullptr);
+    const Part p = first_of<kThreads, true>(y, 0, V, D.vec, parts, nullptr);
     Row<CAP> R = row_of<CAP>(D, m, A, p.best, p.sum, p.count);
     int32_t token = p.best ? index_of(p.best) : -1, n = p.best ? 1 : 0;
     if (R.mode != kFirst) {
@@ -933,15 +958,15 @@ void draw_row_kernel(DrawView D) {
             S.bins.mass[i] = 0;
         }
         if (t == 0) collected = 0;
-        const Batch again = load_batch(y, 0, V, D.vec);
+        const Batch again = load_batch<kThreads>(y, 0, V, D.vec);
         __syncthreads();
-        const Sum mine = fill_bins(again, D, R, 0, V, S.bins.count, S.bins.mass, S.bins.sparse);
+        const Sum mine = fill_bins<kThreads>(again, D, R, 0, V, S.bins.count, S.bins.mass, S.bins.sparse);
         Sum above;
-        block_before(ask.scan, turn, mine, &above);  // and a barrier behind the atomics
-        Bins B = load_bins(S.bins.count, S.bins.mass);
+        block_before<kThreads>(ask.scan, turn, mine, &above);  // and a barrier behind the atomics
+        Bins<kThreads> B = load_bins<kThreads>(S.bins.count, S.bins.mass);
         sum_bins(ask, turn, B);  // and one behind the loads
         const Head H = choose_bins(ask, R, B, above);
-        collect(load_batch(y, 0, V, D.vec), D, R, H, 0, V, S.sorter.key, &collected);
+        collect<kThreads>(load_batch<kThreads>(y, 0, V, D.vec), D, R, H, 0, V, S.sorter.key, &collected);
         __syncthreads();
         const uint32_t found = collected;
         if (found > kMostCands) {
@@ -962,7 +987,7 @@ void draw_row_kernel(DrawView D) {
 template <bool WIDE>
 __global__ __launch_bounds__(kThreads)
 void draw_first_kernel(DrawView D) {
-    __shared__ Part parts[kWaves];
+    __shared__ Part parts[kMostWaves];
     const int64_t m = blockIdx.y, lo = blockIdx.x * D.part_len;
     const int t = threadIdx.x;
     const Args A = args_of(D, m);
@@ -971,7 +996,7 @@ void draw_first_kernel(DrawView D) {
         D.count[m * kBins + i] = 0;
         D.mass[m * kBins + i] = 0;
     }
-    const Part p = first_of<WIDE>(D.a.logits + m * D.a.ldl, lo, min(lo + D.part_len, D.a.V), D.vec, parts,
+    const Part p = first_of<kThreads, WIDE>(D.a.logits + m * D.a.ldl, lo, min(lo + D.part_len, D.a.V), D.vec, parts,
                             by_runs(D, A) ? D.run + m * D.runs : nullptr);
     if (t == 0) {
         D.part[m * D.parts + blockIdx.x] = p;
@@ -1062,11 +1087,11 @@ __device__ __forceinline__ Unit unit_of(Shares& S, const DrawView& D, int run_pa
 // Bins of a part of a row.  Rows by runs: one workgroup counts their runs, and
 // says which bins to collect.
 template <bool CAP>
-__global__ __launch_bounds__(kThreads)
+__global__ __launch_bounds__(kBinThreads)
 void draw_bins_kernel(DrawView D) {
     __shared__ uint64_t mass[kBins];
     __shared__ uint32_t count[kBins];
-    __shared__ float sparse[kWaves * kSparse];
+    __shared__ float sparse[kBinThreads / kWave * kSparse];
     __shared__ Ask ask;
     __shared__ Shares shares;
     const int t = threadIdx.x;
@@ -1074,12 +1099,12 @@ void draw_bins_kernel(DrawView D) {
     if (!U.some) return;
     const int64_t m = U.m;
     Batch first;
-    if (!U.runs) first = load_batch(D.a.logits + m * D.a.ldl, U.lo, U.hi, D.vec);
+    if (!U.runs) first = load_batch<kBinThreads>(D.a.logits + m * D.a.ldl, U.lo, U.hi, D.vec);
     Part p = part_of(D, m);
     const Args A = args_of(D, m);
     if (!(A.temperature > 0.0f) || (U.runs && U.lo > 0)) return;
     fill_exp_table();
-    for (int i = t; i < kBins; i += kThreads) {
+    for (int i = t; i < kBins; i += kBinThreads) {
         count[i] = 0;
         mass[i] = 0;
     }
@@ -1090,34 +1115,34 @@ void draw_bins_kernel(DrawView D) {
     int turn = 0;
     if (R.mode == kByRuns) {
         const float* run = D.run + m * D.runs;
-        for (int64_t i = t; i < D.runs; i += 4 * kThreads) {
-            float v[4];
+        for (int64_t i = t; i < D.runs; i += 8 * kBinThreads) {
+            float v[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = i + j * kThreads < D.runs ? run[i + j * kThreads] : kNegInf;
+            for (int j = 0; j < 8; ++j) v[j] = i + j * kBinThreads < D.runs ? run[i + j * kBinThreads] : kNegInf;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 8; ++j)
                 if (weighs(v[j])) atomicAdd(&count[R.bin_of(v[j])], 1u);
         }
         __syncthreads();
-        Bins B = load_bins(count, mass);
+        Bins<kBinThreads> B = load_bins<kBinThreads>(count, mass);
         sum_bins(ask, turn, B);
         const Head H = choose_bins(ask, R, B, {0, 0});
         if (t == 0) D.head[m].u_hi = H.u_hi;
         return;
     }
     R.level_of_top();
-    const Sum mine = fill_bins(first, D, R, U.lo, U.hi, count, mass, sparse);
+    const Sum mine = fill_bins<kBinThreads>(first, D, R, U.lo, U.hi, count, mass, sparse);
     __syncthreads();
     if (R.has_min && R.mode == kSummed) {
         Sum above;
-        block_before(ask.scan, turn, mine, &above);
+        block_before<kBinThreads>(ask.scan, turn, mine, &above);
         if (t == 0 && above.count) {
             atomicAdd(&D.head[m].above_count, above.count);
             atomicAdd(reinterpret_cast<unsigned long long*>(&D.head[m].above_mass),
                       static_cast<unsigned long long>(above.mass));
         }
     }
-    for (int i = t; i < kBins; i += kThreads) {
+    for (int i = t; i < kBins; i += kBinThreads) {
         if (count[i] == 0) continue;
         atomicAdd(&D.count[m * kBins + i], count[i]);
         if (mass[i])
@@ -1127,22 +1152,22 @@ void draw_bins_kernel(DrawView D) {
 }
 
 template <bool CAP>
-__global__ __launch_bounds__(kThreads)
+__global__ __launch_bounds__(kBinThreads)
 void draw_collect_kernel(DrawView D) {
     __shared__ uint64_t keys[kMostCands];
     __shared__ Ask ask;
     __shared__ uint32_t n, base, listed;
-    __shared__ int32_t list[kThreads];
+    __shared__ int32_t list[4 * kBinThreads];
     __shared__ Shares shares;
     const int t = threadIdx.x;
     const Unit U = unit_of(shares, D, D.run_parts);
     if (!U.some) return;
     const int64_t m = U.m, lo = U.lo, hi = U.hi;
-    Bins B = {};
+    Bins<kBinThreads> B = {};
     Batch first;
     if (!U.runs) {
-        B = load_bins(D.count + m * kBins, D.mass + m * kBins);
-        first = load_batch(D.a.logits + m * D.a.ldl, lo, hi, D.vec);
+        B = load_bins<kBinThreads>(D.count + m * kBins, D.mass + m * kBins);
+        first = load_batch<kBinThreads>(D.a.logits + m * D.a.ldl, lo, hi, D.vec);
     }
     Head* head = D.head + m;
     Head H = *head;
@@ -1158,17 +1183,22 @@ void draw_collect_kernel(DrawView D) {
         // only runs that reach the bins are read, by 16 threads each
         const float* run = D.run + m * D.runs;
         const int64_t r0 = lo / kRun, r1 = (hi + kRun - 1) / kRun;
-        for (int64_t r = r0; r < r1; r += kThreads) {
-            const float top = r + t < r1 ? run[r + t] : kNegInf;
-            if (weighs(top) && R.bin_of(top) <= H.u_hi) list[atomicAdd(&listed, 1u)] = static_cast<int32_t>(r + t - r0);
+        for (int64_t r = r0; r < r1; r += 4 * kBinThreads) {
+            float top[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top[j] = r + j * kBinThreads + t < r1 ? run[r + j * kBinThreads + t] : kNegInf;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (weighs(top[j]) && R.bin_of(top[j]) <= H.u_hi)
+                    list[atomicAdd(&listed, 1u)] = static_cast<int32_t>(r + j * kBinThreads + t - r0);
             __syncthreads();
             const uint32_t have = listed;
-            for (uint32_t i = t / 16; i < have; i += 4 * (kThreads / 16)) {  // four at a time
+            for (uint32_t i = t / 16; i < have; i += 4 * (kBinThreads / 16)) {  // four at a time
                 float v[4][4];
                 int64_t at[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t k = i + j * (kThreads / 16);
+                    const uint32_t k = i + j * (kBinThreads / 16);
                     at[j] = k < have ? (r0 + list[k]) * kRun + (t & 15) * 4 : hi;
                     if (D.vec && at[j] + 4 <= hi) {
                         const float4 x = *reinterpret_cast<const float4*>(R.y + at[j]);
@@ -1202,14 +1232,14 @@ void draw_collect_kernel(DrawView D) {
             head->u_lo = H.u_lo;
             head->u_hi = H.u_hi;
         }
-        collect(first, D, R, H, lo, hi, keys, &n);
+        collect<kBinThreads>(first, D, R, H, lo, hi, keys, &n);
     }
     __syncthreads();
     const uint32_t found = n;
     if (found == 0) return;
     if (t == 0) base = atomicAdd(&head->collected, found);
     __syncthreads();
-    for (uint32_t i = t; i < found && i < kMostCands; i += kThreads)
+    for (uint32_t i = t; i < found && i < kMostCands; i += kBinThreads)
         if (base + i < kMostCands) D.cand[m * kMostCands + base + i] = keys[i];
 }
 
@@ -1229,8 +1259,8 @@ void draw_token_kernel(DrawView D) {
     const uint64_t* cand = D.cand + m * kMostCands;
     key[0] = cand[threadIdx.x];
     fill_exp_table();
-    Bins B = {};
-    if (A.temperature > 0.0f && !by_runs(D, A)) B = load_bins(D.count + m * kBins, D.mass + m * kBins);
+    Bins<kThreads> B = {};
+    if (A.temperature > 0.0f && !by_runs(D, A)) B = load_bins<kThreads>(D.count + m * kBins, D.mass + m * kBins);
 #pragma unroll
     for (int j = 1; j < kCandsPer; ++j) {
         key[j] = 0;
@@ -1262,17 +1292,18 @@ hipError_t launch(const DrawView& D, hipStream_t stream) {
         return hipGetLastError();
     }
     const dim3 grid(static_cast<unsigned>(D.parts), static_cast<unsigned>(D.a.M));
-    if (D.part_len >= kStep)
+    if (D.part_len >= kStep<kThreads>)
         hipLaunchKernelGGL(draw_first_kernel<true>, grid, block, 0, stream, D);
     else
         hipLaunchKernelGGL(draw_first_kernel<false>, grid, block, 0, stream, D);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const dim3 shares(static_cast<unsigned>(D.parts * D.a.M));
-    hipLaunchKernelGGL(draw_bins_kernel<CAP>, shares, block, 0, stream, D);
+    const dim3 bin_block(kBinThreads);
+    hipLaunchKernelGGL(draw_bins_kernel<CAP>, shares, bin_block, 0, stream, D);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(draw_collect_kernel<CAP>, shares, block, 0, stream, D);
+    hipLaunchKernelGGL(draw_collect_kernel<CAP>, shares, bin_block, 0, stream, D);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(draw_token_kernel<CAP>, rows, block, 0, stream, D);
