@@ -56,7 +56,7 @@ constexpr int kRun = 64;            // logits whose largest is kept
 constexpr int kDigitBins = 2048;
 constexpr int kMaxParts = kWave;  // a lane a part when they are joined
 constexpr int kWorkgroups = 512;   // of a call, about
-constexpr int kMostSplit = kWorkgroups / 2;  // rows that are split have two parts at least
+constexpr int kMostSplit = 512;    // rows that are split, each in two parts at least
 constexpr float kMaxLogit = 3.4028234663852886e38f;
 
 struct Sum {
@@ -175,7 +175,8 @@ struct Row {
                                                           (static_cast<uint32_t>(b + 1 - static_cast<int>(kEqualBins)) << 16));
         const float t = x / per_bin * 1.00001f;
         const float v = top - t - (fabsf(top) + t) * 1e-6f;
-        return b < kBins - 1 ? v : -kMaxLogit;
+        // -infinity, where the bins are infinitely wide, would let masked logits in
+        return b < kBins - 1 ? fmaxf(v, -kMaxLogit) : -kMaxLogit;
     }
     // Sums that the answers have to reach.
     __device__ __forceinline__ uint64_t need_p(uint64_t mass) const {
@@ -1310,12 +1311,18 @@ hipError_t launch(const DrawView& D, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Workgroups of a row: about 512 in all (two a CU), 4096 logits each at least.
+// Workgroups of a row: one, in one launch, for short rows, and for longer ones
+// where there are many; else about 512 in all (two a CU), of 4096 logits each at
+// least, in four launches.  Top-k 50 / top-p 0.9, one launch against four, us:
+//   1 x 16384     17 / 25   23 / 29       256 x 32000   29 / 45   35 / 69
+//   1 x 32000     22 / 37   24 / 30       300 x 65536   75 / 131  55 / 131
+//   64 x 32000    23 / 38   31 / 54       512 x 131072  150 / 255  92 / 296
 constexpr int64_t kPartLeast = 4096;
 int parts_of(int64_t V, int64_t M) {
-    const int64_t most = (V + kPartLeast - 1) / kPartLeast, want = kWorkgroups / M;
+    if (V <= 16384 || (V <= 40960 && M >= 16) || M > kMostSplit) return 1;
+    const int64_t most = (V + kPartLeast - 1) / kPartLeast, want = M > kWorkgroups / 2 ? 2 : kWorkgroups / M;
     const int64_t parts = want < most ? want : most;
-    return static_cast<int>(parts < 1 ? 1 : (parts > kMaxParts ? kMaxParts : parts));
+    return static_cast<int>(parts > kMaxParts ? kMaxParts : parts);
 }
 
 int64_t runs_of(int64_t V) { return (V + kRun - 1) / kRun; }
