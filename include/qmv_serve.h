@@ -63,7 +63,7 @@ typedef struct qmv_kv_pool {
  *     the stack into its table (a sequence does one or the other).
  * A page is moved as the number that it is: a table that holds -1 gives back
  * -1.  Outputs:
- *   new_len   [B] int32 (may be kv_len)
+ *   new_len   [B] int32 (may be kv_len or keep)
  *   new_count [1] int32 (may be free_count): free pages after the step
  *   row_start [B + 1] int32: the running sum of n_new
  *   position  [T] int32 (or NULL): row row_start[b] + i has keep[b] + i
