@@ -14,7 +14,7 @@
 // products).  A single row would waste 15 of 16 columns: it has the same loads
 // and ordinary multiplications (32 rows of rank 64: 12.4 -> 8.5 us for shrink).
 //
-// Bounds, and what was measured: chunks are bound by HBM (1540 rows, 5376 ->
+// Bounds, and what was measured: chunks are bound by HBM (1611 rows, 5376 ->
 // 21504, rank 16: 308 MB in 67 us, 4.6 TB/s); single rows with many adapters by
 // the lines of Bm (a row of Bm of max_rank 64 is a 128-byte line, read whole
 // whatever the adapter's own rank: 32 rows over 24 adapters 24 us, 4.9 TB/s
@@ -138,7 +138,7 @@ __device__ __forceinline__ void shrink_wave(const LoraView& D, const float* x, c
                                             int64_t hi, f32x4 (&acc)[NT]) {
     // steps of 32 k that are loaded at once: their latency is the time of this
     // kernel, and 128 k are a wave's share where there are many.  Of several rows
-    // and many ranks fewer at once, for a wave more a SIMD (1460 rows, rank up to
+    // and many ranks fewer at once, for a wave more a SIMD (1620 rows, rank up to
     // 128: 20.8 -> 18.6 us).
     constexpr int kSteps = NT <= 2 ? 4 : (NT <= 4 ? (ONE ? 4 : 2) : (NT <= 8 ? (ONE ? 2 : 1) : 1));
     const int lane = threadIdx.x & (kWave - 1), i = lane & 15, g = lane >> 4;
@@ -505,8 +505,8 @@ void split_k(const qmv_lora& l, int64_t B, int64_t T, int* shares, int64_t* per_
 
 // Outputs of a workgroup of the expand kernel, a multiple of 256: some 4096
 // workgroups for ranks up to 32, where HBM is the limit and an even end counts
-// (1540 rows of 21504, rank 16: 67 us, with 1024 of them 76), some 1024 above,
-// where the start of one, v and its own registers cost more (1460 rows of 5376,
+// (1611 rows of 21504, rank 16: 67 us, with 1024 of them 76), some 1024 above,
+// where the start of one, v and its own registers cost more (1620 rows of 5376,
 // rank up to 128: 49 us, with 4096 of them 53).
 int64_t share_n(const qmv_lora& l, int64_t B, int64_t T) {
     const int64_t workgroups = l.max_rank <= 32 ? 4096 : 1024;
