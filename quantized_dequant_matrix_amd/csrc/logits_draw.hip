@@ -57,6 +57,7 @@ constexpr int kBinThreads = 512;
 constexpr int kMostWaves = kThreads / kWave;
 constexpr int kBins = 4096;
 constexpr float kEqualBins = 3072.0f;
+constexpr float kFar = 786431.0f;    // 8 octaves on, at the end of the last bin
 constexpr int kMostCands = 4096, kCandsPer = kMostCands / kThreads;
 constexpr int kMostCounted = 2048;  // largest top-k that is collected whole
 constexpr int kSparse = 256;        // logits of a wave's 1024 that are brought together
@@ -163,16 +164,16 @@ struct Row {
         return __builtin_bit_cast(uint64_t, r) & 0xFFFFFFFFFFFFFull;
     }
     // Bins follow the order: 3072 equal steps of the distance from the largest
-    // logit, then 128 an octave.  *part: where in the bin, of 4096 parts.
+    // logit, then 128 an octave, up to kFar.  *part: where in the bin, of 4096
+    // parts.
     __device__ __forceinline__ int bin_of(float v, int* part = nullptr) const {
-        const float x = fminf(fminf(top - fminf(v, kMaxLogit), kMaxLogit) * per_bin, 1e6f);
+        const float x = fminf(fminf(top - fminf(v, kMaxLogit), kMaxLogit) * per_bin, kFar);
         const uint32_t past = __float_as_uint(x) - __float_as_uint(kEqualBins);
-        const int b = static_cast<int>(past >> 16) + static_cast<int>(kEqualBins);
         const int e = static_cast<int>(x);
         const bool equal = x < kEqualBins;
         // 12 bits of a float below 3072 lie behind its point
         if (part) *part = equal ? static_cast<int>((x - static_cast<float>(e)) * 4096.0f) : static_cast<int>((past & 0xffffu) >> 4);
-        return equal ? e : (b < kBins ? b : kBins - 1);
+        return equal ? e : static_cast<int>(past >> 16) + static_cast<int>(kEqualBins);
     }
     // A logit below this one lies behind bin `b`: what that bin can reach, and
     // more than the roundings of bin_of below it.

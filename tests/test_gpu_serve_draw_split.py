@@ -75,6 +75,24 @@ def test_bins_without_width():
         assert len(ok) == V - -(-V // 3)
 
 
+@pytest.mark.parametrize("V", [3000, 45000])
+def test_far_logits_keep_their_order(V):
+    """Logits hundreds of times the mean distance away, which weigh as much as any at such a temperature."""
+    say(f"logits_draw far logits V={V}")
+    rng = np.random.default_rng(3)
+    z = rng.normal(0, 0.1, (6, V)).astype(np.float32)
+    far = rng.permutation(V)[:900]
+    z[:, far] = -(10.0 ** rng.uniform(1, 5.9, (6, 900)))
+    for k in (0, V - 450, V - 100, 2000, 2048):
+        check(z, 1e20, k, 1.0, u=rng.random(6), least=0)
+        for u in (0.97, 0.99, 0.999):
+            token, kept, _ = run(z, INF, k, 1.0, u=u)
+            for m in range(6):
+                n = k or V
+                order = np.lexsort((np.arange(V), -z[m]))
+                assert kept[m] == n and token[m] == order[int(np.float64(np.float32(u)) * n)], (k, u, m)
+
+
 def test_ties():
     say("logits_draw split, ties")
     rng = np.random.default_rng(2)
