@@ -32,7 +32,7 @@
 // and barriers (4.5, 8.7, 6.8, 9.4); 32 rows with mixed filters 43-49 us, 128 of
 // which 97% is masked 81: the first launch reads them at 4.0 TB/s (33 us), and
 // rows that need sums are read twice more, from the last-level cache.  Short rows
-// are one launch, a workgroup each (256 rows of 32,000: 32 us).
+// are one launch, a workgroup each (256 rows of 32,000, top-k: 25 us).
 #include <stdint.h>
 
 #include <type_traits>
@@ -62,6 +62,7 @@ constexpr int kMostCands = 4096, kCandsPer = kMostCands / kThreads;
 constexpr int kMostCounted = 2048;  // largest top-k that is collected whole
 constexpr int kSparse = 256;        // logits of a wave's 1024 that are brought together
 constexpr int kRun = 64;            // logits whose largest is kept
+constexpr int kMostRuns = 4096;     // of a row by one workgroup
 constexpr int kDigitBins = 2048;
 constexpr int kMaxParts = kWave;  // a lane a part when they are joined
 constexpr int kWorkgroups = 512;   // of a call, about
@@ -983,51 +984,156 @@ __device__ __forceinline__ void collect(const Batch& first, const DrawView& D, c
     });
 }
 
+// Counts of the runs' largest logits in bins in LDS, zero before.
+template <int T, bool CAP>
+__device__ __forceinline__ void count_runs(const Row<CAP>& R, const float* run, int64_t runs, uint32_t* count) {
+    const int t = threadIdx.x;
+    for (int64_t i = t; i < runs; i += 8 * T) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = i + j * T < runs ? run[i + j * T] : kNegInf;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bool same = weighs(v[j]) && __float_as_uint(v[j]) == __builtin_amdgcn_readfirstlane(__float_as_uint(v[j]));
+            if (__ballot(same) == ~uint64_t{0}) {
+                if ((t & (kWave - 1)) == 0) atomicAdd(&count[R.bin_of(v[j])], static_cast<uint32_t>(kWave));
+            } else if (weighs(v[j])) {
+                atomicAdd(&count[R.bin_of(v[j])], 1u);
+            }
+        }
+    }
+}
+
+// Keys of the logits of [lo, hi) in bins up to u_hi, as collect() has them: only
+// runs that reach the bins are read, by 16 threads each.  list: 4 T numbers in
+// LDS; *listed and *n are 0 before, behind a barrier.
+template <int T, bool CAP>
+__device__ __forceinline__ void collect_runs(const DrawView& D, const Row<CAP>& R, int u_hi, const float* run, int64_t lo,
+                                             int64_t hi, int32_t* list, uint32_t* listed, uint64_t* keys, uint32_t* n) {
+    const int t = threadIdx.x;
+    const int64_t r0 = lo / kRun, r1 = (hi + kRun - 1) / kRun;
+    for (int64_t r = r0; r < r1; r += 4 * T) {
+        float top[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top[j] = r + j * T + t < r1 ? run[r + j * T + t] : kNegInf;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (weighs(top[j]) && R.bin_of(top[j]) <= u_hi)
+                list[atomicAdd(listed, 1u)] = static_cast<int32_t>(r + j * T + t - r0);
+        __syncthreads();
+        const uint32_t have = *listed;
+        for (uint32_t i = t / 16; i < have; i += 4 * (T / 16)) {  // four at a time
+            float v[4][4];
+            int64_t at[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t k = i + j * (T / 16);
+                at[j] = k < have ? (r0 + list[k]) * kRun + (t & 15) * 4 : hi;
+                if (D.vec && at[j] + 4 <= hi) {
+                    const float4 x = *reinterpret_cast<const float4*>(R.y + at[j]);
+                    v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[j][e] = at[j] + e < hi ? R.y[at[j] + e] : kNegInf;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (!weighs(v[j][e]) || R.bin_of(v[j][e]) > u_hi) continue;
+                    const uint32_t to = atomicAdd(n, 1u);
+                    if (to < kMostCands) keys[to] = key_of(v[j][e], at[j] + e);
+                }
+        }
+        __syncthreads();
+        if (t == 0) *listed = 0;
+        __syncthreads();
+    }
+}
+
 // ------------------------------------------------------------ a row by one workgroup
+
+struct BinLds {
+    uint64_t mass[kBins];
+    uint32_t count[kBins];
+    float sparse[kMostWaves * kSparse];
+};
+
+union RowLds {
+    BinLds bins;
+    Sorter sorter;
+    Digits digits;
+};
+
+// What of a row holds the answers, by bins of all its elements: keys to
+// S.sorter.key, returns how many.
+template <bool CAP>
+__device__ __forceinline__ uint32_t by_bins(RowLds& S, Ask& ask, uint32_t& collected, int& turn, const DrawView& D,
+                                            const Row<CAP>& R, Bins<kThreads>& B, Head& H) {
+    const int t = threadIdx.x;
+    const int64_t V = D.a.V;
+    for (int i = t; i < kBins; i += kThreads) {
+        S.bins.count[i] = 0;
+        S.bins.mass[i] = 0;
+    }
+    if (t == 0) collected = 0;
+    const Batch again = load_batch<kThreads>(R.y, 0, V, D.vec);
+    __syncthreads();
+    const Sum mine = fill_bins<kThreads>(again, D, R, 0, V, S.bins.count, S.bins.mass, S.bins.sparse);
+    Sum above;
+    block_before<kThreads>(ask.scan, turn, mine, &above);  // and a barrier behind the atomics
+    B = load_bins<kThreads>(S.bins.count, S.bins.mass);
+    sum_bins(ask, turn, B);  // and one behind the loads
+    H = choose_bins(ask, R, B, above);
+    collect<kThreads>(load_batch<kThreads>(R.y, 0, V, D.vec), D, R, H, 0, V, S.sorter.key, &collected);
+    __syncthreads();
+    return collected;
+}
 
 template <bool CAP>
 __global__ __launch_bounds__(kThreads)
 void draw_row_kernel(DrawView D) {
-    union Lds {
-        struct {
-            uint64_t mass[kBins];
-            uint32_t count[kBins];
-            float sparse[kMostWaves * kSparse];
-        } bins;
-        Sorter sorter;
-        Digits digits;
-    };
-    __shared__ Lds S;
+    __shared__ RowLds S;
     __shared__ Ask ask;
     __shared__ Part parts[kMostWaves];
-    __shared__ uint32_t collected;
+    __shared__ float run[kMostRuns];
+    __shared__ uint32_t collected, listed;
     const int64_t m = blockIdx.x, V = D.a.V;
     const int t = threadIdx.x;
     const Args A = args_of(D, m);
     fill_exp_table();
     const float* y = D.a.logits + m * D.a.ldl;
-    const Part p = first_of<kThreads, true>(y, 0, V, D.vec, parts, nullptr);
+    const Part p = first_of<kThreads, true>(y, 0, V, D.vec, parts, by_runs(D, A) ? run : nullptr);
     Row<CAP> R = row_of<CAP>(D, m, A, p.best, p.sum, p.count);
     int32_t token = p.best ? index_of(p.best) : -1, n = p.best ? 1 : 0;
     if (R.mode != kFirst) {
         int turn = 0;
+        uint32_t found = 0;
+        Bins<kThreads> B;
+        Head H;
         R.level_of_top();
-        for (int i = t; i < kBins; i += kThreads) {
-            S.bins.count[i] = 0;
-            S.bins.mass[i] = 0;
+        if (R.mode == kByRuns) {
+            for (int i = t; i < kBins; i += kThreads) {
+                S.bins.count[i] = 0;
+                S.bins.mass[i] = 0;
+            }
+            if (t == 0) collected = listed = 0;
+            __syncthreads();
+            count_runs<kThreads>(R, run, D.runs, S.bins.count);
+            __syncthreads();
+            B = load_bins<kThreads>(S.bins.count, S.bins.mass);
+            sum_bins(ask, turn, B);
+            H = choose_bins(ask, R, B, {0, 0});
+            collect_runs<kThreads>(D, R, H.u_hi, run, 0, V, reinterpret_cast<int32_t*>(S.sorter.sorted), &listed, S.sorter.key,
+                                   &collected);
+            found = collected;
+            if (found > kMostCands) {  // see draw_token_kernel
+                R.mode = kCounted;
+                __syncthreads();  // collected is read before it is written
+            }
         }
-        if (t == 0) collected = 0;
-        const Batch again = load_batch<kThreads>(y, 0, V, D.vec);
-        __syncthreads();
-        const Sum mine = fill_bins<kThreads>(again, D, R, 0, V, S.bins.count, S.bins.mass, S.bins.sparse);
-        Sum above;
-        block_before<kThreads>(ask.scan, turn, mine, &above);  // and a barrier behind the atomics
-        Bins<kThreads> B = load_bins<kThreads>(S.bins.count, S.bins.mass);
-        sum_bins(ask, turn, B);  // and one behind the loads
-        const Head H = choose_bins(ask, R, B, above);
-        collect<kThreads>(load_batch<kThreads>(y, 0, V, D.vec), D, R, H, 0, V, S.sorter.key, &collected);
-        __syncthreads();
-        const uint32_t found = collected;
+        if (R.mode != kByRuns) found = by_bins(S, ask, collected, turn, D, R, B, H);
         if (found > kMostCands) {
             by_digits(S.digits, D, R, &token, &n);
         } else {
@@ -1173,21 +1279,7 @@ void draw_bins_kernel(DrawView D) {
     __syncthreads();
     int turn = 0;
     if (R.mode == kByRuns) {
-        const float* run = D.run + m * D.runs;
-        for (int64_t i = t; i < D.runs; i += 8 * kBinThreads) {
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = i + j * kBinThreads < D.runs ? run[i + j * kBinThreads] : kNegInf;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const bool same = weighs(v[j]) && __float_as_uint(v[j]) == __builtin_amdgcn_readfirstlane(__float_as_uint(v[j]));
-                if (__ballot(same) == ~uint64_t{0}) {
-                    if ((t & (kWave - 1)) == 0) atomicAdd(&count[R.bin_of(v[j])], static_cast<uint32_t>(kWave));
-                } else if (weighs(v[j])) {
-                    atomicAdd(&count[R.bin_of(v[j])], 1u);
-                }
-            }
-        }
+        count_runs<kBinThreads>(R, D.run + m * D.runs, D.runs, count);
         __syncthreads();
         Bins<kBinThreads> B = load_bins<kBinThreads>(count, mass);
         sum_bins(ask, turn, B);
@@ -1245,47 +1337,7 @@ void draw_collect_kernel(DrawView D) {
     if (R.mode == kFirst) return;
     if (R.mode == kByRuns) {
         __syncthreads();
-        // only runs that reach the bins are read, by 16 threads each
-        const float* run = D.run + m * D.runs;
-        const int64_t r0 = lo / kRun, r1 = (hi + kRun - 1) / kRun;
-        for (int64_t r = r0; r < r1; r += 4 * kBinThreads) {
-            float top[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) top[j] = r + j * kBinThreads + t < r1 ? run[r + j * kBinThreads + t] : kNegInf;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (weighs(top[j]) && R.bin_of(top[j]) <= H.u_hi)
-                    list[atomicAdd(&listed, 1u)] = static_cast<int32_t>(r + j * kBinThreads + t - r0);
-            __syncthreads();
-            const uint32_t have = listed;
-            for (uint32_t i = t / 16; i < have; i += 4 * (kBinThreads / 16)) {  // four at a time
-                float v[4][4];
-                int64_t at[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t k = i + j * (kBinThreads / 16);
-                    at[j] = k < have ? (r0 + list[k]) * kRun + (t & 15) * 4 : hi;
-                    if (D.vec && at[j] + 4 <= hi) {
-                        const float4 x = *reinterpret_cast<const float4*>(R.y + at[j]);
-                        v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[j][e] = at[j] + e < hi ? R.y[at[j] + e] : kNegInf;
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (!weighs(v[j][e]) || R.bin_of(v[j][e]) > H.u_hi) continue;
-                        const uint32_t to = atomicAdd(&n, 1u);
-                        if (to < kMostCands) keys[to] = key_of(v[j][e], at[j] + e);
-                    }
-            }
-            __syncthreads();
-            if (t == 0) listed = 0;
-            __syncthreads();
-        }
+        collect_runs<kBinThreads>(D, R, H.u_hi, D.run + m * D.runs, lo, hi, list, &listed, keys, &n);
     } else {
         int turn = 0;
         sum_bins(ask, turn, B);
@@ -1311,11 +1363,9 @@ void draw_collect_kernel(DrawView D) {
 template <bool CAP>
 __global__ __launch_bounds__(kThreads)
 void draw_token_kernel(DrawView D) {
-    union Lds {
-        Sorter sorter;
-        Digits digits;
-    };
-    __shared__ Lds S;
+    __shared__ RowLds S;
+    __shared__ Ask ask;
+    __shared__ uint32_t collected;
     const int64_t m = blockIdx.x;
     Part p = part_of(D, m);
     const Args A = args_of(D, m);
@@ -1338,12 +1388,23 @@ void draw_token_kernel(DrawView D) {
         __syncthreads();
         R.level_of_top();
         if (R.mode == kByRuns) H.k_bin = H.p_hi = -1, H.p_lo = H.u_lo = 0;
-        if (H.collected > kMostCands) {
+        int turn = 0;
+        uint32_t found = H.collected;
+        if (found > kMostCands && R.mode == kByRuns) {
+            // About as many runs as top_k weigh anything, or fewer: their border is
+            // far down.  (One range of 57,600 allowed, top-k 1000: 78 us, 445 by
+            // digits; 32 such rows 108 and 588.)
+            R.mode = kCounted;
+            found = by_bins(S, ask, collected, turn, D, R, B, H);
+#pragma unroll
+            for (int j = 0; j < kCandsPer; ++j) key[j] = S.sorter.key[j * kThreads + threadIdx.x];
+            __syncthreads();
+        }
+        if (found > kMostCands) {
             by_digits(S.digits, D, R, &token, &n);
         } else {
-            int turn = 0;
             if (R.mode == kSummed) sum_bins(S.sorter.ask, turn, B);
-            draw_from_cands(S.sorter, turn, R, B, H, H.collected, key, &token, &n);
+            draw_from_cands(S.sorter, turn, R, B, H, found, key, &token, &n);
         }
     }
     store(D, m, token, n);
@@ -1378,12 +1439,17 @@ hipError_t launch(const DrawView& D, hipStream_t stream) {
 // Workgroups of a row: one, in one launch, for short rows, and for longer ones
 // where there are many; else about 512 in all (two a CU), of 4096 logits each at
 // least, in four launches.  Top-k 50 / top-p 0.9, one launch against four, us:
-//   1 x 16384     17 / 25   23 / 29       256 x 32000   29 / 45   35 / 69
-//   1 x 32000     22 / 37   24 / 30       300 x 65536   75 / 131  55 / 131
-//   64 x 32000    23 / 38   31 / 54       512 x 131072  150 / 255  92 / 296
+//   1 x 16384    15 / 23   22 / 27        128 x 65536  23 / 64   33 / 66
+//   4 x 20000    17 / 30   25 / 31        256 x 65536  29 / 74   43 / 100
+//   1 x 32000    17 / 35   23 / 29        300 x 65536  53 / 136  57 / 132
+//   16 x 40000   19 / 44   26 / 35        256 x 131072 45 / 138  59 / 165
+//   64 x 32000   19 / 38   31 / 52        300 x 262144 131 / 479 124 / 385
+//   256 x 32000  23 / 45   35 / 66        512 x 262144 150 / 494 163 / 530
+// Longer rows stay with four, which share the work out where rows differ: one
+// launch takes what its slowest row does.
 constexpr int64_t kPartLeast = 4096;
 int parts_of(int64_t V, int64_t M) {
-    if (V <= 16384 || (V <= 40960 && M >= 16) || M > kMostSplit) return 1;
+    if (V <= 20480 || (V <= 40960 && M >= 16) || (V <= 65536 && M >= 128) || M > kMostSplit) return 1;
     const int64_t most = (V + kPartLeast - 1) / kPartLeast, want = M > kWorkgroups / 2 ? 2 : kWorkgroups / M;
     const int64_t parts = want < most ? want : most;
     return static_cast<int>(parts > kMaxParts ? kMaxParts : parts);
@@ -1419,7 +1485,7 @@ hipError_t launch_logits_draw(const DrawArgs& a, void* ws, hipStream_t stream) {
     // whole runs, which are whole quads
     D.part_len = ((a.V + D.parts - 1) / D.parts + kRun - 1) / kRun * kRun;
     D.vec = (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 && a.ldl % 4 == 0;
-    D.runs = D.parts > 1 ? runs_of(a.V) : 0;
+    D.runs = D.parts > 1 || runs_of(a.V) <= kMostRuns ? runs_of(a.V) : 0;
     const size_t m = static_cast<size_t>(a.M);
     char* p = static_cast<char*>(ws);
     D.part = reinterpret_cast<Part*>(p);

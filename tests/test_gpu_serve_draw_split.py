@@ -194,3 +194,27 @@ def test_graph():
         call(*out[2:])
         torch.cuda.synchronize()
         assert torch.equal(out[0], out[2]) and torch.equal(out[1], out[3])
+
+
+@pytest.mark.parametrize("V,M", [(32000, 20), (90000, 3), (262144, 1)])
+@pytest.mark.parametrize("less", [-1, 0, 1, 40])
+def test_a_range_is_allowed(V, M, less):
+    """As many runs of 64 as top_k have logits at all, or a few more or fewer: most of the range is behind their border."""
+    say(f"logits_draw a range of V={V}, runs less {less}")
+    rng = np.random.default_rng(11)
+    k = min(V // 256, 1000)
+    z = np.full((M, V), NEG, np.float32)
+    z[:, 640 : 640 + 64 * (k - less)] = rng.normal(0, 2, (M, 64 * (k - less)))
+    check(z, 1.0, k, u=rng.random(M))
+    check(z, 0.7, k, 0.9, 0.01, u=rng.random(M))
+
+
+@pytest.mark.parametrize("M", [257, 512])
+def test_many_long_rows(M):
+    """As many as are shared out by workgroups, of all kinds."""
+    rng = np.random.default_rng(M)
+    say(f"logits_draw {M} long rows")
+    z = logits(rng, M, 66000)
+    z[rng.integers(0, M, 40)] = NEG
+    check(z, rng.choice([0.0, 0.7, 1.0], M), rng.choice([0, 0, 1, 64, 900, 5000], M), rng.choice([1.0, 0.95, 0.5], M),
+          rng.choice([0.0, 0.02], M), u=rng.random(M))
