@@ -31,7 +31,8 @@
 // One row of 262,144 takes 33 us, which is their four chains of dependent loads
 // and barriers (4.5, 8.7, 6.8, 9.4); 32 rows with mixed filters 43-49 us, 128 of
 // which 97% is masked 81: the first launch reads them at 4.0 TB/s (33 us), and
-// rows that need sums are read twice more, from the last-level cache.  Short rows
+// rows that need sums are read twice more, from the last-level cache (the second
+// time only runs that reach the answers, where they are few).  Short rows
 // are one launch, a workgroup each (256 rows of 32,000, top-k: 25 us).
 #include <stdint.h>
 
@@ -588,17 +589,20 @@ __device__ __forceinline__ void ask_bins(Ask& S, const Bins<T>& B, int slot, boo
     }
 }
 
-// Bins that hold the answers, in every thread.
+// Bins that hold the answers, in every thread; *reach: elements up to the last
+// of them.
 template <bool CAP, int T>
-__device__ __forceinline__ Head choose_bins(Ask& S, const Row<CAP>& R, const Bins<T>& B, Sum above) {
+__device__ __forceinline__ Head choose_bins(Ask& S, const Row<CAP>& R, const Bins<T>& B, Sum above, uint32_t* reach) {
     Head H = {above.mass, above.count, 0, -1, 0, -1, 0, -1};
     const uint32_t kk = R.top_k > 0 && static_cast<uint32_t>(R.top_k) < B.total.count ? R.top_k : B.total.count;
     if (R.mode != kSummed) {  // the first kk whole (of runs: fewer than k may be there, then all)
         ask_bins(S, B, 0, false, kk);
         __syncthreads();
         H.u_hi = R.mode == kByRuns && B.total.count < static_cast<uint32_t>(R.top_k) ? kBins - 1 : S.hit[0].at;
+        *reach = S.hit[0].upto.count;
         return H;
     }
+    *reach = 0;
     uint64_t k_lo = B.total.mass, k_hi = B.total.mass;
     if (kk < B.total.count) {
         ask_bins(S, B, 0, false, kk);
@@ -608,6 +612,7 @@ __device__ __forceinline__ Head choose_bins(Ask& S, const Row<CAP>& R, const Bin
         if (h.upto.count != kk) {
             H.k_bin = h.at;
             k_lo = h.before.mass;
+            *reach = h.upto.count;
         }
     }
     uint64_t lo = k_lo, hi = k_hi;
@@ -617,6 +622,7 @@ __device__ __forceinline__ Head choose_bins(Ask& S, const Row<CAP>& R, const Bin
         __syncthreads();
         H.p_lo = S.hit[1].at;
         H.p_hi = S.hit[2].at;
+        *reach = max(*reach, S.hit[2].upto.count);
         lo = min(lo, S.hit[1].before.mass);
         hi = min(hi, S.hit[2].upto.mass);
     }
@@ -630,6 +636,7 @@ __device__ __forceinline__ Head choose_bins(Ask& S, const Row<CAP>& R, const Bin
     __syncthreads();
     H.u_lo = S.hit[3].at;
     H.u_hi = S.hit[4].at;
+    *reach = max(*reach, S.hit[4].upto.count);
     return H;
 }
 
@@ -1004,12 +1011,13 @@ __device__ __forceinline__ void count_runs(const Row<CAP>& R, const float* run, 
     }
 }
 
-// Keys of the logits of [lo, hi) in bins up to u_hi, as collect() has them: only
-// runs that reach the bins are read, by 16 threads each.  list: 4 T numbers in
-// LDS; *listed and *n are 0 before, behind a barrier.
+// The same where few runs reach the bins: only those are read, by 16 threads
+// each.  list: 4 T numbers in LDS; *listed and *n are 0 before, behind a barrier.
 template <int T, bool CAP>
-__device__ __forceinline__ void collect_runs(const DrawView& D, const Row<CAP>& R, int u_hi, const float* run, int64_t lo,
+__device__ __forceinline__ void collect_runs(const DrawView& D, const Row<CAP>& R, const Head& H, const float* run, int64_t lo,
                                              int64_t hi, int32_t* list, uint32_t* listed, uint64_t* keys, uint32_t* n) {
+    const int last = max(H.u_hi, max(H.p_hi, H.k_bin));
+    const float least = R.floor_of(last);  // drops most (and NaN) by one comparison
     const int t = threadIdx.x;
     const int64_t r0 = lo / kRun, r1 = (hi + kRun - 1) / kRun;
     for (int64_t r = r0; r < r1; r += 4 * T) {
@@ -1018,7 +1026,7 @@ __device__ __forceinline__ void collect_runs(const DrawView& D, const Row<CAP>& 
         for (int j = 0; j < 4; ++j) top[j] = r + j * T + t < r1 ? run[r + j * T + t] : kNegInf;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (weighs(top[j]) && R.bin_of(top[j]) <= u_hi)
+            if (top[j] >= least && R.bin_of(top[j]) <= last)
                 list[atomicAdd(listed, 1u)] = static_cast<int32_t>(r + j * T + t - r0);
         __syncthreads();
         const uint32_t have = *listed;
@@ -1041,7 +1049,7 @@ __device__ __forceinline__ void collect_runs(const DrawView& D, const Row<CAP>& 
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    if (!weighs(v[j][e]) || R.bin_of(v[j][e]) > u_hi) continue;
+                    if (!(v[j][e] >= least) || !chosen(H, R.bin_of(v[j][e]))) continue;
                     const uint32_t to = atomicAdd(n, 1u);
                     if (to < kMostCands) keys[to] = key_of(v[j][e], at[j] + e);
                 }
@@ -1050,6 +1058,15 @@ __device__ __forceinline__ void collect_runs(const DrawView& D, const Row<CAP>& 
         if (t == 0) *listed = 0;
         __syncthreads();
     }
+}
+
+// Whether collect_runs() pays where so many elements of a row reach the bins: at
+// most half the runs do, and there are enough of them.  (Top-p 0.9 of a few kept
+// tokens, with this and without: 128 rows of 262,144 126 and 145 us, of 50,257 57
+// and 66; in parts of 4096 a row takes 31 us and 29.)
+constexpr int64_t kDirect = 32768;
+__device__ __forceinline__ bool few_runs(const DrawView& D, uint32_t reach, int64_t len) {
+    return len > kDirect && 2 * static_cast<int64_t>(reach) <= D.runs;
 }
 
 // ------------------------------------------------------------ a row by one workgroup
@@ -1069,15 +1086,15 @@ union RowLds {
 // What of a row holds the answers, by bins of all its elements: keys to
 // S.sorter.key, returns how many.
 template <bool CAP>
-__device__ __forceinline__ uint32_t by_bins(RowLds& S, Ask& ask, uint32_t& collected, int& turn, const DrawView& D,
-                                            const Row<CAP>& R, Bins<kThreads>& B, Head& H) {
+__device__ __forceinline__ uint32_t by_bins(RowLds& S, Ask& ask, uint32_t& collected, uint32_t& listed, int& turn,
+                                            const DrawView& D, const Row<CAP>& R, const float* run, Bins<kThreads>& B, Head& H) {
     const int t = threadIdx.x;
     const int64_t V = D.a.V;
     for (int i = t; i < kBins; i += kThreads) {
         S.bins.count[i] = 0;
         S.bins.mass[i] = 0;
     }
-    if (t == 0) collected = 0;
+    if (t == 0) collected = listed = 0;
     const Batch again = load_batch<kThreads>(R.y, 0, V, D.vec);
     __syncthreads();
     const Sum mine = fill_bins<kThreads>(again, D, R, 0, V, S.bins.count, S.bins.mass, S.bins.sparse);
@@ -1085,8 +1102,12 @@ __device__ __forceinline__ uint32_t by_bins(RowLds& S, Ask& ask, uint32_t& colle
     block_before<kThreads>(ask.scan, turn, mine, &above);  // and a barrier behind the atomics
     B = load_bins<kThreads>(S.bins.count, S.bins.mass);
     sum_bins(ask, turn, B);  // and one behind the loads
-    H = choose_bins(ask, R, B, above);
-    collect<kThreads>(load_batch<kThreads>(R.y, 0, V, D.vec), D, R, H, 0, V, S.sorter.key, &collected);
+    uint32_t reach;
+    H = choose_bins(ask, R, B, above, &reach);
+    if (few_runs(D, reach, V))
+        collect_runs<kThreads>(D, R, H, run, 0, V, reinterpret_cast<int32_t*>(S.sorter.sorted), &listed, S.sorter.key, &collected);
+    else
+        collect<kThreads>(load_batch<kThreads>(R.y, 0, V, D.vec), D, R, H, 0, V, S.sorter.key, &collected);
     __syncthreads();
     return collected;
 }
@@ -1104,7 +1125,7 @@ void draw_row_kernel(DrawView D) {
     const Args A = args_of(D, m);
     fill_exp_table();
     const float* y = D.a.logits + m * D.a.ldl;
-    const Part p = first_of<kThreads, true>(y, 0, V, D.vec, parts, by_runs(D, A) ? run : nullptr);
+    const Part p = first_of<kThreads, true>(y, 0, V, D.vec, parts, D.runs > 0 && (V > kDirect || by_runs(D, A)) ? run : nullptr);
     Row<CAP> R = row_of<CAP>(D, m, A, p.best, p.sum, p.count);
     int32_t token = p.best ? index_of(p.best) : -1, n = p.best ? 1 : 0;
     if (R.mode != kFirst) {
@@ -1124,8 +1145,9 @@ void draw_row_kernel(DrawView D) {
             __syncthreads();
             B = load_bins<kThreads>(S.bins.count, S.bins.mass);
             sum_bins(ask, turn, B);
-            H = choose_bins(ask, R, B, {0, 0});
-            collect_runs<kThreads>(D, R, H.u_hi, run, 0, V, reinterpret_cast<int32_t*>(S.sorter.sorted), &listed, S.sorter.key,
+            uint32_t reach;
+            H = choose_bins(ask, R, B, {0, 0}, &reach);
+            collect_runs<kThreads>(D, R, H, run, 0, V, reinterpret_cast<int32_t*>(S.sorter.sorted), &listed, S.sorter.key,
                                    &collected);
             found = collected;
             if (found > kMostCands) {  // see draw_token_kernel
@@ -1133,7 +1155,7 @@ void draw_row_kernel(DrawView D) {
                 __syncthreads();  // collected is read before it is written
             }
         }
-        if (R.mode != kByRuns) found = by_bins(S, ask, collected, turn, D, R, B, H);
+        if (R.mode != kByRuns) found = by_bins(S, ask, collected, listed, turn, D, R, run, B, H);
         if (found > kMostCands) {
             by_digits(S.digits, D, R, &token, &n);
         } else {
@@ -1162,7 +1184,7 @@ void draw_first_kernel(DrawView D) {
         D.mass[m * kBins + i] = 0;
     }
     const Part p = first_of<kThreads, WIDE>(D.a.logits + m * D.a.ldl, lo, min(lo + D.part_len, D.a.V), D.vec, parts,
-                            by_runs(D, A) ? D.run + m * D.runs : nullptr);
+                            A.temperature > 0.0f ? D.run + m * D.runs : nullptr);
     if (t == 0) {
         D.part[m * D.parts + blockIdx.x] = p;
         if (blockIdx.x == 0) D.head[m] = Head{};
@@ -1283,8 +1305,13 @@ void draw_bins_kernel(DrawView D) {
         __syncthreads();
         Bins<kBinThreads> B = load_bins<kBinThreads>(count, mass);
         sum_bins(ask, turn, B);
-        const Head H = choose_bins(ask, R, B, {0, 0});
-        if (t == 0) D.head[m].u_hi = H.u_hi;
+        uint32_t reach;
+        const Head H = choose_bins(ask, R, B, {0, 0}, &reach);
+        if (t == 0) {
+            D.head[m].k_bin = H.k_bin;
+            D.head[m].p_hi = H.p_hi;
+            D.head[m].u_hi = H.u_hi;
+        }
         return;
     }
     R.level_of_top();
@@ -1335,13 +1362,15 @@ void draw_collect_kernel(DrawView D) {
     p = join(p);
     const Row<CAP> R = row_of<CAP>(D, m, A, p.best, p.sum, p.count);
     if (R.mode == kFirst) return;
+    const float* run = D.run + m * D.runs;
     if (R.mode == kByRuns) {
         __syncthreads();
-        collect_runs<kBinThreads>(D, R, H.u_hi, D.run + m * D.runs, lo, hi, list, &listed, keys, &n);
+        collect_runs<kBinThreads>(D, R, H, run, lo, hi, list, &listed, keys, &n);
     } else {
         int turn = 0;
         sum_bins(ask, turn, B);
-        H = choose_bins(ask, R, B, {H.above_mass, H.above_count});
+        uint32_t reach;
+        H = choose_bins(ask, R, B, {H.above_mass, H.above_count}, &reach);
         if (lo == 0 && t == 0) {
             head->k_bin = H.k_bin;
             head->p_lo = H.p_lo;
@@ -1349,7 +1378,10 @@ void draw_collect_kernel(DrawView D) {
             head->u_lo = H.u_lo;
             head->u_hi = H.u_hi;
         }
-        collect<kBinThreads>(first, D, R, H, lo, hi, keys, &n);
+        if (few_runs(D, reach, hi - lo))
+            collect_runs<kBinThreads>(D, R, H, run, lo, hi, list, &listed, keys, &n);
+        else
+            collect<kBinThreads>(first, D, R, H, lo, hi, keys, &n);
     }
     __syncthreads();
     const uint32_t found = n;
@@ -1365,7 +1397,7 @@ __global__ __launch_bounds__(kThreads)
 void draw_token_kernel(DrawView D) {
     __shared__ RowLds S;
     __shared__ Ask ask;
-    __shared__ uint32_t collected;
+    __shared__ uint32_t collected, listed;
     const int64_t m = blockIdx.x;
     Part p = part_of(D, m);
     const Args A = args_of(D, m);
@@ -1387,7 +1419,6 @@ void draw_token_kernel(DrawView D) {
     if (R.mode != kFirst) {
         __syncthreads();
         R.level_of_top();
-        if (R.mode == kByRuns) H.k_bin = H.p_hi = -1, H.p_lo = H.u_lo = 0;
         int turn = 0;
         uint32_t found = H.collected;
         if (found > kMostCands && R.mode == kByRuns) {
@@ -1395,7 +1426,7 @@ void draw_token_kernel(DrawView D) {
             // far down.  (One range of 57,600 allowed, top-k 1000: 78 us, 445 by
             // digits; 32 such rows 108 and 588.)
             R.mode = kCounted;
-            found = by_bins(S, ask, collected, turn, D, R, B, H);
+            found = by_bins(S, ask, collected, listed, turn, D, R, D.run + m * D.runs, B, H);
 #pragma unroll
             for (int j = 0; j < kCandsPer; ++j) key[j] = S.sorter.key[j * kThreads + threadIdx.x];
             __syncthreads();

@@ -218,3 +218,20 @@ def test_many_long_rows(M):
     z[rng.integers(0, M, 40)] = NEG
     check(z, rng.choice([0.0, 0.7, 1.0], M), rng.choice([0, 0, 1, 64, 900, 5000], M), rng.choice([1.0, 0.95, 0.5], M),
           rng.choice([0.0, 0.02], M), u=rng.random(M))
+
+
+@pytest.mark.parametrize("V,M", [(50257, 16), (80001, 200)])
+@pytest.mark.parametrize("masked", [0.0, 0.97])
+def test_few_kept_of_long_parts(V, M, masked):
+    """Filters on sums that end among few elements: only the runs that reach them are read again."""
+    say(f"logits_draw few kept of V={V} M={M} masked={masked}")
+    rng = np.random.default_rng(V)
+    z = rng.normal(0, 2, (M, V)).astype(np.float32)
+    z[np.arange(M)[:, None], rng.integers(0, V, (M, 40))] = rng.uniform(14, 26, (M, 40))
+    z[rng.random((M, V)) < masked] = NEG
+    z[:, V - 1] = rng.uniform(20, 27, M)
+    z[:, 100:200] = NAN
+    check(z, rng.choice([0.7, 1.0], M), rng.choice([0, 0, 5000, V // 200], M), rng.choice([0.9, 0.5, 0.999], M),
+          rng.choice([0.0, 0.02], M), u=rng.random(M))
+    check(z, 1.0, 0, 0.95, u=rng.random(M), offset=1, ld=V + 2)
+    check(z, 1.0, u=rng.random(M))
