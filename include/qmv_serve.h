@@ -139,8 +139,8 @@ typedef struct qmv_lora {
  * (row_start[b] .. row_start[b + 1] - 1, as in qmv_kv_batch) with s =
  * adapter[b]; y_r = base_r where adapter[b] is outside [0, slots).
  * x float32, row r at x + r * ldx (ldx >= K); base (or NULL: zeros) and y
- * likewise with N.  base may be y: then the product's output is updated in
- * place, and rows without an adapter are not touched.  Rows at or behind
+ * likewise with N.  base may be y, with ldb = ldy: then the product's output is
+ * updated in place, and rows without an adapter are not touched.  Rows at or behind
  * row_start[B] are left as they were.  Weights enter as they are, x and all
  * sums are float32.  row_start and adapter are checked where they are used:
  * row starts out of order leave rows undefined.
