@@ -235,3 +235,34 @@ def test_few_kept_of_long_parts(V, M, masked):
           rng.choice([0.0, 0.02], M), u=rng.random(M))
     check(z, 1.0, 0, 0.95, u=rng.random(M), offset=1, ld=V + 2)
     check(z, 1.0, u=rng.random(M))
+
+
+@pytest.mark.parametrize("V", [65536, 262200])
+def test_the_same_in_any_batch(V):
+    """One workgroup a row for 513 rows, several for 100: sums are exact, so tokens and counts are the same."""
+    qmv = _qmv()
+    say(f"logits_draw V={V}, 513 rows and 100 at a time")
+    M = 513
+    g = torch.Generator(device=DEV).manual_seed(V)
+    z = torch.randn(M, V, generator=g, device=DEV) * 3
+    u = torch.rand(M, generator=g, device=DEV)
+
+    def pick(values, dtype):
+        i = torch.randint(0, len(values), (M,), generator=g, device=DEV)
+        return torch.tensor(values, dtype=dtype, device=DEV)[i]
+
+    t, p = pick([0.0, 0.5, 1.0, 1.0], torch.float32), pick([1.0, 0.9, 0.3], torch.float32)
+    k, low = pick([0, 0, 1, 50, 900, 5000], torch.int32), pick([0.0, 0.05], torch.float32)
+
+    def draw(rows):
+        a = [x[rows].contiguous() for x in (z, t, k, p, low, u)]
+        n = a[0].shape[0]
+        token, kept = (torch.full((n,), -7, dtype=torch.int32, device=DEV) for _ in range(2))
+        size = qmv.logits_draw_ws_bytes(V, n)
+        qmv.logits_draw(a[0], V, *a[1:], token, kept, V, n, 0.0, torch.empty(size, dtype=torch.uint8, device=DEV), size)
+        return torch.stack([token, kept])
+
+    whole = draw(slice(0, M))
+    parts = torch.cat([draw(slice(i, min(i + 100, M))) for i in range(0, M, 100)], 1)
+    torch.cuda.synchronize()
+    assert torch.equal(whole, parts)
