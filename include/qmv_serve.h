@@ -140,9 +140,9 @@ typedef struct qmv_lora {
  * adapter[b]; y_r = base_r where adapter[b] is outside [0, slots).
  * x float32, row r at x + r * ldx (ldx >= K); base (or NULL: zeros) and y
  * likewise with N.  base may be y, with ldb = ldy: then the product's output is
- * updated in place, and rows without an adapter are not touched.  Rows at or behind
- * row_start[B] are left as they were.  Weights enter as they are, x and all
- * sums are float32.  row_start and adapter are checked where they are used:
+ * updated in place, and rows without an adapter are not touched.  Rows before
+ * row_start[0] (of a part of a batch) and at or behind row_start[B] are left as
+ * they were.  Weights enter as they are, x and all sums are float32.  row_start and adapter are checked where they are used:
  * row starts out of order leave rows undefined.
  * 1 <= B <= 65535, 1 <= T < 2^24.
  * ws: lora_add_ws_bytes(lora, B, T) bytes, 16-byte aligned, overwritten. */

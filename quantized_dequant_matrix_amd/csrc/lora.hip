@@ -64,7 +64,8 @@ struct Tile {
 // Sequence b's tiles have the numbers from row_start[b] / 16 + b on: enough for
 // its rows whatever their alignment, and in the order of the sequences, so
 // that a tile's sequence is found by a search (64 entries a step, by the whole
-// wave) without sums over the batch.
+// wave) without sums over the batch.  Numbers below row_start[0] / 16 are found
+// in the first sequence and are of rows before it, which belong to none.
 __device__ __forceinline__ Tile tile_of(const LoraView& D, int tile) {
     const int32_t* start = D.a.row_start;
     const int lane = threadIdx.x & (kWave - 1), B = static_cast<int>(D.a.B);
@@ -97,7 +98,7 @@ __device__ __forceinline__ Tile tile_of(const LoraView& D, int tile) {
     }
     end = min(end, D.a.T);
     const int64_t row = first + kTile * (tile - (first >> 4) - lo);
-    if (row < 0 || row >= end) return t;
+    if (row < 0 || row < first || row >= end) return t;
     t.row = static_cast<int>(row);
     t.rows = static_cast<int>(min(end - row, static_cast<int64_t>(kTile)));
     return t;
