@@ -83,6 +83,14 @@ __device__ __forceinline__ bool weighs(float y) {
     return (from_low & 0x7fffffffu) >= 0x00800000u || b == 0x7f800000u;
 }
 
+// The largest of four numbers, NaN dropped (NaN if all are).  The compiler makes
+// v_max3_f32 of nested maxima and does not quiet what it gives it, and of a
+// signalling NaN the instruction makes NaN, whatever stands beside it.
+__device__ __forceinline__ float max4(const float (&v)[4]) {
+    return fmaxf(fmaxf(__builtin_canonicalizef(v[0]), __builtin_canonicalizef(v[1])),
+                 fmaxf(__builtin_canonicalizef(v[2]), __builtin_canonicalizef(v[3])));
+}
+
 // Larger logits have larger codes; -0 ranks with +0.
 __device__ __forceinline__ uint32_t code_of(float y) {
     const float v = fminf(y, kMaxLogit);
@@ -863,7 +871,7 @@ __device__ __forceinline__ Part first_of(const float* y, int64_t lo, int64_t hi,
     uint32_t count = 0;
     for_quads<T, WIDE>(load_batch<T, WIDE>(y, lo, hi, vec), y, lo, hi, vec, [&](const float (&v)[4], int64_t at) {
         // NaN is dropped; a NaN that is left is not larger than anything
-        float top = fminf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), kMaxLogit);
+        float top = fminf(max4(v), kMaxLogit);
         top = v[0] != v[0] && v[1] != v[1] && v[2] != v[2] && v[3] != v[3] ? kNegInf : top;
         at_best = top > best ? static_cast<int32_t>(at) : at_best;  // a thread goes through rising indexes
         best = fmaxf(best, top);
@@ -879,7 +887,7 @@ __device__ __forceinline__ Part first_of(const float* y, int64_t lo, int64_t hi,
     if (best > kNegInf) {
         int place = 3;
 #pragma unroll
-        for (int e = 2; e >= 0; --e) place = at_best + e < hi && fminf(y[at_best + e], kMaxLogit) == best ? e : place;
+        for (int e = 2; e >= 0; --e) place = at_best + e < hi && y[at_best + e] >= best ? e : place;  // +infinity reaches it, NaN does not
         p.best = key_of(best, at_best + place);
     }
     p = join(p);
@@ -981,7 +989,7 @@ __device__ __forceinline__ void collect(const Batch& first, const DrawView& D, c
     // four at a time are dropped, most of them (NaN is not above anything)
     const float least = R.floor_of(max(H.u_hi, max(H.p_hi, H.k_bin)));
     for_quads<T, false>(first, R.y, lo, hi, D.vec, [&](const float (&v)[4], int64_t i) {
-        if (!(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) >= least)) return;
+        if (!(max4(v) >= least)) return;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if (!(v[e] >= least) || !chosen(H, R.bin_of(v[e]))) continue;
