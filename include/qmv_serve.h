@@ -178,7 +178,8 @@ int lora_add(const qmv_lora* lora, const int32_t* adapter, const int32_t* row_st
  * (tanh to 2^-42 of softcap), so that decisions within about that of their
  * border may fall either way.
  * 1 <= M <= 65535, 1 <= V < 2^31, softcap in [0, 65536].
- * ws: logits_draw_ws_bytes(V, M) bytes, 16-byte aligned, overwritten. */
+ * ws: logits_draw_ws_bytes(V, M) bytes, 16-byte aligned, overwritten.  They do
+ * not fall as V or M grows: what serves a batch serves every smaller one. */
 size_t logits_draw_ws_bytes(int64_t V, int64_t M);
 int logits_draw(const float* logits, int64_t ldl, const float* temperature, const int32_t* top_k, const float* top_p,
                 const float* min_p, const float* u, int32_t* token, int32_t* kept, int64_t V, int64_t M, float softcap,

@@ -1487,8 +1487,12 @@ hipError_t launch(const DrawView& D, hipStream_t stream) {
 // Longer rows stay with four, which share the work out where rows differ: one
 // launch takes what its slowest row does.
 constexpr int64_t kPartLeast = 4096;
+int64_t most_split(int64_t V) {  // rows of a call that are split
+    return V <= 20480 ? 0 : (V <= 40960 ? 15 : (V <= 65536 ? 127 : kMostSplit));
+}
+
 int parts_of(int64_t V, int64_t M) {
-    if (V <= 20480 || (V <= 40960 && M >= 16) || (V <= 65536 && M >= 128) || M > kMostSplit) return 1;
+    if (M > most_split(V)) return 1;
     const int64_t most = (V + kPartLeast - 1) / kPartLeast, want = M > kWorkgroups / 2 ? 2 : kWorkgroups / M;
     const int64_t parts = want < most ? want : most;
     return static_cast<int>(parts > kMaxParts ? kMaxParts : parts);
@@ -1500,11 +1504,15 @@ size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
 
+// What the largest batch of up to M rows needs that is split: a program that
+// allocates once for its largest batch has enough for a smaller one, and for a
+// longer vocabulary more.  (A row more is 80 KB for its bins and candidates, which
+// what all parts of all rows say, 16 KB at most, does not outweigh.)
 size_t draw_ws_bytes(int64_t V, int64_t M) {
-    const int parts = parts_of(V, M);
-    if (parts == 1) return 256;
+    if (M > most_split(V)) M = most_split(V);
+    if (M == 0) return 256;
     const size_t m = static_cast<size_t>(M);
-    return align256(m * static_cast<size_t>(parts) * sizeof(Part)) + align256(m * sizeof(Head)) +
+    return align256(m * static_cast<size_t>(parts_of(V, M)) * sizeof(Part)) + align256(m * sizeof(Head)) +
            m * (kBins * (sizeof(uint32_t) + sizeof(uint64_t)) + kMostCands * sizeof(uint64_t)) +
            align256(m * static_cast<size_t>(runs_of(V)) * sizeof(float));
 }
