@@ -145,7 +145,8 @@ typedef struct qmv_lora {
  * they were.  Weights enter as they are, x and all sums are float32.  row_start and adapter are checked where they are used:
  * row starts out of order leave rows undefined.
  * 1 <= B <= 65535, 1 <= T < 2^24.
- * ws: lora_add_ws_bytes(lora, B, T) bytes, 16-byte aligned, overwritten. */
+ * ws: lora_add_ws_bytes(lora, B, T) bytes, 16-byte aligned, overwritten.  They do
+ * not fall as B or T grows: what serves a batch serves every smaller one. */
 size_t lora_add_ws_bytes(const qmv_lora* lora, int64_t B, int64_t T);
 int lora_add(const qmv_lora* lora, const int32_t* adapter, const int32_t* row_start, const float* x, int64_t ldx,
              const float* base, int64_t ldb, float* y, int64_t ldy, int64_t B, int64_t T, void* ws, size_t ws_bytes,

@@ -496,8 +496,10 @@ int64_t tiles_with_rows(int64_t B, int64_t T) { return tiles_of(B, T) < T ? tile
 // loads at once) or a multiple.  More shares of fewer k gain nothing here and
 // cost the expansion their sums (32 rows of rank up to 64: 128 k a wave 24 us,
 // 64 k 25, 32 k 33 when the rest was 4 us slower).
+int64_t most_shares(const qmv_lora& l) { return (l.K + kWaves * 128 - 1) / (kWaves * 128); }
+
 void split_k(const qmv_lora& l, int64_t B, int64_t T, int* shares, int64_t* per_wave) {
-    const int64_t most = (l.K + kWaves * 128 - 1) / (kWaves * 128);
+    const int64_t most = most_shares(l);
     int64_t want = 1024 / tiles_with_rows(B, T);
     want = want < 1 ? 1 : (want > most ? most : want);
     *per_wave = ((l.K + want * kWaves - 1) / (want * kWaves) + 127) / 128 * 128;
@@ -543,11 +545,13 @@ bool rows_aligned(const float* p, int64_t ld) { return (reinterpret_cast<uintptr
 
 }  // namespace
 
-size_t lora_ws_bytes(const qmv_lora& l, int64_t B, int64_t T) {
-    int shares;
-    int64_t per_wave;
-    split_k(l, B, T, &shares, &per_wave);
-    return static_cast<size_t>(shares) * static_cast<size_t>(T) * static_cast<size_t>(l.max_rank) * sizeof(float);
+// Enough for every batch of up to T rows, of any sequences.  Shares fall as the
+// batch grows: the shares times the tiles are 1024 at most where there are
+// several, and a tile has 16 rows at most; else there is one share.
+size_t lora_ws_bytes(const qmv_lora& l, int64_t, int64_t T) {
+    int64_t rows = most_shares(l) * T;
+    if (rows > 1024 * kTile) rows = 1024 * kTile;
+    return static_cast<size_t>(rows > T ? rows : T) * static_cast<size_t>(l.max_rank) * sizeof(float);
 }
 
 hipError_t launch_lora(const qmv_lora& l, const LoraArgs& a, void* ws, hipStream_t stream) {

@@ -27,6 +27,31 @@ def test_draw_in_the_vocabulary(M):
     assert not falls(sizes), falls(sizes)
 
 
+def lora_bytes(B, T, K=5376, N=21504, max_rank=64):
+    l = qmv._Lora(None, None, None, None, K, N, 8, max_rank, 0)
+    return qmv.lora_add_ws_bytes(type("D", (), {"ref": ctypes.addressof(l)}), B, T)
+
+
+@pytest.mark.parametrize("K", [8, 128, 512, 520, 4096, 5376, 21504, 100000, 2 ** 23])
+@pytest.mark.parametrize("max_rank", [8, 16, 64, 256])
+def test_adapters_in_rows_and_sequences(K, max_rank):
+    rows = sorted(set(MANY) | {1000, 1500, 1501, 2000, 3001, 8192, 16384, 16385, 2 ** 20, 2 ** 24 - 1})
+    for B in (1, 4, 32, 300, 65535):
+        sizes = [(T, lora_bytes(B, T, K, 21504, max_rank)) for T in rows]
+        assert all(n > 0 for _, n in sizes) and not falls(sizes), (B, falls(sizes))
+    for T in rows:
+        sizes = [(B, lora_bytes(B, T, K, 21504, max_rank)) for B in MANY]
+        assert not falls(sizes), (T, falls(sizes))
+
+
+def test_adapters_in_widths():
+    for B, T in ((1, 1), (32, 32), (4, 1611), (6, 8192)):
+        for vary, values in (("K", (8, 512, 1024, 4096, 5376, 21504, 65536)), ("N", (1, 300, 5376, 21504, 2 ** 23)),
+                             ("max_rank", (8, 16, 24, 64, 128, 256))):
+            sizes = [(v, lora_bytes(B, T, **{vary: v})) for v in values]
+            assert not falls(sizes), (vary, falls(sizes))
+
+
 def test_plan_in_the_sequences():
     def size(B):
         p = qmv._KVPool(None, None, 100, B, 8, 16)
