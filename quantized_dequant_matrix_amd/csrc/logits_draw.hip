@@ -123,6 +123,7 @@ struct Head {
     uint32_t above_count;
     uint32_t collected;
     int32_t k_bin, p_lo, p_hi, u_lo, u_hi;
+    uint32_t first_k;  // of rows that are collected whole: how many the first top_k are, 0: all that are collected
 };
 
 struct DrawView {
@@ -197,6 +198,26 @@ struct Row {
         // -infinity, where the bins are infinitely wide, would let masked logits in
         return b < kBins - 1 ? fmaxf(v, -kMaxLogit) : -kMaxLogit;
     }
+    // A weight below this logit is below 2^-150: it adds nothing to any sum and
+    // passes no min_p, so that such an element need not be collected where it is
+    // known how many there are.  (After level_of_top().)
+    __device__ __forceinline__ float least_weighing() const {
+        double v;
+        if constexpr (CAP) {
+            // levels are known to 2^-42; cap = softcap * tanh backwards
+            const double t = level - 152.0 / w.cap - 0x1p-38;
+            if (!(t > -1.0)) return -kMaxLogit;
+            v = log2((1.0 + t) / (1.0 - t)) / w.twice;
+        } else {
+            v = static_cast<double>(top) - 152.0 / w.k;
+        }
+        return fmaxf(static_cast<float>(v - fabs(v) * 0x1p-23), -kMaxLogit);  // rounded down
+    }
+    // Below this logit there is nothing to collect for the chosen bins.
+    __device__ __forceinline__ float least_of(const Head& H) const {
+        const float v = floor_of(max(H.u_hi, max(H.p_hi, H.k_bin)));
+        return mode != kSummed && H.first_k ? fmaxf(v, least_weighing()) : v;
+    }
     // Sums that the answers have to reach.
     __device__ __forceinline__ uint64_t need_p(uint64_t mass) const {
         const double border = ceil(fmax(static_cast<double>(top_p), 0.0) * static_cast<double>(mass));
@@ -256,9 +277,13 @@ __device__ __forceinline__ Row<CAP> row_of(const DrawView& D, int64_t m, const A
     R.w.twice = D.twice;
     R.unit = static_cast<double>(uint64_t{1} << D.q);
     R.top = logit_of(static_cast<uint32_t>(best >> 32));
-    // the equal steps reach to the nearer of twice the mean distance and a
-    // weight of 2^-64: neither the spread of the logits nor the temperature
-    // then matters much
+    // The equal steps reach to the nearer of twice the mean distance and a
+    // weight of 2^-64, all bins 64 times as far: the spread of the logits then
+    // matters little.  At a small temperature most of a row lies behind them, in
+    // the last bin.  A top-k that ends there is not slower for it: what weighs
+    // nothing is counted, not collected (see least_weighing and choose_bins; one
+    // row of 262,144 with a top-k of 40 at a temperature of 0.001 25 us, 1122 when
+    // it went digit by digit).
     const float mean = count ? fmaxf(R.top - sum / static_cast<float>(count), 0.0f) : 0.0f;
     R.per_bin = fminf(fmaxf(mean > 0.0f ? 0.5f * kEqualBins / mean : 0.0f,
                             static_cast<float>(fmin(R.w.k, 1e28)) * (kEqualBins / 64.0f)), 1e30f);
@@ -601,12 +626,14 @@ __device__ __forceinline__ void ask_bins(Ask& S, const Bins<T>& B, int slot, boo
 // of them.
 template <bool CAP, int T>
 __device__ __forceinline__ Head choose_bins(Ask& S, const Row<CAP>& R, const Bins<T>& B, Sum above, uint32_t* reach) {
-    Head H = {above.mass, above.count, 0, -1, 0, -1, 0, -1};
+    Head H = {above.mass, above.count, 0, -1, 0, -1, 0, -1, 0};
     const uint32_t kk = R.top_k > 0 && static_cast<uint32_t>(R.top_k) < B.total.count ? R.top_k : B.total.count;
     if (R.mode != kSummed) {  // the first kk whole (of runs: fewer than k may be there, then all)
         ask_bins(S, B, 0, false, kk);
         __syncthreads();
-        H.u_hi = R.mode == kByRuns && B.total.count < static_cast<uint32_t>(R.top_k) ? kBins - 1 : S.hit[0].at;
+        const bool all = R.mode == kByRuns && B.total.count < static_cast<uint32_t>(R.top_k);
+        H.u_hi = all ? kBins - 1 : S.hit[0].at;
+        H.first_k = all ? 0 : kk;
         *reach = S.hit[0].upto.count;
         return H;
     }
@@ -617,7 +644,7 @@ __device__ __forceinline__ Head choose_bins(Ask& S, const Row<CAP>& R, const Bin
         __syncthreads();
         const Hit h = S.hit[0];
         k_lo = k_hi = h.upto.mass;
-        if (h.upto.count != kk) {
+        if (h.upto.count != kk && h.upto.mass != h.before.mass) {  // whichever of a bin of zeros are among them
             H.k_bin = h.at;
             k_lo = h.before.mass;
             *reach = h.upto.count;
@@ -768,6 +795,7 @@ __device__ __forceinline__ void draw_from_cands(Sorter& S, int& turn, const Row<
         }
         if (R.has_min && above) atomicAdd(&S.above, above);
         const Sum before = block_before<kThreads>(S.ask.scan, turn, own, &of_k);
+        if (H.first_k) of_k.count = H.first_k;  // with those that weigh nothing
         auto ask = [&](int slot, bool mass, uint64_t need) {
             Sum run = before;
 #pragma unroll
@@ -825,10 +853,10 @@ __device__ __forceinline__ void draw_from_cands(Sorter& S, int& turn, const Row<
     of_k = B.total;
     if (H.k_bin >= 0) {
         of_k = ask(0, false, kk).upto;
-    } else if (kk < B.total.count) {  // the end of a bin
+    } else if (kk < B.total.count) {  // the end of a bin, or among zeros
         ask_bins(S.ask, B, 0, false, kk);
         __syncthreads();
-        of_k = S.ask.hit[0].upto;
+        of_k = {S.ask.hit[0].upto.mass, kk};
     }
     kept = of_k;
     if (R.has_min && H.above_count < kept.count) kept = {H.above_mass, H.above_count};
@@ -987,7 +1015,7 @@ template <int T, bool CAP>
 __device__ __forceinline__ void collect(const Batch& first, const DrawView& D, const Row<CAP>& R, const Head& H, int64_t lo,
                                         int64_t hi, uint64_t* keys, uint32_t* n) {
     // four at a time are dropped, most of them (NaN is not above anything)
-    const float least = R.floor_of(max(H.u_hi, max(H.p_hi, H.k_bin)));
+    const float least = R.least_of(H);
     for_quads<T, false>(first, R.y, lo, hi, D.vec, [&](const float (&v)[4], int64_t i) {
         if (!(max4(v) >= least)) return;
 #pragma unroll
@@ -1025,7 +1053,7 @@ template <int T, bool CAP>
 __device__ __forceinline__ void collect_runs(const DrawView& D, const Row<CAP>& R, const Head& H, const float* run, int64_t lo,
                                              int64_t hi, int32_t* list, uint32_t* listed, uint64_t* keys, uint32_t* n) {
     const int last = max(H.u_hi, max(H.p_hi, H.k_bin));
-    const float least = R.floor_of(last);  // drops most (and NaN) by one comparison
+    const float least = R.least_of(H);  // drops most (and NaN) by one comparison
     const int t = threadIdx.x;
     const int64_t r0 = lo / kRun, r1 = (hi + kRun - 1) / kRun;
     for (int64_t r = r0; r < r1; r += 4 * T) {
@@ -1319,6 +1347,7 @@ void draw_bins_kernel(DrawView D) {
             D.head[m].k_bin = H.k_bin;
             D.head[m].p_hi = H.p_hi;
             D.head[m].u_hi = H.u_hi;
+            D.head[m].first_k = H.first_k;
         }
         return;
     }
@@ -1367,16 +1396,19 @@ void draw_collect_kernel(DrawView D) {
     const Args A = args_of(D, m);
     if (!(A.temperature > 0.0f)) return;
     if (t == 0) n = listed = 0;
+    if constexpr (CAP) fill_exp_table();
     p = join(p);
-    const Row<CAP> R = row_of<CAP>(D, m, A, p.best, p.sum, p.count);
+    Row<CAP> R = row_of<CAP>(D, m, A, p.best, p.sum, p.count);
     if (R.mode == kFirst) return;
     const float* run = D.run + m * D.runs;
     if (R.mode == kByRuns) {
         __syncthreads();
+        R.level_of_top();
         collect_runs<kBinThreads>(D, R, H, run, lo, hi, list, &listed, keys, &n);
     } else {
         int turn = 0;
-        sum_bins(ask, turn, B);
+        sum_bins(ask, turn, B);  // a barrier
+        R.level_of_top();
         uint32_t reach;
         H = choose_bins(ask, R, B, {H.above_mass, H.above_count}, &reach);
         if (lo == 0 && t == 0) {
@@ -1385,6 +1417,7 @@ void draw_collect_kernel(DrawView D) {
             head->p_hi = H.p_hi;
             head->u_lo = H.u_lo;
             head->u_hi = H.u_hi;
+            head->first_k = H.first_k;
         }
         if (few_runs(D, reach, hi - lo))
             collect_runs<kBinThreads>(D, R, H, run, lo, hi, list, &listed, keys, &n);
