@@ -419,7 +419,7 @@ void lora_expand_kernel(LoraView D) {
     const Tile t = tile_of(D, blockIdx.x);
     if (t.rows == 0) return;
     const int64_t lo = static_cast<int64_t>(blockIdx.y) * D.n_share, hi = min(lo + D.n_share, D.l.N);
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1), i = lane & 15, g = lane >> 4;
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
     const int rank = rank_of(D, t);
     if (rank == 0) {
         if (D.a.base == D.a.y) return;

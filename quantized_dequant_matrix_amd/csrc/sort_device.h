@@ -84,13 +84,12 @@ __device__ __forceinline__ void wave_sort_desc(uint64_t (&key)[NK]) {
     }
 }
 
-// Sorts NB * 1024 keys held by a 1024-thread workgroup, largest first:
-// key[j] of thread t is element j * 1024 + t.  Steps with distance < 64 are
-// shuffles inside a wave, steps with distance >= 1024 stay in registers, the
+// Sorts NB * T keys held by a workgroup of T threads (a power of two), largest
+// first: key[j] of thread t is element j * T + t.  Steps with distance < 64 are
+// shuffles inside a wave, steps with distance >= T stay in registers, the
 // rest exchange through LDS (two buffers alternate, so one barrier a step).
-template <int NB>
-__device__ __forceinline__ void block_sort_desc(uint64_t (&key)[NB], uint64_t* lds /* 2 * NB * 1024 */) {
-    constexpr int T = 1024;
+template <int T, int NB>
+__device__ __forceinline__ void block_sort_desc(uint64_t (&key)[NB], uint64_t* lds /* 2 * NB * T */) {
     constexpr int n = T * NB;
     const int t = threadIdx.x;
     int buf = 0;

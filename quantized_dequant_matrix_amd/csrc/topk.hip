@@ -284,7 +284,7 @@ void topk_select_kernel(const float* __restrict__ y, int64_t N, int k, int nlist
 
     // 1. sort the heads; T = the k-th largest (0 if fewer than k lists)
     uint64_t h[1] = {t < nlists ? cm[static_cast<int64_t>(t) * k] : 0ull};
-    block_sort_desc<1>(h, lds);
+    block_sort_desc<kMergeThreads>(h, lds);
     if (t == k - 1) sh_T = h[0];
     __syncthreads();
     const uint64_t T = sh_T;
@@ -356,7 +356,7 @@ void topk_select_kernel(const float* __restrict__ y, int64_t N, int k, int nlist
         for (int j = 0; j < kMaxCand / kMergeThreads; ++j)
             key[j] = (j * kMergeThreads + t < C) ? cbuf[j * kMergeThreads + t] : 0ull;
         __syncthreads();  // the candidates are in registers: the buffers are free
-        block_sort_desc(key, lds);
+        block_sort_desc<kMergeThreads>(key, lds);
         best = key[0];
     }
     if (t < kWave) {  // wave 0; k <= 64
