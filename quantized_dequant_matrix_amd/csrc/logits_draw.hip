@@ -1396,7 +1396,7 @@ void draw_collect_kernel(DrawView D) {
     const Args A = args_of(D, m);
     if (!(A.temperature > 0.0f)) return;
     if (t == 0) n = listed = 0;
-    if constexpr (CAP) fill_exp_table();
+    if (CAP && A.top_k > 0 && A.top_k <= kMostCounted) fill_exp_table();  // least_weighing() asks for the level
     p = join(p);
     Row<CAP> R = row_of<CAP>(D, m, A, p.best, p.sum, p.count);
     if (R.mode == kFirst) return;
@@ -1408,7 +1408,7 @@ void draw_collect_kernel(DrawView D) {
     } else {
         int turn = 0;
         sum_bins(ask, turn, B);  // a barrier
-        R.level_of_top();
+        if (R.mode == kCounted) R.level_of_top();
         uint32_t reach;
         H = choose_bins(ask, R, B, {H.above_mass, H.above_count}, &reach);
         if (lo == 0 && t == 0) {
