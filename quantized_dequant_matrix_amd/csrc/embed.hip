@@ -2,9 +2,11 @@
 //
 // One thread forms four neighbouring elements: a few bytes of codes in, 16
 // bytes out.  The output is 4 bytes an element against 0.56-1.06 of codes, so
-// stores bound it: 8192 rows of 5376 from Q4_K (201 MB) take 34 us, 5.9 TB/s; one
-// row is a launch (2.3 us of kernel in a call of 5).  They go past the L2 and are whole cache lines a wave; the
-// codes' narrow loads (a Q8_0 or Q4_0 block is 2-byte aligned) stay in the L1.
+// stores bound it: 8192 rows of 5376 from Q4_K (201 MB) take 34 us, 5.9 TB/s, from
+// Q8_0, Q4_0 and Q6_K (223, 201, 212 MB) 34, 32 and 32; one row is a launch (2.3 us
+// of kernel in a call of 5).  They go past the L2 and are whole cache lines a wave
+// (a y that is not 16-byte aligned: 43-44 us); the codes' narrow loads (a Q8_0 or
+// Q4_0 block is 2-byte aligned) stay in the L1.
 //
 // A weight's products are exact in float32: a float16 scale has 11 bits, codes
 // and sub-scales add at most 13.  Only Q4_K's difference is rounded.

@@ -17,8 +17,13 @@
 // Bounds, and what was measured: chunks are bound by HBM (1611 rows, 5376 ->
 // 21504, rank 16: 308 MB in 67 us, 4.6 TB/s); single rows with many adapters by
 // the lines of Bm (a row of Bm of max_rank 64 is a 128-byte line, read whole
-// whatever the adapter's own rank: 32 rows over 24 adapters 24 us, 4.9 TB/s
-// of lines in expand); one row by its two launches (7.9 us).
+// whatever the adapter's own rank: 28 rows over 18 adapters 24 us, of which
+// expand takes 15 and reads 75 MB by the counters of HBM, 50 of lines of Bm and
+// again what rows of one adapter on different dies do not share); one row by its
+// two launches (7.9 us).  Two to eight rows of each of those sequences take 31-40
+// us: lines of 75-100 MB at 2.7-3.6 TB/s, by tiles of 16 rows.  Rows of y that are
+// not 16-byte aligned are stored by 4 bytes: chunks of 1600 rows take 126 us then,
+// not 66.
 //
 // The operands' k index is a dummy: lane (i, g) = (l % 16, l / 16) holds
 // eight neighbouring elements of its row (four of ranks up to 16), and

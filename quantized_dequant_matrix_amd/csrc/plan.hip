@@ -317,7 +317,10 @@ hipError_t launch_kv_plan(const qmv_kv_pool& pool, const PlanArgs& a, void* ws, 
     // One workgroup goes through 1024 rows or pages at a time, a few
     // microseconds each, which a second launch costs once: 32 sequences with 100
     // rows take 7.1 us here and 9.4 there, with 5000 rows 11.7 and 9.7, 256
-    // sequences of which some end and give back 12,000 pages 12.8 and 10.6.
+    // sequences of which some end and give back 12,000 pages 12.8 and 10.6.  How
+    // many pages move is known on the device only, and a step that moves most of
+    // its cache is here all the same: 8192 pages 7.0 and 9.1, 16,384 12.2 and 9.0,
+    // 64 sequences of 1024 pages that end at once 43 and 9.2.
     if (pool.B <= kMostSmall && a.T <= 2048) {
         hipLaunchKernelGGL(plan_small_kernel, dim3(1), dim3(kPlanThreads), 0, stream, D);
         return hipGetLastError();
